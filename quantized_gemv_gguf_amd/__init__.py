@@ -15,10 +15,12 @@ from dataclasses import dataclass
 from typing import Sequence
 
 Q8_0, Q4_0, MXFP4, Q4_K, Q6_K = 1, 2, 3, 4, 5
+F32, F16, BF16 = 32, 33, 34  # float element types of a qg_tensor (qgemv_mx.h)
 FORMATS = {"q8_0": Q8_0, "q4_0": Q4_0, "mxfp4": MXFP4, "q4_k": Q4_K, "q6_k": Q6_K}
 MAX_WINDOWS = 64
 MAX_K = 49152
 CHAIN_MAX_K = 24576
+MAX_EXPERTS = 1024
 IN_X, IN_RMS, IN_GELU_RMS, IN_SILU_MUL = 0, 1, 2, 3
 OUT_Y, OUT_GELU = 0, 1
 
@@ -67,6 +69,11 @@ class qg_chain_window(ctypes.Structure):
 
 class qg_chain_step(ctypes.Structure):
     _fields_ = [("k", _i64), ("first_win", _i32), ("n_win", _i32), ("in_op", _i32), ("eps", ctypes.c_float)]
+
+
+class qg_tensor(ctypes.Structure):
+    _fields_ = [("data", _vp), ("type", _i32), ("reserved", _i32), ("n_rows", _i64), ("n_cols", _i64),
+                ("stride", _i64)]
 
 
 _lib = None
@@ -125,6 +132,19 @@ def lib():
         "qgemv_chain_set_spin_limit": ([_vp, ctypes.c_uint32], ctypes.c_int),
         "qgemv_chain_grid": ([_vp], _i64),
         "qgemv_chain_destroy": ([_vp], ctypes.c_int),
+        "qgemv_mx_quantize": ([P(qg_tensor), P(qg_matrix), _vp], ctypes.c_int),
+        "qgemv_mx_dequantize": ([P(qg_matrix), _i64, _i64, P(qg_tensor), _vp], ctypes.c_int),
+        "qgemv_rows_mx": ([P(qg_matrix), _i64, _i64, P(qg_tensor), P(qg_tensor), _vp], ctypes.c_int),
+        "qgemv_rows_mx_swiglu": ([P(qg_matrix), P(qg_matrix), _i64, _i64, P(qg_tensor), P(qg_tensor), _vp],
+                                 ctypes.c_int),
+        "qgemv_expert_sort": ([_vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp], ctypes.c_int),
+        "qgemv_expert_mx": ([P(qg_matrix), _i64, P(qg_tensor), _vp, _vp, _i32, P(qg_tensor), _vp], ctypes.c_int),
+        "qgemv_expert_mx_swiglu": ([P(qg_matrix), P(qg_matrix), _i64, P(qg_tensor), _vp, _vp, _i32, P(qg_tensor),
+                                    _vp], ctypes.c_int),
+        "qgemv_expert_gather": ([P(qg_tensor), _vp, _i32, P(qg_tensor), _vp], ctypes.c_int),
+        "qgemv_expert_combine": ([P(qg_tensor), _vp, _vp, _i32, P(qg_tensor), _vp], ctypes.c_int),
+        "qgemv_expert_combine_grad": ([P(qg_tensor), P(qg_tensor), _vp, _vp, _i32, P(qg_tensor), _vp, _vp],
+                                      ctypes.c_int),
         "qgemv_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "qgemv_last_hip_error": ([], ctypes.c_char_p),
         "qgemv_version": ([], ctypes.c_char_p),
@@ -632,6 +652,155 @@ class Chain:
 
 def qgemv_chain_create(fmt: int, steps: Sequence[ChainStep]) -> Chain:
     return Chain(fmt, steps)
+
+
+# --- prompts over MXFP4 weights (include/qgemv_mx.h) -------------------------------
+#
+# Activations are 2-D device tensors of float32, float16 or bfloat16 with unit
+# column stride (any row stride), or MXFP4 blocks as a Matrix.  Every tensor of
+# a call must lie on the current device.
+
+def _here(t, name: str):
+    """The tensor's address, checked to be on the current device."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _rows(t, name: str) -> qg_tensor:
+    """A qg_tensor of a 2-D float tensor, or of a Matrix of blocks."""
+    import torch
+    if isinstance(t, Matrix):
+        _blocks(t, name)
+        return qg_tensor(t.data.data_ptr(), int(t.fmt), 0, int(t.n_rows), int(t.k), int(t.k))
+    kind = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    # (the stride of a single row says nothing)
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return qg_tensor(_here(t, name), kind, 0, int(t.shape[0]), int(t.shape[1]), int(stride))
+
+
+def _blocks(m: Matrix, name: str) -> qg_matrix:
+    """A qg_matrix whose blocks are on the current device and all there."""
+    _here(m.data, name)
+    c = m.c()
+    if m.fmt == MXFP4 and m.k > 0 and m.k % 32 == 0 and c.n_bytes < m.n_rows * (m.k // 32 * 17):
+        raise ValueError(f"{name} holds {c.n_bytes} bytes, needs {m.n_rows * (m.k // 32 * 17)}")
+    return c
+
+
+def _i32s(t, n: int, name: str) -> int:
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} values, needs {n}")
+    _here(t, name)
+    return _ptr(t)
+
+
+def _weights(w, n: int, name: str) -> int:
+    _here(w, name)
+    return _f32(w, n, name)
+
+
+def qgemv_mx_quantize(x, q: Matrix, stream=None) -> None:
+    """Quantises the rows of ``x`` into the MXFP4 blocks of ``q`` (n_rows x k of x's shape)."""
+    _check(lib().qgemv_mx_quantize(ctypes.byref(_rows(x, "x")), ctypes.byref(_blocks(q, "q")), _stream(stream)),
+           "qgemv_mx_quantize")
+
+
+def qgemv_mx_dequantize(q: Matrix, row_start: int, row_end: int, out, stream=None) -> None:
+    """The values of rows [row_start, row_end) of ``q``, rounded to out's type."""
+    _check(lib().qgemv_mx_dequantize(ctypes.byref(_blocks(q, "q")), row_start, row_end,
+                                     ctypes.byref(_rows(out, "out")), _stream(stream)), "qgemv_mx_dequantize")
+
+
+def qgemv_rows_mx(w: Matrix, row_start: int, row_end: int, x, y, stream=None) -> None:
+    """y[t] = W[row_start:row_end] . x[t] for any number of tokens; ``x`` a float
+    tensor (tokens, k) or an MXFP4 Matrix, ``y`` (tokens, rows) of any float type."""
+    _check(lib().qgemv_rows_mx(ctypes.byref(_blocks(w, "w")), row_start, row_end, ctypes.byref(_rows(x, "x")),
+                               ctypes.byref(_rows(y, "y")), _stream(stream)), "qgemv_rows_mx")
+
+
+def qgemv_rows_mx_swiglu(gate: Matrix, up: Matrix, row_start: int, row_end: int, x, h, stream=None) -> None:
+    """h = silu(gate[rows] . x) * (up[rows] . x), as qgemv_rows_mx."""
+    _check(lib().qgemv_rows_mx_swiglu(ctypes.byref(_blocks(gate, "gate")), ctypes.byref(_blocks(up, "up")), row_start,
+                                      row_end, ctypes.byref(_rows(x, "x")), ctypes.byref(_rows(h, "h")),
+                                      _stream(stream)), "qgemv_rows_mx_swiglu")
+
+
+def qgemv_expert_sort(ids, n_expert: int, offsets, slots, pos, stream=None) -> None:
+    """Stable sort of the slots of ``ids`` (tokens, choices; int32) by expert:
+    ``offsets`` (n_expert + 1), ``slots`` and ``pos`` (one per slot), int32."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be (tokens, choices)")
+    n_tok, n_sel = ids.shape
+    n = n_tok * n_sel
+    _check(lib().qgemv_expert_sort(_i32s(ids, n, "ids"), n_tok, n_sel, int(n_expert),
+                                   _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"), _i32s(slots, n, "slots"),
+                                   _i32s(pos, n, "pos"), _stream(stream)), "qgemv_expert_sort")
+
+
+def _expert_args(x, n_expert: int, offsets, y, slots, n_sel: int):
+    yt = _rows(y, "y")
+    return (ctypes.byref(_rows(x, "x")), _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"),
+            _i32s(slots, yt.n_rows, "slots") if slots is not None else None, int(n_sel), ctypes.byref(yt))
+
+
+def qgemv_expert_mx(w: Matrix, n_expert: int, x, offsets, y, slots=None, n_sel: int = 1, stream=None) -> None:
+    """y[p] = W_e . x[src] for the sorted places p of every expert e; src =
+    slots[p] // n_sel, or p without ``slots``.  Rows of y behind the last place stay."""
+    xt, op, sp, ns, yt = _expert_args(x, n_expert, offsets, y, slots, n_sel)
+    _check(lib().qgemv_expert_mx(ctypes.byref(_blocks(w, "w")), int(n_expert), xt, op, sp, ns, yt, _stream(stream)),
+           "qgemv_expert_mx")
+
+
+def qgemv_expert_mx_swiglu(gate: Matrix, up: Matrix, n_expert: int, x, offsets, h, slots=None, n_sel: int = 1,
+                           stream=None) -> None:
+    """h[p] = silu(gate_e . x[src]) * (up_e . x[src]), as qgemv_expert_mx."""
+    xt, op, sp, ns, ht = _expert_args(x, n_expert, offsets, h, slots, n_sel)
+    _check(lib().qgemv_expert_mx_swiglu(ctypes.byref(_blocks(gate, "gate")), ctypes.byref(_blocks(up, "up")),
+                                        int(n_expert), xt, op, sp, ns, ht, _stream(stream)),
+           "qgemv_expert_mx_swiglu")
+
+
+def qgemv_expert_gather(x, slots, n_sel: int, out, stream=None) -> None:
+    """out[p] = x[slots[p] // n_sel]; rows with a negative slot stay."""
+    ot = _rows(out, "out")
+    _check(lib().qgemv_expert_gather(ctypes.byref(_rows(x, "x")), _i32s(slots, ot.n_rows, "slots"), int(n_sel),
+                                     ctypes.byref(ot), _stream(stream)), "qgemv_expert_gather")
+
+
+def qgemv_expert_combine(y, pos, out, w=None, stream=None) -> None:
+    """out[t] = sum_s w[t, s] y[pos[t, s]]; without ``w`` the weights are 1 (the
+    gather's gradient).  ``pos`` and ``w`` are (tokens, choices)."""
+    if pos.dim() != 2 or pos.shape[0] != out.shape[0]:
+        raise ValueError("pos must be (tokens, choices) with out's tokens")
+    n = pos.numel()
+    _check(lib().qgemv_expert_combine(ctypes.byref(_rows(y, "y")), _i32s(pos, n, "pos"),
+                                      _weights(w, n, "w") if w is not None else None, pos.shape[1],
+                                      ctypes.byref(_rows(out, "out")), _stream(stream)), "qgemv_expert_combine")
+
+
+def qgemv_expert_combine_grad(dout, y, pos, w, dy, dw, stream=None) -> None:
+    """The gradient of qgemv_expert_combine: dy[pos[t, s]] = w[t, s] dout[t],
+    dw[t, s] = <dout[t], y[pos[t, s]]> (float32)."""
+    if pos.dim() != 2 or pos.shape[0] != dout.shape[0]:
+        raise ValueError("pos must be (tokens, choices) with dout's tokens")
+    n = pos.numel()
+    _check(lib().qgemv_expert_combine_grad(ctypes.byref(_rows(dout, "dout")), ctypes.byref(_rows(y, "y")),
+                                           _i32s(pos, n, "pos"), _weights(w, n, "w"), pos.shape[1],
+                                           ctypes.byref(_rows(dy, "dy")), _weights(dw, n, "dw"), _stream(stream)),
+           "qgemv_expert_combine_grad")
 
 
 def qgemv_version() -> str:

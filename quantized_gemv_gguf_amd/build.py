@@ -18,6 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 # compiled in parallel and linked into one library.
 SOURCES = ["qgemv.hip"] + [f"gemv_op{i}.hip" for i in range(7)] + ["gemv_batch.hip", "gemv_mfma.hip"]
 HEADERS = ["qgemv_impl.h"]
+# mx.hip: the C ABI of qgemv_mx.h, quantisation and routing; the products of one
+# activation type each.
+MX_SOURCES = ["mx.hip", "mx_f32.hip", "mx_f16.hip", "mx_bf16.hip", "mx_fp4.hip"]
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqgemv.so")
 ARCH = "gfx950"
@@ -43,7 +46,7 @@ def hipcc() -> str:
 
 
 def source_paths():
-    """Every file the kernels are built from (hashed by bench.py to tie HBM
+    """Every file the GEMV kernels are built from (hashed by bench.py to tie HBM
     counter summaries to the code they were taken on)."""
     return [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
 
@@ -53,7 +56,7 @@ def build(verbose: bool = False) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     procs = []
-    for s in SOURCES:
+    for s in SOURCES + MX_SOURCES:
         obj = os.path.join(objdir, s.replace(".hip", ".o"))
         log = obj + ".log"
         cmd = [hipcc(), *HIPCC_FLAGS, f"-I{INC}", "-c", os.path.join(CSRC, s), "-o", obj]

@@ -1,0 +1,615 @@
+// mx.hip -- the C ABI of include/qgemv_mx.h, with quantisation to MXFP4 and the
+// routing kernels (sort by expert, gather, weighted sum back, its gradient).
+// The products' kernels are in mx_gemm.h.
+#include "mx_gemm.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace qgemv_detail {
+int record_hip_error(hipError_t e, const char *what);  // qgemv.hip: for qgemv_last_hip_error
+}
+
+using namespace qgemv_mx;
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Element types
+// ---------------------------------------------------------------------------
+
+template <int T> struct Elem;
+template <> struct Elem<QG_F32> {
+  typedef float Raw;
+  static constexpr int kSize = 4;
+  __device__ static inline float to(Raw v) { return v; }
+  __device__ static inline Raw from(float v) { return v; }
+};
+template <> struct Elem<QG_F16> {
+  typedef _Float16 Raw;
+  static constexpr int kSize = 2;
+  __device__ static inline float to(Raw v) { return (float)v; }
+  __device__ static inline Raw from(float v) { return (_Float16)v; }
+};
+template <> struct Elem<QG_BF16> {
+  typedef __bf16 Raw;
+  static constexpr int kSize = 2;
+  __device__ static inline float to(Raw v) { return (float)v; }
+  __device__ static inline Raw from(float v) { return (__bf16)v; }
+};
+
+// N values from / to any element-aligned address, as one access of N elements.
+template <int T, int N>
+__device__ __forceinline__ void load_n(const void *p, float (&v)[N]) {
+  typedef typename Elem<T>::Raw V __attribute__((ext_vector_type(N)));
+  V r;
+  __builtin_memcpy(&r, p, N * Elem<T>::kSize);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = Elem<T>::to(r[i]);
+}
+template <int T, int N>
+__device__ __forceinline__ void store_n(void *p, const float (&v)[N]) {
+  typedef typename Elem<T>::Raw V __attribute__((ext_vector_type(N)));
+  V r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = Elem<T>::from(v[i]);
+  __builtin_memcpy(p, &r, N * Elem<T>::kSize);
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation.  Four lanes per block of 32: lane q holds elements 4q + b and
+// 16 + 4q + b (b < 4), which are word q of the block's codes.
+// ---------------------------------------------------------------------------
+
+constexpr int kQBlocks = 256;  // blocks per workgroup: 4352 bytes, 272 granules
+
+template <int T>
+__global__ void __launch_bounds__(256) quantize_kernel(const uint8_t *x, int64_t stride, int nb, int64_t blocks,
+                                                       uint8_t *out) {
+  __shared__ __attribute__((aligned(16))) uint8_t buf[kQBlocks * 17];
+  constexpr int ES = Elem<T>::kSize;
+  const int tid = threadIdx.x, q = tid & 3;
+  const int64_t first = (int64_t)blockIdx.x * kQBlocks;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int bl = 64 * v + (tid >> 2);
+    const int64_t b = first + bl;
+    if (b < blocks) {
+      const int64_t r = b / nb;
+      const uint8_t *p = x + (r * stride + 32 * (b - r * nb) + 4 * q) * ES;
+      float lo[4], hi[4];
+      load_n<T>(p, lo);
+      load_n<T>(p + 16 * ES, hi);
+      // the largest magnitude as bits: their order is the magnitudes' order,
+      // infinities and NaN above every finite one
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        m = max(m, __float_as_uint(lo[e]) & 0x7fffffffu);
+        m = max(m, __float_as_uint(hi[e]) & 0x7fffffffu);
+      }
+      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+      // floor(log2 a) - 2 + 127 is the exponent field less 2 for a normal a,
+      // and below 0 for a subnormal one
+      const int field = (int)(m >> 23);
+      const bool fine = field < 255;
+      const int e = fine ? max(field - 2, 0) : 255;
+      const float scale = __uint_as_float((uint32_t)e << 23);
+      uint32_t c = 0;
+      if (fine) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, lo[0], hi[0], scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, lo[1], hi[1], scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, lo[2], hi[2], scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, lo[3], hi[3], scale, 3);
+      }
+      uint8_t *o = buf + 17 * bl;
+      if (q == 0) o[0] = (uint8_t)e;
+      __builtin_memcpy(o + 1 + 4 * q, &c, 4);
+    }
+  }
+  __syncthreads();
+  const int64_t left = min((int64_t)kQBlocks, blocks - first) * 17;  // bytes
+  uint8_t *dst = out + first * 17;                                   // 16-byte aligned: 4352 = 16 * 272
+  for (int o = 16 * tid; o < left; o += 4096) {
+    if (o + 16 <= left) *(u32x4 *)(dst + o) = *(const u32x4 *)(buf + o);
+    else
+      for (int k = o; k < left; ++k) dst[k] = buf[k];
+  }
+}
+
+template <int T>
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *w, int nb, int64_t blocks, uint8_t *out,
+                                                         int64_t stride) {
+  constexpr int ES = Elem<T>::kSize;
+  const int q = threadIdx.x & 3;
+  const int64_t b = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
+  if (b >= blocks) return;
+  const uint8_t *p = w + b * 17;
+  uint32_t c;
+  __builtin_memcpy(&c, p + 1 + 4 * q, 4);
+  const float s = __uint_as_float((uint32_t)p[0] << 23);
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+  const f2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+  const float lo[4] = {v0.x, v1.x, v2.x, v3.x}, hi[4] = {v0.y, v1.y, v2.y, v3.y};
+  const int64_t r = b / nb;
+  uint8_t *o = out + (r * stride + 32 * (b - r * nb) + 4 * q) * ES;
+  store_n<T>(o, lo);
+  store_n<T>(o + 16 * ES, hi);
+}
+
+// ---------------------------------------------------------------------------
+// Routing
+// ---------------------------------------------------------------------------
+
+// Workgroup e < n_expert places the slots of expert e: its first pass counts
+// the ids below e (the expert's offset) and equal to e per wave, its second
+// writes each slot's place, in slot order (a lane's four ids, then the lanes,
+// then the waves).  Workgroup n_expert does the same for the dropped slots:
+// pos -1, and slots -1 behind the last kept one.  No atomics, no workspace,
+// one launch; every workgroup reads all ids from L2.
+constexpr int kSortWaves = 16;
+__global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(const int32_t *ids, int n, int n_expert,
+                                                               int32_t *offsets, int32_t *slots, int32_t *pos) {
+  __shared__ int below[kSortWaves], equal[kSortWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.x;
+  const bool rest = e == n_expert;
+  // whole groups of 256 ids per wave
+  const int groups = (n + 255) / 256, per = (groups + kSortWaves - 1) / kSortWaves;
+  const int g0 = min(wave * per, groups), g1 = min(g0 + per, groups);
+  auto load4 = [&](int g, int (&v)[4]) {
+    const int at = 256 * g + 4 * lane;
+    if (at + 4 <= n) {
+      __builtin_memcpy(v, ids + at, 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = at + k < n ? ids[at + k] : 0x7fffffff;
+    }
+  };
+  auto mine = [&](int id) { return rest ? (id < 0 || id >= n_expert) : id == e; };
+  int nb = 0, ne = 0;
+  for (int g = g0; g < g1; ++g) {
+    int v[4];
+    load4(g, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      nb += __popcll(__ballot(v[k] >= 0 && v[k] < e));
+      ne += __popcll(__ballot(mine(v[k])));
+    }
+  }
+  if (lane == 0) {
+    below[wave] = nb;
+    equal[wave] = ne;
+  }
+  __syncthreads();
+  int base = 0, before = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    base += below[w];
+    if (w < wave) before += equal[w];
+  }
+  if (threadIdx.x == 0) offsets[e] = base;
+  if (rest) {
+    for (int p = base + threadIdx.x; p < n; p += 64 * kSortWaves) slots[p] = -1;
+  }
+  int at = base + before;
+  const uint64_t lower = (1ull << lane) - 1;
+  for (int g = g0; g < g1; ++g) {
+    int v[4];
+    load4(g, v);
+    int rank = 0, all = 0;
+    bool m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      m[k] = mine(v[k]) && 256 * g + 4 * lane + k < n;
+      const uint64_t b = __ballot(m[k]);
+      rank += __popcll(b & lower);
+      all += __popcll(b);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!m[k]) continue;
+      const int slot = 256 * g + 4 * lane + k;
+      if (rest) {
+        pos[slot] = -1;
+      } else {
+        slots[at + rank] = slot;
+        pos[slot] = at + rank;
+        ++rank;
+      }
+    }
+    at += all;
+  }
+}
+
+// A wave copies one row at a time, 16 bytes per lane, then the row's last bytes
+// by elements of 2.
+__global__ void __launch_bounds__(256) gather_kernel(const uint8_t *x, int64_t x_bytes, int64_t x_rows, int64_t row,
+                                                     const int32_t *slots, int n_sel, int64_t n, uint8_t *out,
+                                                     int64_t out_bytes) {
+  const int lane = threadIdx.x & 63;
+  const int64_t waves = (int64_t)gridDim.x * 4;
+  for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < n; p += waves) {
+    const int s = slots[p];
+    if (s < 0 || s / n_sel >= x_rows) continue;
+    const uint8_t *src = x + (int64_t)(s / n_sel) * x_bytes;
+    uint8_t *dst = out + p * out_bytes;
+    const int64_t whole = row & ~15ll;
+    for (int64_t o = 16 * lane; o < whole; o += 1024) {
+      u32x4 v;
+      __builtin_memcpy(&v, src + o, 16);
+      __builtin_memcpy(dst + o, &v, 16);
+    }
+    for (int64_t o = whole + 2 * lane; o < row; o += 128) {
+      uint16_t v;
+      __builtin_memcpy(&v, src + o, 2);
+      __builtin_memcpy(dst + o, &v, 2);
+    }
+  }
+}
+
+// Columns of one token, kCols at a time per lane: the places' rows are added
+// one after the other in s order.
+constexpr int kCols = 8;
+template <int TY, int TO>
+__global__ void __launch_bounds__(256) combine_kernel(const uint8_t *y, int64_t y_stride, int64_t y_rows,
+                                                      const int32_t *pos, const float *w, int n_sel, int64_t n_cols,
+                                                      uint8_t *out, int64_t out_stride) {
+  constexpr int EY = Elem<TY>::kSize, EO = Elem<TO>::kSize;
+  const int64_t t = blockIdx.x;
+  pos += t * n_sel;
+  const int64_t groups = (n_cols + kCols - 1) / kCols;
+  for (int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x; c < groups; c += (int64_t)gridDim.y * 256) {
+    const int64_t col = kCols * c;
+    float acc[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+    const bool whole = col + kCols <= n_cols;
+    for (int s = 0; s < n_sel; ++s) {
+      const int64_t p = pos[s];
+      if (p < 0 || p >= y_rows) continue;
+      const float ws = w ? w[t * n_sel + s] : 1.0f;
+      const uint8_t *src = y + (p * y_stride + col) * EY;
+      float v[kCols];
+      if (whole) load_n<TY>(src, v);
+      else
+        for (int k = 0; k < kCols; ++k) {
+          float o[1] = {0.0f};
+          if (col + k < n_cols) load_n<TY>(src + k * EY, o);
+          v[k] = o[0];
+        }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) acc[k] = fmaf(ws, v[k], acc[k]);
+    }
+    uint8_t *dst = out + (t * out_stride + col) * EO;
+    if (whole) store_n<TO>(dst, acc);
+    else
+      for (int k = 0; k < kCols; ++k) {
+        const float o[1] = {acc[k]};
+        if (col + k < n_cols) store_n<TO>(dst + k * EO, o);
+      }
+  }
+}
+
+// One workgroup per (token, choice): dy's row and the dot product, summed by
+// lane, then over the lanes, then over the waves.
+template <int TD, int TY>
+__global__ void __launch_bounds__(256) combine_grad_kernel(const uint8_t *dout, int64_t d_stride, const uint8_t *y,
+                                                           int64_t y_stride, int64_t y_rows, const int32_t *pos,
+                                                           const float *w, int n_sel, int64_t n_cols, uint8_t *dy,
+                                                           int64_t dy_stride, float *dw) {
+  constexpr int ED = Elem<TD>::kSize, EY = Elem<TY>::kSize;
+  __shared__ float part[4];
+  const int64_t slot = blockIdx.x;
+  const int64_t t = slot / n_sel;
+  const int64_t p = pos[slot];
+  if (p < 0 || p >= y_rows) {
+    if (threadIdx.x == 0) dw[slot] = 0.0f;
+    return;
+  }
+  const float ws = w[slot];
+  float sum = 0.0f;
+  const int64_t groups = (n_cols + kCols - 1) / kCols;
+  for (int64_t c = threadIdx.x; c < groups; c += 256) {
+    const int64_t col = kCols * c;
+    const uint8_t *d = dout + (t * d_stride + col) * ED;
+    const uint8_t *src = y + (p * y_stride + col) * EY;
+    uint8_t *dst = dy + (p * dy_stride + col) * EY;
+    if (col + kCols <= n_cols) {
+      float a[kCols], b[kCols], o[kCols];
+      load_n<TD>(d, a);
+      load_n<TY>(src, b);
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
+        sum = fmaf(a[k], b[k], sum);
+        o[k] = ws * a[k];
+      }
+      store_n<TY>(dst, o);
+    } else {
+      for (int k = 0; col + k < n_cols; ++k) {
+        float a[1], b[1];
+        load_n<TD>(d + k * ED, a);
+        load_n<TY>(src + k * EY, b);
+        sum = fmaf(a[0], b[0], sum);
+        const float o[1] = {ws * a[0]};
+        store_n<TY>(dst + k * EY, o);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) dw[slot] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Checks
+// ---------------------------------------------------------------------------
+
+#define MX_HIP(call)                                                       \
+  do {                                                                     \
+    hipError_t e_ = (call);                                                \
+    if (e_ != hipSuccess) return qgemv_detail::record_hip_error(e_, #call); \
+  } while (0)
+
+constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxStride = 1ll << 40;
+
+int elem_size(int32_t type) { return type == QG_F32 ? 4 : type == QG_F16 || type == QG_BF16 ? 2 : 0; }
+
+// An MXFP4 matrix of at most kMaxDim rows.
+int check_mx(const qg_matrix *w) {
+  if (!w) return QG_E_NULL;
+  if (w->fmt != QG_MXFP4) return QG_E_FMT;
+  if (w->k <= 0 || w->k % 32 != 0 || w->k > QG_MAX_K || w->n_rows < 0 || w->n_rows > kMaxDim) return QG_E_SHAPE;
+  if (w->reserved != 0) return QG_E_ARG;
+  if (w->n_bytes != w->n_rows * (w->k / 32 * 17)) return QG_E_SIZE;
+  if (!w->data && w->n_bytes > 0) return QG_E_NULL;
+  if ((uintptr_t)w->data & 15) return QG_E_ARG;
+  return QG_OK;
+}
+
+// blocks: MXFP4 is taken too.  out: rows may not overlap.
+int check_tensor(const qg_tensor *t, bool blocks, bool out) {
+  if (!t) return QG_E_NULL;
+  const int es = elem_size(t->type);
+  if (!es && !(blocks && t->type == QG_MXFP4)) return QG_E_FMT;
+  if (t->n_rows < 0 || t->n_cols < 0 || t->n_rows > kMaxDim || t->n_cols > kMaxDim) return QG_E_SHAPE;
+  if (!es && t->n_cols % 32 != 0) return QG_E_SHAPE;
+  if (t->reserved != 0 || t->stride < 0 || t->stride > kMaxStride) return QG_E_ARG;
+  if (!es && t->stride != t->n_cols) return QG_E_ARG;
+  if (out && t->n_rows > 1 && t->stride < t->n_cols) return QG_E_ARG;
+  if (t->n_rows > 0 && t->n_cols > 0 && !t->data) return QG_E_NULL;
+  if ((uintptr_t)t->data & (es ? es - 1 : 15)) return QG_E_ARG;
+  return QG_OK;
+}
+
+int check_window(int64_t n_rows, int64_t r0, int64_t r1) {
+  return r0 < 0 || r0 > r1 || r1 > n_rows ? QG_E_RANGE : QG_OK;
+}
+
+int launch(int32_t x_type, const MxArgs &a, hipStream_t stream) {
+  switch (x_type) {
+    case QG_F32: MX_HIP(launch_mx<kF32>(a, stream)); break;
+    case QG_F16: MX_HIP(launch_mx<kF16>(a, stream)); break;
+    case QG_BF16: MX_HIP(launch_mx<kBf16>(a, stream)); break;
+    case QG_MXFP4: MX_HIP(launch_mx<kFp4>(a, stream)); break;
+    default: return QG_E_FMT;
+  }
+  return QG_OK;
+}
+
+int64_t row_bytes(const qg_tensor *x) {
+  return x->type == QG_MXFP4 ? x->n_cols / 32 * 17 : x->stride * elem_size(x->type);
+}
+
+int rows_mx(const qg_matrix *w, const qg_matrix *w2, int64_t r0, int64_t r1, const qg_tensor *x, const qg_tensor *y,
+            hipStream_t stream) {
+  int rc;
+  if ((rc = check_mx(w)) || (w2 && (rc = check_mx(w2)))) return rc;
+  if (w2 && (w2->n_rows != w->n_rows || w2->k != w->k)) return QG_E_SHAPE;
+  if ((rc = check_window(w->n_rows, r0, r1)) || (rc = check_tensor(x, true, false)) ||
+      (rc = check_tensor(y, false, true)))
+    return rc;
+  if (x->n_cols != w->k || y->n_rows != x->n_rows || y->n_cols != r1 - r0) return QG_E_SHAPE;
+  if (x->n_rows == 0 || r0 == r1) return QG_OK;
+  MxArgs a = {};
+  const int64_t rb = w->k / 32 * 17;
+  a.w = (const uint8_t *)w->data + r0 * rb;
+  a.w2 = w2 ? (const uint8_t *)w2->data + r0 * rb : nullptr;
+  a.x = (const uint8_t *)x->data;
+  a.y = y->data;
+  a.x_bytes = row_bytes(x);
+  a.y_stride = y->stride;
+  a.row_bytes = (int32_t)rb;
+  a.nb = (int32_t)(w->k / 32);
+  a.n = (int32_t)(r1 - r0);
+  a.places = (int32_t)x->n_rows;
+  a.x_rows = (int32_t)x->n_rows;
+  a.n_expert = a.n_sel = 1;
+  a.y_type = y->type;
+  return launch(x->type, a, stream);
+}
+
+int expert_mx(const qg_matrix *w, const qg_matrix *w2, int64_t n_expert, const qg_tensor *x, const int32_t *offsets,
+              const int32_t *slots, int32_t n_sel, const qg_tensor *y, hipStream_t stream) {
+  int rc;
+  if ((rc = check_mx(w)) || (w2 && (rc = check_mx(w2)))) return rc;
+  if (w2 && (w2->n_rows != w->n_rows || w2->k != w->k)) return QG_E_SHAPE;
+  if ((rc = check_tensor(x, true, false)) || (rc = check_tensor(y, false, true))) return rc;
+  if (n_expert < 1 || n_expert > QG_MAX_EXPERTS || w->n_rows % n_expert != 0) return QG_E_SHAPE;
+  const int64_t out = w->n_rows / n_expert;
+  if (x->n_cols != w->k || y->n_cols != out || (!slots && x->n_rows < y->n_rows)) return QG_E_SHAPE;
+  if (slots && n_sel < 1) return QG_E_ARG;
+  if (y->n_rows == 0 || out == 0) return QG_OK;
+  if (!offsets) return QG_E_NULL;
+  MxArgs a = {};
+  a.w = (const uint8_t *)w->data;
+  a.w2 = w2 ? (const uint8_t *)w2->data : nullptr;
+  a.x = (const uint8_t *)x->data;
+  a.y = y->data;
+  a.offsets = offsets;
+  a.slots = slots;
+  a.row_bytes = (int32_t)(w->k / 32 * 17);
+  a.expert_bytes = out * a.row_bytes;
+  a.x_bytes = row_bytes(x);
+  a.y_stride = y->stride;
+  a.nb = (int32_t)(w->k / 32);
+  a.n = (int32_t)out;
+  a.places = (int32_t)y->n_rows;
+  a.x_rows = (int32_t)x->n_rows;
+  a.n_expert = (int32_t)n_expert;
+  a.n_sel = slots ? n_sel : 1;
+  a.y_type = y->type;
+  return launch(x->type, a, stream);
+}
+
+// f(integral_constant<type>) for a checked float type.
+template <typename F>
+void with_type(int32_t type, F f) {
+  if (type == QG_F32) f(std::integral_constant<int, QG_F32>());
+  else if (type == QG_F16) f(std::integral_constant<int, QG_F16>());
+  else f(std::integral_constant<int, QG_BF16>());
+}
+
+}  // namespace
+
+extern "C" {
+
+int qgemv_mx_quantize(const qg_tensor *x, const qg_matrix *q, qg_stream_t stream) {
+  int rc;
+  if ((rc = check_mx(q)) || (rc = check_tensor(x, false, false))) return rc;
+  if (x->n_rows != q->n_rows || x->n_cols != q->k) return QG_E_SHAPE;
+  if (x->n_rows == 0) return QG_OK;
+  const int nb = (int)(q->k / 32);
+  const int64_t blocks = q->n_rows * nb, grid = (blocks + kQBlocks - 1) / kQBlocks;
+  if (grid > kMaxDim) return QG_E_SHAPE;
+  with_type(x->type, [&](auto T) {
+    hipLaunchKernelGGL(quantize_kernel<decltype(T)::value>, dim3((unsigned)grid), dim3(256), 0, stream,
+                       (const uint8_t *)x->data, x->stride, nb, blocks, (uint8_t *)q->data);
+  });
+  MX_HIP(hipGetLastError());
+  return QG_OK;
+}
+
+int qgemv_mx_dequantize(const qg_matrix *q, int64_t row_start, int64_t row_end, const qg_tensor *out,
+                        qg_stream_t stream) {
+  int rc;
+  if ((rc = check_mx(q)) || (rc = check_window(q->n_rows, row_start, row_end)) ||
+      (rc = check_tensor(out, false, true)))
+    return rc;
+  if (out->n_rows != row_end - row_start || out->n_cols != q->k) return QG_E_SHAPE;
+  if (out->n_rows == 0) return QG_OK;
+  const int nb = (int)(q->k / 32);
+  const int64_t blocks = out->n_rows * nb, grid = (blocks + 63) / 64;
+  if (grid > kMaxDim) return QG_E_SHAPE;
+  with_type(out->type, [&](auto T) {
+    hipLaunchKernelGGL(dequantize_kernel<decltype(T)::value>, dim3((unsigned)grid), dim3(256), 0, stream,
+                       (const uint8_t *)q->data + row_start * nb * 17, nb, blocks, (uint8_t *)out->data, out->stride);
+  });
+  MX_HIP(hipGetLastError());
+  return QG_OK;
+}
+
+int qgemv_rows_mx(const qg_matrix *w, int64_t row_start, int64_t row_end, const qg_tensor *x, const qg_tensor *y,
+                  qg_stream_t stream) {
+  return rows_mx(w, nullptr, row_start, row_end, x, y, stream);
+}
+
+int qgemv_rows_mx_swiglu(const qg_matrix *gate, const qg_matrix *up, int64_t row_start, int64_t row_end,
+                         const qg_tensor *x, const qg_tensor *h, qg_stream_t stream) {
+  if (!gate || !up) return QG_E_NULL;
+  return rows_mx(gate, up, row_start, row_end, x, h, stream);
+}
+
+int qgemv_expert_mx(const qg_matrix *w, int64_t n_expert, const qg_tensor *x, const int32_t *offsets,
+                    const int32_t *slots, int32_t n_sel, const qg_tensor *y, qg_stream_t stream) {
+  return expert_mx(w, nullptr, n_expert, x, offsets, slots, n_sel, y, stream);
+}
+
+int qgemv_expert_mx_swiglu(const qg_matrix *gate, const qg_matrix *up, int64_t n_expert, const qg_tensor *x,
+                           const int32_t *offsets, const int32_t *slots, int32_t n_sel, const qg_tensor *h,
+                           qg_stream_t stream) {
+  if (!gate || !up) return QG_E_NULL;
+  return expert_mx(gate, up, n_expert, x, offsets, slots, n_sel, h, stream);
+}
+
+int qgemv_expert_sort(const int32_t *ids, int64_t n_tok, int32_t n_sel, int64_t n_expert, int32_t *offsets,
+                      int32_t *slots, int32_t *pos, qg_stream_t stream) {
+  if (n_tok < 0 || n_sel < 1) return QG_E_ARG;
+  if (n_expert < 1 || n_expert > QG_MAX_EXPERTS || n_tok > (1ll << 30) / n_sel) return QG_E_SHAPE;
+  const int64_t n = n_tok * n_sel;
+  if (!offsets || (n > 0 && (!ids || !slots || !pos))) return QG_E_NULL;
+  hipLaunchKernelGGL(sort_kernel, dim3((unsigned)n_expert + 1), dim3(64 * kSortWaves), 0, stream, ids, (int)n,
+                     (int)n_expert, offsets, slots, pos);
+  MX_HIP(hipGetLastError());
+  return QG_OK;
+}
+
+int qgemv_expert_gather(const qg_tensor *x, const int32_t *slots, int32_t n_sel, const qg_tensor *out,
+                        qg_stream_t stream) {
+  int rc;
+  if ((rc = check_tensor(x, false, false)) || (rc = check_tensor(out, false, true))) return rc;
+  if (x->type != out->type) return QG_E_FMT;
+  if (x->n_cols != out->n_cols) return QG_E_SHAPE;
+  if (n_sel < 1) return QG_E_ARG;
+  if (out->n_rows == 0 || out->n_cols == 0) return QG_OK;
+  if (!slots) return QG_E_NULL;
+  const int es = elem_size(x->type);
+  const unsigned grid = (unsigned)std::min<int64_t>((out->n_rows + 3) / 4, 1 << 20);
+  hipLaunchKernelGGL(gather_kernel, dim3(grid), dim3(256), 0, stream, (const uint8_t *)x->data, x->stride * es,
+                     x->n_rows, x->n_cols * es, slots, n_sel, out->n_rows, (uint8_t *)out->data, out->stride * es);
+  MX_HIP(hipGetLastError());
+  return QG_OK;
+}
+
+int qgemv_expert_combine(const qg_tensor *y, const int32_t *pos, const float *w, int32_t n_sel, const qg_tensor *out,
+                         qg_stream_t stream) {
+  int rc;
+  if ((rc = check_tensor(y, false, false)) || (rc = check_tensor(out, false, true))) return rc;
+  if (y->n_cols != out->n_cols) return QG_E_SHAPE;
+  if (n_sel < 0) return QG_E_ARG;
+  if (out->n_rows == 0 || out->n_cols == 0) return QG_OK;
+  if (n_sel > 0 && !pos) return QG_E_NULL;
+  const int64_t groups = (out->n_cols + kCols - 1) / kCols;
+  const dim3 grid((unsigned)out->n_rows, (unsigned)std::min<int64_t>((groups + 255) / 256, 64));
+  with_type(y->type, [&](auto TY) {
+    with_type(out->type, [&](auto TO) {
+      hipLaunchKernelGGL((combine_kernel<decltype(TY)::value, decltype(TO)::value>), grid, dim3(256), 0, stream,
+                         (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel, out->n_cols,
+                         (uint8_t *)out->data, out->stride);
+    });
+  });
+  MX_HIP(hipGetLastError());
+  return QG_OK;
+}
+
+int qgemv_expert_combine_grad(const qg_tensor *dout, const qg_tensor *y, const int32_t *pos, const float *w,
+                              int32_t n_sel, const qg_tensor *dy, float *dw, qg_stream_t stream) {
+  int rc;
+  if ((rc = check_tensor(dout, false, false)) || (rc = check_tensor(y, false, false)) ||
+      (rc = check_tensor(dy, false, true)))
+    return rc;
+  if (dy->type != y->type) return QG_E_FMT;
+  if (dout->n_cols != y->n_cols || dy->n_cols != y->n_cols || dy->n_rows != y->n_rows) return QG_E_SHAPE;
+  if (n_sel < 1) return QG_E_ARG;
+  if (dout->n_rows > (1ll << 30) / n_sel) return QG_E_SHAPE;
+  if (y->n_rows > 0 && y->data == dy->data && y->n_cols > 0) return QG_E_ARG;
+  if (dout->n_rows == 0) return QG_OK;
+  if (!pos || !w || !dw) return QG_E_NULL;
+  with_type(dout->type, [&](auto TD) {
+    with_type(y->type, [&](auto TY) {
+      hipLaunchKernelGGL((combine_grad_kernel<decltype(TD)::value, decltype(TY)::value>),
+                         dim3((unsigned)(dout->n_rows * n_sel)), dim3(256), 0, stream, (const uint8_t *)dout->data,
+                         dout->stride, (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel,
+                         dout->n_cols, (uint8_t *)dy->data, dy->stride, dw);
+    });
+  });
+  MX_HIP(hipGetLastError());
+  return QG_OK;
+}
+
+}  // extern "C"

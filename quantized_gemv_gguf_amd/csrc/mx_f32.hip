@@ -1,0 +1,6 @@
+// mx_f32.hip -- products of f32 activations with MXFP4 weights (mx_gemm.h).
+#include "mx_launch.h"
+
+namespace qgemv_mx {
+template hipError_t launch_mx<kF32>(const MxArgs &a, hipStream_t stream);
+}

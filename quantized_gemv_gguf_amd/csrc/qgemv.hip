@@ -1069,6 +1069,20 @@ struct qg_streamer {
   uint64_t next;
 };
 
+namespace qgemv_detail {
+
+// For the library's other translation units: the text behind
+// qgemv_last_hip_error; no exception leaves a C entry.
+int record_hip_error(hipError_t e, const char *what) {
+  try {
+    return hip_fail(e, what);
+  } catch (...) {
+    return QG_E_HIP;
+  }
+}
+
+}  // namespace qgemv_detail
+
 extern "C" {
 
 const char *qgemv_version(void) { return "0.1.0"; }

@@ -1,0 +1,514 @@
+"""GPU parity of the MXFP4 prompt operators (include/qgemv_mx.h) against plain
+64-bit forms (mxref.py, where the bounds are derived): quantisation byte for
+byte, products within the bound of their fp32 sums, the sort's integers and the
+gather bit for bit, and the calls together as a prompt uses them."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import mxref
+import quantized_gemv_gguf_amd as q
+from mxref import near
+
+pytestmark = pytest.mark.gpu
+
+
+def T(kind):
+    import torch
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[kind]
+
+
+def dput(a, dev, kind=None):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if kind is None else t.to(T(kind))).to(dev)
+
+
+def host(t):
+    return t.cpu().double().numpy()
+
+
+def blocks(a, k, dev):
+    return q.Matrix(dput(a, dev), q.MXFP4, a.shape[0], k)
+
+
+def activations(rng, n, k, kind, dev, pad=0):
+    """(what the call takes, its values in 64 bits): floats, or MXFP4 blocks."""
+    x = rng.standard_normal((n, k + pad)) * 2.0 ** rng.uniform(-3, 3, (1, k + pad))
+    if kind == "mxfp4":
+        b = mxref.quantize(x[:, :k].astype(np.float32).astype(np.float64))
+        return blocks(b, k, dev), mxref.values(b, k)
+    t = dput(x.astype(np.float32), dev, kind)[:, :k]
+    return t, host(t)
+
+
+def nan_buffer(n, cols, kind, dev, pad=0):
+    import torch
+    return torch.full((n, cols + pad), float("nan"), dtype=T(kind), device=dev)
+
+
+# --- quantisation ------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,k,pad", [(1, 32, 0), (1, 2880, 0), (3, 64, 5), (257, 96, 1), (70, 4096, 32), (1021, 160, 0)])
+def test_quantize(dev, kind, n, k, pad):
+    import torch
+    rng = np.random.default_rng(n * 1000 + k)
+    x = rng.standard_normal((n, k + pad)) * 2.0 ** rng.integers(-6, 6, (n, 1))
+    x[0, :8] = [0.25, -0.75, 1.25, 5.0, 6.0, 2.5, 3.5, 0.0]
+    if n > 2:
+        x[1, :32] = 0.0
+        x[2, 3] = np.inf
+        x[n - 1, 7] = np.nan
+        x[n - 1, 40 % k] = -np.inf
+    t = dput(x.astype(np.float32), dev, kind)[:, :k]
+    out = torch.full((n * k // 32 * 17 + 64,), 0xA5, dtype=torch.uint8, device=dev)
+    m = q.Matrix(out[:n * k // 32 * 17], q.MXFP4, n, k)
+    q.qgemv_mx_quantize(t, m)
+    ref = mxref.quantize(host(t))
+    assert np.array_equal(m.data.cpu().numpy().reshape(n, -1), ref)
+    assert (out[n * k // 32 * 17:] == 0xA5).all().item(), "wrote past the blocks"
+
+
+def test_quantize_range(dev):
+    """Every exponent of fp32, subnormals among them, and ties at each of them."""
+    import torch
+    rows = []
+    for e in range(-149, 128):
+        s = 2.0 ** max(e - 2, -149)
+        r = np.arange(32) * 0.25 * s
+        r[31] = 2.0 ** e
+        rows.append(np.where(np.arange(32) % 3 == 1, -r, r))
+    x = np.array(rows).astype(np.float32)
+    m = q.Matrix(torch.zeros(len(rows) * 17, dtype=torch.uint8, device=dev), q.MXFP4, len(rows), 32)
+    q.qgemv_mx_quantize(dput(x, dev), m)
+    assert np.array_equal(m.data.cpu().numpy().reshape(-1, 17), mxref.quantize(x.astype(np.float64)))
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+def test_dequantize_every_code_and_scale(dev, kind):
+    import torch
+    b = np.zeros((256, 2, 17), np.uint8)
+    b[..., 0] = np.arange(256)[:, None]
+    b[:, 0, 1:] = np.arange(16) * 17
+    b[:, 1, 1:] = (np.arange(16) * 16 + 15 - np.arange(16))
+    ref = mxref.values(b.reshape(256, -1), 64)
+    out = nan_buffer(250, 64, kind, dev, 3)
+    q.qgemv_mx_dequantize(blocks(b.reshape(256, -1), 64, dev), 6, 256, out[:, :64])
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(ref[6:]).to(T(kind))
+    got = out[:, :64].cpu()
+    assert torch.equal(torch.nan_to_num(got.double(), nan=7.0), torch.nan_to_num(want.double(), nan=7.0))
+    assert torch.equal(torch.signbit(got)[~torch.isnan(got)], torch.signbit(want)[~torch.isnan(want)])
+    assert torch.isnan(out[:, 64:]).all().item()
+
+
+# --- products ------------------------------------------------------------------------
+
+# tokens, rows, k: single values; one block; tails of the four blocks of a step; rows and tokens around the tiles
+SHAPES = [(1, 1, 32), (1, 2880, 2880), (2, 17, 64), (5, 70, 96), (16, 128, 128), (17, 129, 160), (33, 63, 2880),
+          (64, 65, 256), (65, 200, 544), (130, 257, 1024), (300, 130, 288), (513, 300, 416), (7, 40, 11008)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
+@pytest.mark.parametrize("tok,n,k", SHAPES)
+def test_rows(dev, kind, tok, n, k):
+    rng = np.random.default_rng(tok + 7 * n + k)
+    out = ["f32", "f16", "bf16"][(tok + n) % 3]
+    skip, pad = 3 * (n % 2), n % 5
+    wb = mxref.random_blocks(rng, n + skip + 2, k)
+    x, xv = activations(rng, tok, k, kind, dev, pad=tok % 4)
+    y = nan_buffer(tok, n, out, dev, pad)
+    q.qgemv_rows_mx(blocks(wb, k, dev), skip, skip + n, x, y[:, :n])
+    ref, bound = mxref.product(xv, mxref.values(wb, k)[skip:skip + n], kind)
+    near(host(y[:, :n]), ref, bound, out)
+    assert np.isnan(host(y[:, n:])).all(), "wrote past a row"
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
+@pytest.mark.parametrize("tok,n,k", [(1, 2880, 2880), (3, 33, 96), (18, 64, 544), (100, 190, 256), (260, 129, 416)])
+def test_rows_swiglu(dev, kind, tok, n, k):
+    rng = np.random.default_rng(tok + n + k)
+    out = ["bf16", "f32", "f16"][tok % 3]
+    gb, ub = mxref.random_blocks(rng, n + 1, k, 115, 121), mxref.random_blocks(rng, n + 1, k, 115, 121)
+    x, xv = activations(rng, tok, k, kind, dev)
+    h = nan_buffer(tok, n, out, dev, 1)
+    q.qgemv_rows_mx_swiglu(blocks(gb, k, dev), blocks(ub, k, dev), 1, n + 1, x, h[:, :n])
+    g, dg = mxref.product(xv, mxref.values(gb, k)[1:], kind)
+    u, du = mxref.product(xv, mxref.values(ub, k)[1:], kind)
+    near(host(h[:, :n]), *mxref.swiglu(g, dg, u, du), out)
+    assert np.isnan(host(h[:, n:])).all()
+
+
+@pytest.mark.parametrize("tok", [2, 40, 200])
+def test_rows_special_values(dev, tok):
+    """Scales 255 (NaN) and 0 (subnormal weights), rows of zeros, infinities and NaN of x in their places alone."""
+    import torch
+    rng = np.random.default_rng(3)
+    n, k = 50, 320
+    wb = mxref.random_blocks(rng, n, k).reshape(n, -1, 17)
+    wb[5, 3, 0] = 255
+    wb[20, :, 0] = 0
+    # no zero codes where the infinities of x meet them, but in the rows of zeros (whose sums are exactly 0)
+    wb[:, 1, 1:] |= 0x11
+    wb[30, :, 1:] = 0
+    wb[31, :, 1:] = 0x88
+    wb = wb.reshape(n, -1)
+    wv = mxref.values(wb, k)
+    for kind in ("f32", "f16", "bf16"):
+        xv = rng.standard_normal((tok, k))
+        xv[0, 33], xv[1, 40] = np.inf, np.nan
+        x = dput(xv.astype(np.float32), dev, kind)
+        if kind == "f32":  # a NaN whose payload is in the lowest bits alone
+            x.view(torch.int32)[1, 40] = 0x7f800001
+        y = nan_buffer(tok, n, "f32", dev)
+        q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, x, y)
+        with np.errstate(invalid="ignore"):
+            ref, bound = mxref.product(host(x), wv, kind)
+        near(host(y), ref, np.where(np.isfinite(bound), bound, 0.0), "f32", kind)
+    xb = mxref.random_blocks(rng, tok, k, 120, 128).reshape(tok, -1, 17)
+    xb[1, 2, 0] = 255
+    xb = xb.reshape(tok, -1)
+    y = nan_buffer(tok, n, "f32", dev)
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, blocks(xb, k, dev), y)
+    ref, bound = mxref.product(mxref.values(xb, k), wv, "mxfp4")
+    near(host(y), ref, np.where(np.isfinite(bound), bound, 0.0), "f32", "mxfp4")
+
+
+def test_rows_f32_keeps_all_bits(dev):
+    """x with 24 significant bits against one weight of 1: the exact x comes back (three terms, no rounding)."""
+    rng = np.random.default_rng(4)
+    k, tok = 64, 40
+    wb = np.zeros((k, k // 32, 17), np.uint8)
+    wb[..., 0] = 127
+    for r in range(k):  # row r picks element r
+        e = r % 32
+        wb[r, r // 32, 1 + e % 16] = 2 << (4 * (e // 16))
+    x = (rng.standard_normal((tok, k)) * 2.0 ** rng.integers(-60, 60, (tok, k))).astype(np.float32)
+    for t in (1, 16, tok):
+        y = nan_buffer(t, k, "f32", dev)
+        q.qgemv_rows_mx(blocks(wb.reshape(k, -1), k, dev), 0, k, dput(x[:t], dev), y)
+        assert np.array_equal(host(y), x[:t].astype(np.float64))
+
+
+def test_rows_shared_x_and_no_tokens(dev):
+    rng = np.random.default_rng(5)
+    n, k = 40, 128
+    wb = mxref.random_blocks(rng, n, k)
+    x, xv = activations(rng, 1, k, "bf16", dev)
+    y = nan_buffer(20, n, "f32", dev)
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, x.expand(20, k), y)
+    ref, bound = mxref.product(np.repeat(xv, 20, 0), mxref.values(wb, k), "bf16")
+    near(host(y), ref, bound, "f32")
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, x[:0], y[:0])
+    q.qgemv_rows_mx(blocks(wb, k, dev), 9, 9, x.expand(20, k), y[:, :0])
+    near(host(y), ref, bound, "f32")
+
+
+# --- experts ---------------------------------------------------------------------------
+
+def expert_case(rng, tok, sel, n_expert, dropped):
+    ids = np.stack([rng.permutation(max(n_expert, sel))[:sel] for _ in range(tok)]).reshape(tok, sel)
+    ids[rng.random((tok, sel)) < dropped] = -1
+    return ids
+
+
+# tokens, choices, experts, rows, k, share of dropped slots
+EXPERTS = [(1, 1, 1, 16, 32, 0.0), (1, 4, 128, 96, 160, 0.0), (3, 2, 5, 33, 96, 0.2), (40, 4, 16, 130, 288, 0.1),
+           (200, 2, 3, 70, 256, 0.0), (130, 8, 64, 64, 128, 0.3), (64, 1, 200, 20, 64, 0.0), (9, 3, 4, 40, 64, 1.0),
+           (70, 2, 1024, 5, 32, 0.0), (500, 2, 7, 65, 160, 0.05)]
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
+@pytest.mark.parametrize("tok,sel,n_expert,n,k,dropped", EXPERTS)
+def test_experts(dev, kind, pair, tok, sel, n_expert, n, k, dropped):
+    rng = np.random.default_rng(tok * sel + n_expert + n)
+    out = ["f32", "bf16", "f16"][(tok + pair) % 3]
+    ids = expert_case(rng, tok, sel, n_expert, dropped)
+    offsets, slots, _ = mxref.sort(ids, n_expert)
+    gathered = (n + k // 32) % 2 == 0
+    spare = 3  # places behind the last slot
+    x, xv = activations(rng, tok if gathered else tok * sel + spare, k, kind, dev)
+    wbs = [mxref.random_blocks(rng, n_expert * n, k, 115, 121) for _ in range(1 + pair)]
+    y = nan_buffer(tok * sel + spare, n, out, dev, 2)
+    sl = dput(np.concatenate([slots, [-1] * spare]).astype(np.int32), dev)
+    call = q.qgemv_expert_mx_swiglu if pair else q.qgemv_expert_mx
+    call(*[blocks(b, k, dev) for b in wbs], n_expert, x, dput(offsets.astype(np.int32), dev), y[:, :n],
+         **(dict(slots=sl, n_sel=sel) if gathered else {}))
+    got = host(y)
+    kept = offsets[-1]
+    assert np.isnan(got[kept:]).all() and np.isnan(got[:, n:]).all(), "wrote beyond the places"
+    for e in range(n_expert):
+        lo, hi = offsets[e], offsets[e + 1]
+        if lo == hi:
+            continue
+        xs = xv[slots[lo:hi] // sel] if gathered else xv[lo:hi]
+        r = [mxref.product(xs, mxref.values(b[e * n:(e + 1) * n], k), kind) for b in wbs]
+        near(got[lo:hi, :n], *(mxref.swiglu(*r[0], *r[1]) if pair else r[0]), out, f"expert {e}")
+
+
+def test_experts_all_to_one_and_foreign_slots(dev):
+    """Every token at the last expert; slots that name tokens x does not have count as rows of zeros."""
+    import torch
+    rng = np.random.default_rng(8)
+    tok, n_expert, n, k = 150, 12, 48, 192
+    x, xv = activations(rng, tok, k, "bf16", dev)
+    wb = mxref.random_blocks(rng, n_expert * n, k)
+    offsets = torch.zeros(n_expert + 1, dtype=torch.int32, device=dev)
+    offsets[-1] = tok
+    slots = torch.arange(tok, dtype=torch.int32, device=dev)
+    slots[7], slots[149] = tok + 5, -3
+    y = nan_buffer(tok, n, "f32", dev)
+    q.qgemv_expert_mx(blocks(wb, k, dev), n_expert, x, offsets, y, slots=slots, n_sel=1)
+    xv = xv.copy()
+    xv[[7, 149]] = 0
+    ref, bound = mxref.product(xv, mxref.values(wb[-n:], k), "bf16")
+    near(host(y), ref, bound, "f32")
+    # offsets beyond the places are clamped to them
+    offsets[-1] = tok + 1000
+    y.fill_(float("nan"))
+    q.qgemv_expert_mx(blocks(wb, k, dev), n_expert, x, offsets, y, slots=slots, n_sel=1)
+    near(host(y), ref, bound, "f32")
+
+
+# --- routing ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tok,sel,n_expert,dropped", [(0, 4, 8, 0.0), (1, 1, 1, 0.0), (1, 4, 128, 0.0), (63, 1, 2, 0.3),
+                                                      (64, 4, 16, 0.0), (65, 4, 1024, 0.1), (257, 8, 60, 0.5),
+                                                      (1500, 4, 128, 0.02), (3000, 6, 7, 0.0), (5, 2, 3, 1.0)])
+def test_sort(dev, tok, sel, n_expert, dropped):
+    import torch
+    rng = np.random.default_rng(tok + sel)
+    ids = rng.integers(0, n_expert, (tok, sel))
+    out = rng.random((tok, sel)) < dropped
+    ids[out] = rng.choice([-1, -2 ** 31, n_expert, 2 ** 31 - 1], out.sum())
+    n = tok * sel
+    bufs = [torch.full((m + 4,), 77, dtype=torch.int32, device=dev) for m in (n_expert + 1, n, n)]
+    q.qgemv_expert_sort(dput(ids.astype(np.int32), dev).view(tok, sel), n_expert, *bufs)
+    for buf, ref in zip(bufs, mxref.sort(ids, n_expert)):
+        assert np.array_equal(buf.cpu().numpy(), np.concatenate([ref.ravel(), [77] * 4]))
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tok,sel,cols", [(1, 4, 2880), (5, 1, 1), (9, 2, 7), (33, 3, 64), (40, 4, 250), (20, 2, 2049)])
+def test_gather(dev, kind, tok, sel, cols):
+    import torch
+    rng = np.random.default_rng(cols)
+    x = dput(rng.standard_normal((tok, cols + 3)).astype(np.float32), dev, kind)[:, :cols]
+    slots = rng.permutation(tok * sel).astype(np.int32)
+    slots[::5] = -1
+    slots[1::7] = tok * sel + 9
+    out = nan_buffer(tok * sel, cols, kind, dev, 1)
+    q.qgemv_expert_gather(x, dput(slots, dev), sel, out[:, :cols])
+    ok = (slots >= 0) & (slots < tok * sel)
+    got = out.cpu()
+    assert torch.equal(got[ok][:, :cols], x.cpu()[slots[ok] // sel])
+    assert torch.isnan(got[~ok]).all() and torch.isnan(got[:, cols:]).all()
+
+
+@pytest.mark.parametrize("ky,ko", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f32", "f16"), ("bf16", "f32")])
+@pytest.mark.parametrize("tok,sel,cols", [(1, 4, 2880), (5, 1, 1), (9, 2, 7), (33, 3, 64), (12, 8, 4100), (3, 0, 40)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_combine(dev, ky, ko, tok, sel, cols, weighted):
+    import torch
+    rng = np.random.default_rng(cols + sel)
+    rows = max(1, tok * sel)
+    y = dput(rng.standard_normal((rows, cols + 2)).astype(np.float32), dev, ky)[:, :cols]
+    pos = rng.permutation(rows)[:tok * sel].reshape(tok, sel)
+    pos[rng.random((tok, sel)) < 0.2] = -1
+    if sel:
+        pos[0] = -1          # a token without any expert
+        pos[-1, 0] = rows    # beyond y
+    w = rng.standard_normal((tok, sel)).astype(np.float32)
+    out = nan_buffer(tok, cols, ko, dev, 3)
+    q.qgemv_expert_combine(y, dput(pos.astype(np.int32), dev), out[:, :cols], w=dput(w, dev) if weighted else None)
+    yv, ref, mag = host(y), np.zeros((tok, cols)), np.zeros((tok, cols))
+    for t in range(tok):
+        for s in range(sel):
+            if 0 <= pos[t, s] < rows:
+                term = (float(w[t, s]) if weighted else 1.0) * yv[pos[t, s]]
+                ref[t] += term
+                mag[t] += np.abs(term)
+    near(host(out[:, :cols]), ref, sel * 2.0 ** -24 * mag, ko)
+    assert np.isnan(host(out[:, cols:])).all()
+
+
+@pytest.mark.parametrize("kd,ky", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("tok,sel,cols", [(1, 4, 2880), (5, 1, 1), (9, 2, 7), (33, 3, 64), (6, 8, 4100)])
+def test_combine_grad(dev, kd, ky, tok, sel, cols):
+    import torch
+    rng = np.random.default_rng(cols + sel)
+    rows = tok * sel
+    dout = dput(rng.standard_normal((tok, cols)).astype(np.float32), dev, kd)
+    y = dput(rng.standard_normal((rows, cols + 2)).astype(np.float32), dev, ky)[:, :cols]
+    pos = rng.permutation(rows).reshape(tok, sel)
+    pos[rng.random((tok, sel)) < 0.2] = -1
+    w = rng.standard_normal((tok, sel)).astype(np.float32)
+    dy = nan_buffer(rows, cols, ky, dev, 1)
+    dw = torch.full((tok, sel), float("nan"), device=dev)
+    q.qgemv_expert_combine_grad(dout, y, dput(pos.astype(np.int32), dev), dput(w, dev), dy[:, :cols], dw)
+    dv, yv, got, gw = host(dout), host(y), host(dy), host(dw)
+    named = np.zeros(rows, bool)
+    for t in range(tok):
+        for s in range(sel):
+            p = pos[t, s]
+            if p < 0:
+                assert gw[t, s] == 0.0
+                continue
+            named[p] = True
+            near(got[p, :cols], float(w[t, s]) * dv[t], 0.0, ky)
+            # a lane's run of fmas, six additions over the lanes and two over the waves
+            adds = 8 * -(-cols // 2048) + 8
+            mag = np.sum(np.abs(dv[t] * yv[p]))
+            near(gw[t, s:s + 1], np.sum(dv[t] * yv[p])[None], adds * 2.0 ** -24 * mag, "f32")
+    assert np.isnan(got[~named]).all() and np.isnan(got[:, cols:]).all()
+
+
+# --- together ----------------------------------------------------------------------------
+
+class Block:
+    """A mixture of experts: its weights, a prompt, and the calls of one pass."""
+
+    def __init__(self, dev, tok, sel, n_expert, d, f, kind="bf16", four_bit=False, dropped=0.1, seed=1):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.n_expert, self.sel, self.four_bit, self.kind = n_expert, sel, four_bit, kind
+        self.ids_host = expert_case(rng, tok, sel, n_expert, dropped)
+        self.wb = [mxref.random_blocks(rng, n_expert * n, k, 115, 121) for n, k in ((f, d), (f, d), (d, f))]
+        self.w = [blocks(b, k, dev) for b, k in zip(self.wb, (d, d, f))]
+        self.x, self.xv = activations(rng, tok, d, kind, dev)
+        self.rw_host = rng.random((tok, sel)).astype(np.float32)
+        self.ids, self.rw = dput(self.ids_host.astype(np.int32), dev), dput(self.rw_host, dev)
+        z = lambda n, t: torch.zeros(n, dtype=t, device=dev)  # noqa: E731
+        self.offsets, self.slots, self.pos = z(n_expert + 1, torch.int32), z(tok * sel, torch.int32), z((tok, sel), torch.int32)
+        self.h, self.y = z((tok * sel, f), T(kind)), z((tok * sel, d), T(kind))
+        self.out = z((tok, d), torch.float32)
+        self.xq = q.Matrix(z(tok * d // 32 * 17, torch.uint8), q.MXFP4, tok, d)
+        self.hq = q.Matrix(z(tok * sel * f // 32 * 17, torch.uint8), q.MXFP4, tok * sel, f)
+
+    def run(self, stream=None):
+        x, h = self.x, self.h
+        q.qgemv_expert_sort(self.ids, self.n_expert, self.offsets, self.slots, self.pos, stream=stream)
+        if self.four_bit:
+            q.qgemv_mx_quantize(x, self.xq, stream=stream)
+            x = self.xq
+        q.qgemv_expert_mx_swiglu(*self.w[:2], self.n_expert, x, self.offsets, self.h, slots=self.slots,
+                                 n_sel=self.sel, stream=stream)
+        if self.four_bit:
+            q.qgemv_mx_quantize(h, self.hq, stream=stream)
+            h = self.hq
+        q.qgemv_expert_mx(self.w[2], self.n_expert, h, self.offsets, self.y, stream=stream)
+        q.qgemv_expert_combine(self.y, self.pos, self.out, w=self.rw, stream=stream)
+        return self.out
+
+
+@pytest.mark.parametrize("tok,four_bit", [(1, False), (37, False), (37, True), (300, False), (300, True)])
+def test_a_prompt_through_the_experts(dev, tok, four_bit):
+    """Every stage against its definition on the stage before, as computed."""
+    b = Block(dev, tok, 4, 16, 160, 96, four_bit=four_bit)
+    b.run()
+    offsets, slots, pos = mxref.sort(b.ids_host, b.n_expert)
+    assert np.array_equal(b.pos.cpu().numpy(), pos)
+    kept = offsets[-1]
+    kind = "mxfp4" if four_bit else b.kind
+    xv = mxref.values(mxref.quantize(b.xv), 160) if four_bit else b.xv
+    hv, yv = host(b.h)[:kept], host(b.y)[:kept]
+    hin = mxref.values(mxref.quantize(hv), 96) if four_bit else hv
+    for e in range(b.n_expert):
+        lo, hi = offsets[e], offsets[e + 1]
+        xs = xv[slots[lo:hi] // 4]
+        g, u = (mxref.product(xs, mxref.values(wb[e * 96:(e + 1) * 96], 160), kind) for wb in b.wb[:2])
+        near(hv[lo:hi], *mxref.swiglu(*g, *u), b.kind)
+        near(yv[lo:hi], *mxref.product(hin[lo:hi], mxref.values(b.wb[2][e * 160:(e + 1) * 160], 96), kind), b.kind)
+    ref, mag = np.zeros((tok, 160)), np.zeros((tok, 160))
+    for t in range(tok):
+        for s in range(4):
+            if pos[t, s] >= 0:
+                ref[t] += b.rw_host[t, s].astype(np.float64) * yv[pos[t, s]]
+                mag[t] += np.abs(b.rw_host[t, s].astype(np.float64) * yv[pos[t, s]])
+    near(host(b.out), ref, 4 * 2.0 ** -24 * mag, "f32")
+
+
+def test_captured_replayed_and_on_other_streams(dev):
+    """The pass captured once and replayed on new inputs, each replay against the eager pass, eager work between
+    them; and two passes at once on two streams."""
+    import torch
+    a, b = Block(dev, 90, 4, 16, 160, 96, seed=2), Block(dev, 70, 2, 9, 128, 64, "f32", seed=3)
+    want_a, want_b = a.run().clone(), b.run().clone()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.out.zero_(), b.out.zero_()
+        torch.cuda.synchronize()
+        a.run(s1), b.run(s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, want_a) and torch.equal(b.out, want_b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.run()
+    rng = np.random.default_rng(9)
+    for i in range(4):
+        a.x.copy_(dput(rng.standard_normal(a.x.shape).astype(np.float32), dev, "bf16"))
+        a.ids.copy_(dput(expert_case(rng, 90, 4, 16, 0.1 * i).astype(np.int32), dev))
+        g.replay()
+        torch.cuda.synchronize()
+        got = a.out.clone()
+        a.out.zero_()
+        assert torch.equal(a.run(), got)
+
+
+@pytest.mark.parametrize("tok,sel,cols", [(7, 3, 45), (16, 2, 64)])
+def test_gradients_against_differences(dev, tok, sel, cols):
+    """<dout, combine> moved along random directions of y and w, and <dxs, gather> along x: both are linear in each
+    argument, so the difference is the directional derivative up to fp32 rounding."""
+    import torch
+    rng = np.random.default_rng(11)
+    ids = expert_case(rng, tok, sel, 5, 0.2)
+    offsets, slots, pos = mxref.sort(ids, 5)
+    P, S = dput(pos.astype(np.int32), dev), dput(slots.astype(np.int32), dev)
+    r = lambda *s: dput(rng.standard_normal(s).astype(np.float32), dev)  # noqa: E731
+    y, w, dout, ydir, wdir = r(tok * sel, cols), r(tok, sel), r(tok, cols), r(tok * sel, cols), r(tok, sel)
+    dy, dw = torch.zeros_like(y), torch.zeros_like(w)
+    q.qgemv_expert_combine_grad(dout, y, P, w, dy, dw)
+
+    def loss(yy, ww):
+        out = torch.empty(tok, cols, device=dev)
+        q.qgemv_expert_combine(yy, P, out, w=ww)
+        return float((out.double() * dout.double()).sum())
+
+    # n terms of magnitude about 1 each, fp32 sums within: n * sel * 2^-24 and the inputs' own rounding
+    tol = 8 * (sel + 4) * 2.0 ** -24 * tok * cols * sel
+    assert abs((loss(y + ydir, w) - loss(y, w)) - float((dy.double() * ydir.double()).sum())) <= tol
+    assert abs((loss(y, w + wdir) - loss(y, w)) - float((dw.double() * wdir.double()).sum())) <= tol
+    x, xdir, dxs = r(tok, cols), r(tok, cols), r(tok * sel, cols)
+    dx = torch.empty(tok, cols, device=dev)
+    q.qgemv_expert_combine(dxs, P, dx)
+
+    def gathered(v):
+        out = torch.zeros(tok * sel, cols, device=dev)
+        q.qgemv_expert_gather(v, S, sel, out)
+        return float((out.double() * dxs.double()).sum())
+
+    assert abs((gathered(x + xdir) - gathered(x)) - float((dx.double() * xdir.double()).sum())) <= tol
+
+
+def test_refusals_leave_outputs(dev):
+    import torch
+    w = blocks(mxref.random_blocks(np.random.default_rng(1), 8, 64), 64, dev)
+    x = torch.ones(4, 64, device=dev)
+    y = torch.full((4, 8), 7.0, device=dev)
+    with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+        q.qgemv_rows_mx(w, 0, 7, x, y)
+    with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+        q.qgemv_rows_mx(w, 0, 8, x[:3], y)
+    with pytest.raises(q.QgemvError, match="QG_E_FMT"):
+        q.qgemv_rows_mx(q.Matrix(torch.zeros(8 * 2 * 18, dtype=torch.uint8, device=dev), q.Q4_0, 8, 64), 0, 8, x, y)
+    with pytest.raises(q.QgemvError, match="QG_E_ARG"):
+        q.qgemv_rows_mx(w, 0, 8, x, y[:1].expand(4, 8))
+    with pytest.raises(ValueError, match="needs"):
+        q.qgemv_expert_mx(w, 2, x, torch.zeros(2, dtype=torch.int32, device=dev), y[:, :4].contiguous())
+    with pytest.raises(ValueError, match="needs"):
+        q.qgemv_rows_mx(w, 0, 8, q.Matrix(torch.zeros(17, dtype=torch.uint8, device=dev), q.MXFP4, 4, 64), y)
+    assert (y == 7.0).all().item()

@@ -122,7 +122,7 @@ int qgemv_expert_sort(const int32_t *ids, int64_t n_tok, int32_t n_sel, int64_t 
  * the last offset), y->n_cols = out; without slots x->n_rows >= y->n_rows.
  * Each weight is read once per tile of its expert's places; experts without a
  * token cost nothing.  Rows of y behind the last offset stay as they were.
- * Offsets are clamped to [0, y->n_rows]; a src outside x's rows counts as a
+ * Offsets are clamped to [0, y->n_rows]; a src outside x's rows gives a
  * row of zeros.  x, y and arithmetic as qgemv_rows_mx. */
 int qgemv_expert_mx(const qg_matrix *w, int64_t n_expert, const qg_tensor *x, const int32_t *offsets,
                     const int32_t *slots, int32_t n_sel, const qg_tensor *y, qg_stream_t stream);

@@ -457,7 +457,7 @@ int expert_mx(const qg_matrix *w, const qg_matrix *w2, int64_t n_expert, const q
   a.expert_bytes = out * a.row_bytes;
   a.x_bytes = row_bytes(x);
   a.y_stride = y->stride;
-  a.nb = (int32_t)(w->k / 32);
+  a.nb = x->n_rows > 0 ? (int32_t)(w->k / 32) : 0;  // without any row of x every sum is empty
   a.n = (int32_t)out;
   a.places = (int32_t)y->n_rows;
   a.x_rows = (int32_t)x->n_rows;

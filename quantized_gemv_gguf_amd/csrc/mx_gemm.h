@@ -23,6 +23,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "qgemv_mx.h"
 
 namespace qgemv_mx {
@@ -61,51 +63,56 @@ struct Tile {
   int expert, n0, m0, m_end;
 };
 
-// Tile `id` of the grid.  Workgroups go to the eight XCDs in turn; each XCD
-// takes one contiguous run of tiles, so that neighbours in the order below
-// share an L2.  Order: experts; within an expert bands of eight token tiles;
-// within a band tile rows n, and innermost the band's token tiles, so one
-// weight tile is read by up to eight neighbours and the band's tokens stay in
-// the XCD's L2 for the whole sweep over n.
+// This workgroup's tile.  Workgroups go to the eight XCDs in turn; each XCD
+// takes one contiguous run of the tiles there are (of experts: fewer than the
+// grid's bound, so the runs are cut by the count found here), so that
+// neighbours in the order below share an L2.  Order: experts; within an expert
+// bands of eight token tiles; within a band tile rows n, and innermost the
+// band's token tiles, so one weight tile is read by up to eight neighbours and
+// the band's tokens stay in the XCD's L2 for the whole sweep over n.
 // Every wave finds its tile by itself: lane l sums the token tiles of its run
 // of experts, a scan over the lanes gives the first tile of each run, and the
 // lane whose run holds the tile walks it.
 template <int TM>
 __device__ __forceinline__ bool find_tile(const MxArgs &a, int tn_rows, Tile *t) {
-  const int per = (a.tiles + 7) >> 3;
-  const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || id >= a.tiles) return false;
-  int e = 0, lo = 0, hi = a.places, rem = id;
+  const int lane = threadIdx.x & 63;
+  const int run = (a.n_expert + 63) >> 6;
+  const int e0 = min(lane * run, a.n_expert), e1 = min(e0 + run, a.n_expert);
+  auto at = [&](int i) { return min(max(a.offsets[i], 0), a.places); };
+  int mine = 0, upto = 0, tiles = a.tiles;
   if (a.offsets) {
-    const int lane = threadIdx.x & 63;
-    const int run = (a.n_expert + 63) >> 6;
-    const int e0 = min(lane * run, a.n_expert), e1 = min(e0 + run, a.n_expert);
-    auto at = [&](int i) { return min(max(a.offsets[i], 0), a.places); };
-    int mine = 0, o = e0 < e1 ? at(e0) : 0;
+    int o = e0 < e1 ? at(e0) : 0;
     for (int i = e0; i < e1; ++i) {
       const int q = at(i + 1);
       mine += (max(q - o, 0) + TM - 1) / TM;
       o = q;
     }
-    int upto = mine;
+    upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(upto, d);
       if (lane >= d) upto += v;
     }
-    const int mt = id / a.tiles_n;  // token tiles before this tile's expert's end
+    tiles = min(tiles, __builtin_amdgcn_readlane(upto, 63) * a.tiles_n);
+  }
+  const int per = (tiles + 7) >> 3, at_xcd = (int)(blockIdx.x >> 3);
+  const int id = (int)(blockIdx.x & 7) * per + at_xcd;
+  if (at_xcd >= per || id >= tiles) return false;
+  int e = 0, lo = 0, hi = a.places, rem = id;
+  if (a.offsets) {
+    const int mt = id / a.tiles_n;  // token tiles before this one, over all experts
     const uint64_t past = __ballot(upto > mt);
-    if (!past) return false;        // behind the last expert's last tile
+    if (!past) return false;
     const int src = __builtin_ctzll(past);
-    int first = __shfl(upto - mine, src);
-    e = __shfl(e0, src);
-    const int last = __shfl(e1, src);
+    int first = __builtin_amdgcn_readlane(upto - mine, src);
+    e = __builtin_amdgcn_readlane(e0, src);
+    const int last = __builtin_amdgcn_readlane(e1, src);
     lo = at(e);
     hi = at(e + 1);
     for (;;) {
-      const int tiles = (max(hi - lo, 0) + TM - 1) / TM;
-      if (mt < first + tiles || e + 1 >= last) break;
-      first += tiles;
+      const int here = (max(hi - lo, 0) + TM - 1) / TM;
+      if (mt < first + here || e + 1 >= last) break;
+      first += here;
       ++e;
       lo = hi;
       hi = at(e + 1);
@@ -169,37 +176,66 @@ __device__ __forceinline__ void store4(const MxArgs &a, int place, int n, int le
 
 // The bf16 terms of eight values in the lane order of the codes' word: element
 // pairs (lo[b], hi[b]), lo = four values from 4q, hi = four from 16 + 4q.
-// Terms are cut, not rounded: the rest is exact, and an infinity or NaN stays
-// in the first term alone.
+// Terms are cut, not rounded: the rest is exact.
+// What a lane loads of a block: fp32 its own four and four values, two 16-byte
+// loads; bf16 and fp16 values 8q .. 8q + 7 in one, of which lanes q and q ^ 2
+// exchange halves, so that lane q holds word 2 (q & 1) + (q >> 1).
 template <int XK> struct XRaw;
-template <> struct XRaw<kBf16> { u32x2 lo, hi; };
-template <> struct XRaw<kF16> { u32x2 lo, hi; };
+template <> struct XRaw<kBf16> { u32x2 a, b; };
+template <> struct XRaw<kF16> { u32x2 a, b; };
 template <> struct XRaw<kF32> { f32x4 lo, hi; };
+
+template <int XK> __device__ __forceinline__ int x_word(int q) { return XK == kF32 ? q : 2 * (q & 1) + (q >> 1); }
+
+__device__ __forceinline__ uint32_t from_lane_xor2(uint32_t v) {  // lanes of a quad: 2, 3, 0, 1
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true);
+}
+
+template <int XK>
+__device__ __forceinline__ void x_load(const uint8_t *p, XRaw<XK> &r) {  // p: the block's values, q: lane % 4
+  const int q = threadIdx.x & 3;
+  if constexpr (XK == kF32) {
+    __builtin_memcpy(&r.lo, p + 16 * q, 16);
+    __builtin_memcpy(&r.hi, p + 16 * q + 64, 16);
+  } else {
+    u32x4 v;
+    __builtin_memcpy(&v, p + 16 * q, 16);
+    r.a = v.xy;
+    r.b = v.zw;
+  }
+}
 
 __device__ __forceinline__ uint32_t top_halves(uint32_t lo, uint32_t hi) {  // (lo >> 16) | (hi & 0xffff0000)
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// v cut to its first bf16; *rest = v minus it, exactly (0 for an infinity or NaN)
-__device__ __forceinline__ uint32_t cut(float v, float *rest) {
-  const uint32_t b = __float_as_uint(v);
-  const bool fine = (b & 0x7f800000u) != 0x7f800000u;
-  // a NaN keeps a set top mantissa bit, so the cut does not turn it into an infinity
-  const uint32_t h = (b & 0xffff0000u) | (v != v ? 0x00400000u : 0u);
-  *rest = fine ? v - __uint_as_float(h) : 0.0f;
+// v cut to its first bf16; *rest = v minus it, exactly: 0 for an infinity, and
+// NaN for a NaN, which then stays one whatever the cut leaves of its payload.
+__device__ __forceinline__ uint32_t cut(float v, float *rest, bool first) {
+  const uint32_t h = __float_as_uint(v) & 0xffff0000u;
+  *rest = v - __uint_as_float(h);
+  if (first && __builtin_isinf(v)) *rest = 0.0f;
   return h;
 }
 
 template <int XK>
 __device__ __forceinline__ void x_terms(const XRaw<XK> &r, u32x4 (&out)[XK]) {
+  u32x2 l2, h2;
+  if constexpr (XK != kF32) {
+    const bool first = !(threadIdx.x & 2);
+    const u32x2 give = first ? r.b : r.a;
+    const u32x2 got = {from_lane_xor2(give.x), from_lane_xor2(give.y)};
+    l2 = first ? r.a : got;
+    h2 = first ? got : r.b;
+  }
   if constexpr (XK == kBf16) {
-    out[0] = u32x4{__builtin_amdgcn_perm(r.hi.x, r.lo.x, 0x05040100u), __builtin_amdgcn_perm(r.hi.x, r.lo.x, 0x07060302u),
-                   __builtin_amdgcn_perm(r.hi.y, r.lo.y, 0x05040100u), __builtin_amdgcn_perm(r.hi.y, r.lo.y, 0x07060302u)};
+    out[0] = u32x4{__builtin_amdgcn_perm(h2.x, l2.x, 0x05040100u), __builtin_amdgcn_perm(h2.x, l2.x, 0x07060302u),
+                   __builtin_amdgcn_perm(h2.y, l2.y, 0x05040100u), __builtin_amdgcn_perm(h2.y, l2.y, 0x07060302u)};
   } else {
     float lo[4], hi[4];
     if constexpr (XK == kF16) {
       typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-      const h4 l = __builtin_bit_cast(h4, r.lo), h = __builtin_bit_cast(h4, r.hi);
+      const h4 l = __builtin_bit_cast(h4, l2), h = __builtin_bit_cast(h4, h2);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         lo[b] = (float)l[b];
@@ -220,7 +256,7 @@ __device__ __forceinline__ void x_terms(const XRaw<XK> &r, u32x4 (&out)[XK]) {
           out[t][b] = top_halves(__float_as_uint(lo[b]), __float_as_uint(hi[b]));
         } else {
           float rl, rh;
-          const uint32_t l = cut(lo[b], &rl), h = cut(hi[b], &rh);
+          const uint32_t l = cut(lo[b], &rl, t == 0), h = cut(hi[b], &rh, t == 0);
           out[t][b] = top_halves(l, h);
           lo[b] = rl;
           hi[b] = rh;
@@ -228,6 +264,31 @@ __device__ __forceinline__ void x_terms(const XRaw<XK> &r, u32x4 (&out)[XK]) {
       }
   }
 }
+
+// A block at any address: 17-byte blocks start at any byte, and the five
+// aligned words that hold one are read as words 0 .. 3 and 3 .. 4.  For a wave
+// of 16 rows of four blocks, a compute unit's address unit takes 17 cycles for
+// a 16-byte load on a word's boundary, 65 for one off it, 20 for the 8-byte
+// load, and 37 for a load of the fifth word alone (which takes a cycle per
+// line, not per four lanes).  The words lie inside the 16-byte granules that the block
+// touches.
+struct BlockRaw {
+  u32x4 a;
+  u32x2 c;
+};
+__device__ __forceinline__ void block_load(const uint8_t *words, BlockRaw &r) {
+  const uint8_t *p = (const uint8_t *)__builtin_assume_aligned(words, 4);
+  __builtin_memcpy(&r.a, p, 16);
+  __builtin_memcpy(&r.c, p + 12, 8);
+}
+// The codes (bytes 1 .. 16) of a block that starts at byte `phase` (0 .. 3) of its words.
+__device__ __forceinline__ u32x4 block_codes(const BlockRaw &r, uint32_t phase) {
+  asm volatile("" : : "v"(r.c));  // (keeps the second load whole: only its last word is new)
+  const uint32_t sel = 0x04030201u + 0x01010101u * phase;
+  return u32x4{__builtin_amdgcn_perm(r.a.y, r.a.x, sel), __builtin_amdgcn_perm(r.a.z, r.a.y, sel),
+               __builtin_amdgcn_perm(r.a.w, r.a.z, sel), __builtin_amdgcn_perm(r.c.y, r.a.w, sel)};
+}
+__device__ __forceinline__ uint32_t block_scale(const BlockRaw &r, uint32_t phase) { return r.a.x >> (8 * phase); }
 
 // Word j of a lane's block as four bf16 pairs, scale included.
 __device__ __forceinline__ bf16x8 weights8(uint32_t codes, float scale) {
@@ -246,145 +307,173 @@ __device__ __forceinline__ float scale_of(uint32_t bytes, int f) {
   return __uint_as_float(((bytes >> (8 * f)) & 0xffu) << 23);
 }
 
-// The tiled product.  A workgroup of WN x WM waves owns 16 FN WN rows of W (of
-// each of a pair) and 16 FM WM tokens; a wave 16 FN x 16 FM.  Per step of four
-// blocks (128 values): the next step's blocks and activations are loaded into
-// registers while the current step, in LDS, is multiplied.
-// LDS: codes row-major, 16 bytes per (row, block), so a wave's fragment of 16
-// rows is 1 KB read once without conflicts; scale bytes of four fragments of
-// 16 rows in one word; float x as [term][fragment][word j][token][block], one
-// fragment and word 1 KB in a row, planes of words 64 bytes apart beyond it so
-// that a token's sixteen pieces are written to sixteen bank groups.
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM>
+// f(integral_constant<0>) ... f(integral_constant<N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<N, I + 1>(f);
+  }
+}
+
+// The tiled product.  A workgroup of WN x WM x WK waves owns 16 FN WN rows of W
+// (of each of a pair) and 16 FM WM tokens; a wave 16 FN x 16 FM of them, over
+// every WK-th group of four blocks (128 values), and the WK partial sums are
+// added in order through LDS at the end.  A stage is KS such groups: the next
+// stage's blocks and activations are loaded into registers while the current
+// one, in LDS, is multiplied.  NBUF = 2: two stages in LDS, one barrier each.
+// LDS: codes [group][row][block], 16 bytes each, so a wave's fragment of 16
+// rows is 1 KB read without conflicts; scale bytes of four fragments of 16
+// rows in one word; float x as [term][group][fragment][word j][token][block],
+// the planes of words 64 bytes apart beyond their 1 KB so that a token's
+// sixteen pieces are written to sixteen bank groups.
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF>
 struct MxTile {
-  static constexpr int kThreads = 64 * WN * WM;
+  static constexpr int kThreads = 64 * WN * WM * WK;
   static constexpr int TN = 16 * FN * WN, TM = 16 * FM * WM;
   static constexpr int kMats = PAIR ? 2 : 1;
   static constexpr int kWRows = TN * kMats;
-  static constexpr int NW = kWRows * 4 / kThreads;                          // blocks of W per thread and step
-  static constexpr int NX = XK == kFp4 ? (TM * 4 + kThreads - 1) / kThreads : (TM * 16 + kThreads - 1) / kThreads;
-  static constexpr int kPlane = 1024 + 64;                                   // one word of 16 tokens, padded
+  static constexpr int kBlk = 4 * KS;                          // blocks of a row per stage
+  static constexpr int kRowStep = kThreads / kBlk;             // rows of W (of MXFP4 x) loaded at a time
+  static constexpr int NW = kWRows / kRowStep;
+  static constexpr int kTokStep = XK == kFp4 ? kRowStep : kRowStep / 4;
+  static constexpr int NX = (TM + kTokStep - 1) / kTokStep;
+  static constexpr int kWGroup = kWRows * 64 + 256 / KS;       // codes of one group, padded
+  static constexpr int kWSGroup = (kWRows + 63) / 64 * 256;    // its scales
+  static constexpr int kPlane = 1024 + 64;                     // one word of 16 tokens, padded
   static constexpr int kXFrag = 4 * kPlane;
-  static constexpr int kWBytes = kWRows * 64, kWScale = kWRows * 4;
-  static constexpr int kXBytes = XK == kFp4 ? TM * 64 : XK * (TM / 16) * kXFrag;
-  static constexpr int kXScale = XK == kFp4 ? (TM + 63) / 64 * 256 : 0;
-  static constexpr int kLds = kWBytes + kWScale + kXBytes + kXScale;
-  static_assert(kWRows * 4 % kThreads == 0 && kThreads == 256, "a step's blocks divide over 256 threads");
+  static constexpr int kXGroup = XK == kFp4 ? TM * 64 + 256 / KS : (TM / 16) * kXFrag;
+  static constexpr int kXSGroup = XK == kFp4 ? (TM + 63) / 64 * 256 : 0;
+  static constexpr int kTerms = XK == kFp4 ? 1 : XK;
+  static constexpr int kOffWS = KS * kWGroup, kOffX = kOffWS + KS * kWSGroup, kOffXS = kOffX + kTerms * KS * kXGroup;
+  static constexpr int kStage = kOffXS + KS * kXSGroup;
+  static constexpr int kRed = (WK - 1) * WN * WM * kMats * FN * FM * 1024;
+  static constexpr int kLds = NBUF * kStage > kRed ? NBUF * kStage : kRed;
+  static_assert(kThreads % kBlk == 0 && kWRows % kRowStep == 0, "a stage's blocks divide over the threads");
+  static_assert(kRowStep % 4 == 0, "so do its activations, and a thread's rows share their alignment");
+  static_assert(!PAIR || TN % kRowStep == 0, "a load's rows are of one matrix");
+  static_assert(KS % WK == 0 && kLds <= 160 * 1024, "");
 };
 
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM>
-__global__ void __launch_bounds__(256) mx_tile_kernel(const MxArgs a) {
-  using S = MxTile<XK, PAIR, FN, FM, WN, WM>;
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF>
+__global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs a) {
+  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>;
   constexpr int TN = S::TN, TM = S::TM, NW = S::NW, NX = S::NX;
   __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
-  uint8_t *lw = lds, *lws = lds + S::kWBytes, *lx = lws + S::kWScale, *lxs = lx + S::kXBytes;
 
   Tile tile;
   if (!find_tile<TM>(a, TN, &tile)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave % WN, wm = wave / WN;
+  const int wn = wave % WN, wm = wave / WN % WM, wk = wave / (WN * WM);
   const int i = lane & 15, g = lane >> 4;
-  const uint8_t *wbase = a.w + tile.expert * a.expert_bytes + (int64_t)tile.n0 * a.row_bytes;
-  const uint8_t *wbase2 = PAIR ? a.w2 + tile.expert * a.expert_bytes + (int64_t)tile.n0 * a.row_bytes : nullptr;
+  const int64_t first_row = tile.expert * a.expert_bytes + (int64_t)tile.n0 * a.row_bytes;
+  // (gate and up have the same alignment: both start at a 16-byte boundary plus the window)
+  const uint32_t w_odd = (uint32_t)(uintptr_t)(a.w + first_row) & 3u;
+  const uint8_t *wbase = a.w + first_row - w_odd;
+  const uint8_t *wbase2 = PAIR ? a.w2 + first_row - w_odd : nullptr;
   const int rows_left = a.n - tile.n0;
 
-  // This thread's blocks of a step: row (tid / 4 + 64 v) of the tile, block
-  // tid % 4.  Rows past the matrix read its last row; their sums are not stored.
+  // This thread's blocks of a stage: row tid / kBlk + kRowStep v of the tile,
+  // block tid % kBlk.  Rows past the matrix read its last row, tokens past the
+  // tile's end its first token; their sums are not stored.  A stage is a
+  // multiple of four blocks and of four rows a step, so a thread's blocks all
+  // start at the same byte of their first word.
+  const int wblk = tid % S::kBlk, wrow = tid / S::kBlk;
+  const uint32_t wfirst = wblk < a.nb ? 17u * (uint32_t)wblk : 0u;
+  const uint32_t wphase = (w_odd + (uint32_t)wrow * (uint32_t)a.row_bytes + wfirst) & 3u;
   uint32_t woff[NW];
 #pragma unroll
-  for (int v = 0; v < NW; ++v) {
-    const int row = (tid >> 2) + 64 * v;
-    woff[v] = (uint32_t)min(row % TN, rows_left - 1) * (uint32_t)a.row_bytes + 17u * (tid & 3);
-  }
-  // This thread's rows of x: null for places past the tile's end and sources
-  // x does not have, which count as zeros.
+  for (int v = 0; v < NW; ++v)
+    woff[v] = (w_odd + (uint32_t)min((wrow + S::kRowStep * v) % TN, rows_left - 1) * (uint32_t)a.row_bytes + wfirst) & ~3u;
+  // A piece of x: a block (MXFP4), or a quarter of one (floats).
+  const int xblk = XK == kFp4 ? wblk : (tid >> 2) % S::kBlk;
+  const int xtok = XK == kFp4 ? wrow : (tid >> 2) / S::kBlk;
   const uint8_t *xp[NX];
+  uint32_t xphase[NX];
+  // Tiles of few tokens leave out the loads and writes of the tokens past the
+  // end (stale LDS reaches only those tokens' sums); larger ones repeat the
+  // first token, since a branch there would part the matrix instructions.
+  constexpr bool kSkip = TM <= 32;
+  uint32_t there = 0;
 #pragma unroll
   for (int v = 0; v < NX; ++v) {
-    const int tok = XK == kFp4 ? (tid >> 2) + 64 * v : (tid >> 4) + 16 * v;
-    const int p = tile.m0 + tok;
-    xp[v] = nullptr;
-    if (tok < TM && p < tile.m_end) {
-      int src = p;
-      if (a.slots) {
-        const int s = a.slots[p];
-        src = s < 0 ? -1 : s / a.n_sel;
-      }
-      if (src >= 0 && src < a.x_rows) xp[v] = a.x + src * a.x_bytes;
+    const int tok = xtok + S::kTokStep * v;
+    const int p = tile.m0 + tok < tile.m_end ? tile.m0 + tok : tile.m0;
+    there |= (uint32_t)(tok < TM && tile.m0 + tok < tile.m_end) << v;
+    int src = p;
+    if (a.slots) {
+      const int s = a.slots[p];
+      src = s < 0 ? -1 : s / a.n_sel;
     }
+    if (src < 0 || src >= a.x_rows) src = 0;  // (its outputs are zeros: see the end)
+    const uint8_t *row = a.x + src * a.x_bytes;
+    if constexpr (XK == kFp4) {  // the first word of this thread's block, and its phase
+      row += wfirst;
+      xphase[v] = (uint32_t)(uintptr_t)row & 3u;
+      row -= xphase[v];
+    }
+    xp[v] = row;
   }
 
-  u32x4 wr[NW];
-  uint32_t wsr[NW];
-  u32x4 xr4[NX];
-  uint32_t xsr[NX];
-  XRaw<XK == kFp4 ? kBf16 : XK> xr[NX];
-  auto fetch = [&](int b0) {
-    const bool wok = b0 + (tid & 3) < a.nb;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) {
-      const uint8_t *base = (PAIR && 64 * v >= TN) ? wbase2 : wbase;  // 64 divides TN
-      wr[v] = u32x4{0, 0, 0, 0};
-      wsr[v] = 127;
-      if (wok) {
-        const uint8_t *p = base + (woff[v] + 17u * (uint32_t)b0);
-        __builtin_memcpy(&wr[v], p + 1, 16);
-        wsr[v] = p[0];
-      }
-    }
-    if constexpr (XK == kFp4) {
-#pragma unroll
-      for (int v = 0; v < NX; ++v) {
-        xr4[v] = u32x4{0, 0, 0, 0};
-        xsr[v] = 127;
-        if (wok && xp[v]) {
-          const uint8_t *p = xp[v] + 17u * (uint32_t)(b0 + (tid & 3));
-          __builtin_memcpy(&xr4[v], p + 1, 16);
-          xsr[v] = p[0];
-        }
-      }
+  // The blocks and pieces of x of the next stage, one by one: piece v < NW is
+  // a block of W, the others of x.  Blocks past the row's end are read from an
+  // earlier place and zeroed in LDS (TAIL: the row's last stage alone).
+  BlockRaw wr[NW], xr4[XK == kFp4 ? NX : 1];
+  constexpr int XF = XK == kFp4 ? kBf16 : XK;
+  XRaw<XF> xr[XK == kFp4 ? 1 : NX];
+  auto fetch = [&](auto piece, int b0) {
+    constexpr int v = decltype(piece)::value;
+    const uint32_t wb = b0 + wblk < a.nb ? 17u * (uint32_t)b0 : 0u;
+    if (kSkip && v >= NW && !(there >> (v < NW ? 0 : v - NW) & 1)) return;
+    if constexpr (v < NW) {
+      block_load(((PAIR && S::kRowStep * v >= TN) ? wbase2 : wbase) + (woff[v] + wb), wr[v]);
+    } else if constexpr (XK == kFp4) {
+      block_load(xp[v - NW] + wb, xr4[v - NW]);
     } else {
       constexpr int ES = XK == kF32 ? 4 : 2;
-      const int blk = (tid >> 2) & 3, q = tid & 3;
-      const bool ok = b0 + blk < a.nb;
-#pragma unroll
-      for (int v = 0; v < NX; ++v) {
-        xr[v] = {};
-        if (ok && xp[v]) {
-          const uint8_t *p = xp[v] + (uint32_t)ES * (32u * (uint32_t)(b0 + blk) + 4u * q);
-          __builtin_memcpy(&xr[v].lo, p, 4 * ES);
-          __builtin_memcpy(&xr[v].hi, p + 16 * ES, 4 * ES);
-        }
+      x_load<XF>(xp[v - NW] + ES * 32u * (uint32_t)min(b0 + xblk, a.nb - 1), xr[v - NW]);
+    }
+  };
+  uint8_t *const cw = lds + (wblk >> 2) * S::kWGroup + 16 * (wblk & 3) + 64 * wrow;
+  uint8_t *const cx =
+      XK == kFp4 ? lds + S::kOffX + (wblk >> 2) * S::kXGroup + 16 * (wblk & 3) + 64 * wrow
+                 : lds + S::kOffX + (xblk >> 2) * S::kXGroup + x_word<XK>(tid & 3) * S::kPlane + 16 * (xblk & 3);
+  uint8_t *const sw = lds + S::kOffWS + (wblk >> 2) * S::kWSGroup + 4 * (wblk & 3);
+  uint8_t *const sx = lds + S::kOffXS + (wblk >> 2) * S::kXSGroup + 4 * (wblk & 3);
+  auto stage = [&](auto piece, auto tail, int b0, int half) {
+    constexpr int v = decltype(piece)::value;
+    constexpr bool TAIL = decltype(tail)::value;
+    const int off = half * S::kStage;
+    if (kSkip && v >= NW && !(there >> (v < NW ? 0 : v - NW) & 1)) return;
+    if constexpr (v < NW || XK == kFp4) {
+      constexpr bool W = v < NW;
+      constexpr int j = W ? v : v - NW;
+      const int row = wrow + S::kRowStep * j;
+      if (!W && TM % S::kRowStep != 0 && row >= TM) return;
+      const BlockRaw &r = W ? wr[W ? j : 0] : xr4[W ? 0 : j];
+      const uint32_t phase = W ? wphase : xphase[W ? 0 : j];
+      u32x4 codes = block_codes(r, phase);
+      uint32_t scale = block_scale(r, phase);
+      if (TAIL && b0 + wblk >= a.nb) {
+        codes = u32x4{0, 0, 0, 0};
+        scale = 127;
       }
-    }
-  };
-  auto stage = [&]() {
-#pragma unroll
-    for (int v = 0; v < NW; ++v) {
-      *(u32x4 *)(lw + 16 * (tid + 256 * v)) = wr[v];
-      lws[256 * v + 4 * (tid & 63) + (tid >> 6)] = (uint8_t)wsr[v];
-    }
-    if constexpr (XK == kFp4) {
-#pragma unroll
-      for (int v = 0; v < NX; ++v)
-        if ((tid >> 2) + 64 * v < TM) {
-          *(u32x4 *)(lx + 16 * (tid + 256 * v)) = xr4[v];
-          lxs[256 * v + 4 * (tid & 63) + (tid >> 6)] = (uint8_t)xsr[v];
-        }
+      *(u32x4 *)((W ? cw : cx) + off + 64 * S::kRowStep * j) = codes;
+      ((W ? sw : sx) + off)[256 * (row >> 6) + 16 * (row & 15) + ((row >> 4) & 3)] = (uint8_t)scale;
     } else {
-      const int blk = (tid >> 2) & 3, q = tid & 3;
+      constexpr int j = v - NW;
+      const int tok = xtok + S::kTokStep * j;
+      if (TM % S::kTokStep != 0 && tok >= TM) return;
+      if (TAIL && b0 + xblk >= a.nb) xr[j] = {};
+      u32x4 t[XF];
+      x_terms<XF>(xr[j], t);
 #pragma unroll
-      for (int v = 0; v < NX; ++v)
-        if ((tid >> 4) + 16 * v < TM) {
-          u32x4 t[XK];
-          x_terms<XK>(xr[v], t);
-#pragma unroll
-          for (int k = 0; k < XK; ++k)
-            *(u32x4 *)(lx + (k * (TM / 16) + v) * S::kXFrag + q * S::kPlane + ((tid >> 4) * 4 + blk) * 16) = t[k];
-        }
+      for (int k = 0; k < XF; ++k)
+        *(u32x4 *)(cx + off + k * KS * S::kXGroup + (tok >> 4) * S::kXFrag + 64 * (tok & 15)) = t[k];
     }
   };
+  constexpr int P = NW + NX;
 
   f32x4 acc[S::kMats][FN][FM];
 #pragma unroll
@@ -394,67 +483,160 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(const MxArgs a) {
 #pragma unroll
       for (int m = 0; m < FM; ++m) acc[u][n][m] = f32x4{0, 0, 0, 0};
 
-  fetch(0);
-  for (int b0 = 0; b0 < a.nb; b0 += 4) {
-    stage();
-    __syncthreads();
-    if (b0 + 4 < a.nb) fetch(b0 + 4);
-    u32x4 wc[S::kMats][FN];
-    uint32_t ws[S::kMats][FN];
+  const int at = 16 * (4 * i + g);  // this lane's piece of a fragment
+  // One stage's products in kSlots parts, with between(part) after each: the
+  // loads and LDS writes of the stages to come are spread over them, since
+  // issued together they hold every wave while the matrix cores idle.
+  constexpr int kParts = XK == kFp4 ? FM : 4, kSlots = KS / WK * kParts;
+  auto multiply = [&](int half, auto between) {
+    const uint8_t *buf = lds + half * S::kStage;
+    each<KS / WK>([&](auto kk_) {
+      constexpr int kk = decltype(kk_)::value;
+      const int grp = wk + WK * kk;
+      u32x4 wc[S::kMats][FN];
+      uint32_t ws[S::kMats][FN];
 #pragma unroll
-    for (int u = 0; u < S::kMats; ++u)
+      for (int u = 0; u < S::kMats; ++u)
 #pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const int f = u * (TN / 16) + wn * FN + n;  // fragment of the tile
-        wc[u][n] = *(const u32x4 *)(lw + 1024 * f + 16 * (4 * i + g));
-        ws[u][n] = *(const uint32_t *)(lws + 256 * (f >> 2) + 4 * (4 * i + g)) >> (8 * (f & 3));
-      }
-    if constexpr (XK == kFp4) {
-#pragma unroll
-      for (int m = 0; m < FM; ++m) {
-        const int f = wm * FM + m;
-        const u32x4 xc = *(const u32x4 *)(lx + 1024 * f + 16 * (4 * i + g));
-        const uint32_t xs = *(const uint32_t *)(lxs + 256 * (f >> 2) + 4 * (4 * i + g)) >> (8 * (f & 3));
-        const i32x8 B = {(int)xc.x, (int)xc.y, (int)xc.z, (int)xc.w, 0, 0, 0, 0};
-#pragma unroll
-        for (int u = 0; u < S::kMats; ++u)
-#pragma unroll
-          for (int n = 0; n < FN; ++n) {
-            const i32x8 A = {(int)wc[u][n].x, (int)wc[u][n].y, (int)wc[u][n].z, (int)wc[u][n].w, 0, 0, 0, 0};
-            acc[u][n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc[u][n][m], 4, 4, 0,
-                                                                            (int)ws[u][n], 0, (int)xs);
-          }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8 xb[FM][XK];
+        for (int n = 0; n < FN; ++n) {
+          const int f = u * (TN / 16) + wn * FN + n;  // fragment of the tile
+          wc[u][n] = *(const u32x4 *)(buf + grp * S::kWGroup + 1024 * f + at);
+          ws[u][n] = *(const uint32_t *)(buf + S::kOffWS + grp * S::kWSGroup + 256 * (f >> 2) + (at >> 2)) >>
+                     (8 * (f & 3));
+        }
+      // x of this group (MXFP4), or of the part after the current one (floats),
+      // is read ahead of the LDS writes between the parts.
+      const uint8_t *bx = buf + S::kOffX + grp * S::kXGroup + at;
+      u32x4 xc[XK == kFp4 ? FM : 1];
+      uint32_t xs[XK == kFp4 ? FM : 1];
+      bf16x8 xb[2][XK == kFp4 ? 1 : FM][XF];
+      auto read_x = [&](auto part_) {
+        constexpr int part = decltype(part_)::value;
 #pragma unroll
         for (int m = 0; m < FM; ++m)
 #pragma unroll
-          for (int k = 0; k < XK; ++k)
-            xb[m][k] = *(const bf16x8 *)(lx + (k * (TM / 16) + wm * FM + m) * S::kXFrag + j * S::kPlane +
-                                         16 * (4 * i + g));
+          for (int k = 0; k < XF; ++k)
+            xb[part & 1][XK == kFp4 ? 0 : m][k] =
+                *(const bf16x8 *)(bx + k * KS * S::kXGroup + (wm * FM + m) * S::kXFrag + part * S::kPlane);
+      };
+      if constexpr (XK == kFp4) {
 #pragma unroll
-        for (int u = 0; u < S::kMats; ++u)
-#pragma unroll
-          for (int n = 0; n < FN; ++n) {
-            const bf16x8 A = weights8(wc[u][n][j], scale_of(ws[u][n], 0));
-#pragma unroll
-            for (int m = 0; m < FM; ++m)
-#pragma unroll
-              for (int k = 0; k < XK; ++k)
-                acc[u][n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, xb[m][k], acc[u][n][m], 0, 0, 0);
-          }
+        for (int m = 0; m < FM; ++m) {
+          const int f = wm * FM + m;
+          xc[m] = *(const u32x4 *)(bx + 1024 * f);
+          xs[m] =
+              *(const uint32_t *)(buf + S::kOffXS + grp * S::kXSGroup + 256 * (f >> 2) + (at >> 2)) >> (8 * (f & 3));
+        }
+      } else {
+        read_x(std::integral_constant<int, 0>());
       }
+      each<kParts>([&](auto part_) {
+        constexpr int part = decltype(part_)::value;
+        if constexpr (XK == kFp4) {
+          const i32x8 B = {(int)xc[part].x, (int)xc[part].y, (int)xc[part].z, (int)xc[part].w, 0, 0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < S::kMats; ++u)
+#pragma unroll
+            for (int n = 0; n < FN; ++n) {
+              const i32x8 A = {(int)wc[u][n].x, (int)wc[u][n].y, (int)wc[u][n].z, (int)wc[u][n].w, 0, 0, 0, 0};
+              acc[u][n][part] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc[u][n][part], 4, 4, 0,
+                                                                                 (int)ws[u][n], 0, (int)xs[part]);
+            }
+        } else {
+          if constexpr (part + 1 < kParts) read_x(std::integral_constant<int, part + 1>());
+#pragma unroll
+          for (int u = 0; u < S::kMats; ++u)
+#pragma unroll
+            for (int n = 0; n < FN; ++n) {
+              const bf16x8 A = weights8(wc[u][n][part], scale_of(ws[u][n], 0));
+#pragma unroll
+              for (int m = 0; m < FM; ++m)
+#pragma unroll
+                for (int k = 0; k < XF; ++k)
+                  acc[u][n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, xb[part & 1][m][k], acc[u][n][m], 0, 0, 0);
+            }
+        }
+        between(std::integral_constant<int, kk * kParts + part>());
+      });
+    });
+  };
+  // The pieces of one part: all P spread over the kSlots parts.
+  auto pieces = [&](auto slot, auto f) {
+    constexpr int s = decltype(slot)::value, p0 = s * P / kSlots, p1 = (s + 1) * P / kSlots;
+    each<p1 - p0>([&](auto q) { f(std::integral_constant<int, p0 + decltype(q)::value>()); });
+    __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory instructions may pass
+  };
+  const std::true_type last;
+  const std::false_type inner;
+
+  const int stages = (a.nb + S::kBlk - 1) / S::kBlk;
+  if (stages > 0) {
+    each<P>([&](auto p) { fetch(p, 0); });
+    int t = 0;
+    if constexpr (NBUF == 2) {
+      // stage t + 1 goes from registers to LDS, and t + 2 into the registers,
+      // while t is multiplied
+      each<P>([&](auto p) { stage(p, last, 0, 0); });
+      if (stages > 1) each<P>([&](auto p) { fetch(p, S::kBlk); });
+      __syncthreads();
+      for (; t + 2 < stages; ++t) {
+        multiply(t & 1, [&](auto slot) {
+          pieces(slot, [&](auto p) {
+            stage(p, inner, (t + 1) * S::kBlk, (t + 1) & 1);
+            fetch(p, (t + 2) * S::kBlk);
+          });
+        });
+        __syncthreads();
+      }
+      for (; t < stages; ++t) {
+        multiply(t & 1, [&](auto slot) {
+          if (t + 1 < stages) pieces(slot, [&](auto p) { stage(p, last, (t + 1) * S::kBlk, (t + 1) & 1); });
+        });
+        __syncthreads();
+      }
+    } else {
+      for (; t + 1 < stages; ++t) {
+        each<P>([&](auto p) { stage(p, inner, t * S::kBlk, 0); });
+        __syncthreads();
+        multiply(0, [&](auto slot) { pieces(slot, [&](auto p) { fetch(p, (t + 1) * S::kBlk); }); });
+        __syncthreads();
+      }
+      each<P>([&](auto p) { stage(p, last, t * S::kBlk, 0); });
+      __syncthreads();
+      multiply(0, [](auto) {});
+      if (WK > 1) __syncthreads();
     }
+  }
+
+  if constexpr (WK > 1) {
+    // the other waves' sums to the first of each tile part, added in their order
+    f32x4 *red = (f32x4 *)lds + (wm * WN + wn) * S::kMats * FN * FM * 64 + lane;
+    constexpr int kPart = WN * WM * S::kMats * FN * FM * 64;
+#pragma unroll
+    for (int u = 0; u < S::kMats; ++u)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+          if (wk > 0) red[(wk - 1) * kPart + ((u * FN + n) * FM + m) * 64] = acc[u][n][m];
     __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int u = 0; u < S::kMats; ++u)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+          for (int w = 0; w < WK - 1; ++w) acc[u][n][m] += red[w * kPart + ((u * FN + n) * FM + m) * 64];
   }
 
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
     const int p = tile.m0 + 16 * (wm * FM + m) + i;
     if (p >= tile.m_end) continue;
+    // a source that x does not have
+    const bool absent = a.slots && (uint32_t)(a.slots[p] < 0 ? -1 : a.slots[p] / a.n_sel) >= (uint32_t)a.x_rows;
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
       const int r = tile.n0 + 16 * (wn * FN + n) + 4 * g;
@@ -462,14 +644,15 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(const MxArgs a) {
       if constexpr (PAIR)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = silu_times(v[e], acc[1][n][m][e]);
+      if (absent) v = f32x4{0, 0, 0, 0};
       if (r < a.n) store4(a, p, r, a.n - r, v);
     }
   }
 }
 
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM>
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF>
 hipError_t launch_tile(MxArgs a, hipStream_t stream) {
-  using S = MxTile<XK, PAIR, FN, FM, WN, WM>;
+  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>;
   const int64_t tn = ((int64_t)a.n + S::TN - 1) / S::TN;
   // experts: a partial tile each beyond the whole ones, as far as places go
   const int64_t tm = a.offsets ? a.places / S::TM + (int64_t)(a.n_expert < a.places ? a.n_expert : a.places)
@@ -477,8 +660,8 @@ hipError_t launch_tile(MxArgs a, hipStream_t stream) {
   if (tn * tm > 0x7ffffff0) return hipErrorInvalidConfiguration;
   a.tiles_n = (int)tn;
   a.tiles = (int)(tn * tm);
-  hipLaunchKernelGGL((mx_tile_kernel<XK, PAIR, FN, FM, WN, WM>), dim3((unsigned)((tn * tm + 7) / 8 * 8)), dim3(256), 0,
-                     stream, a);
+  hipLaunchKernelGGL((mx_tile_kernel<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>),
+                     dim3((unsigned)((tn * tm + 7) / 8 * 8)), dim3(S::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

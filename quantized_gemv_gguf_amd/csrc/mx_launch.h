@@ -1,20 +1,98 @@
-// mx_launch.h -- which kernel of mx_gemm.h a product takes, by sizes and type.
+// mx_launch.h -- which kernel of mx_gemm.h a product takes.
 #pragma once
 
 #include "mx_gemm.h"
 
 namespace qgemv_mx {
 
-// Places an expert gets on average decide the tile.
+// A tile shape with its measured times, in 0.1 us at k = 4096: kOne, a grid of
+// at most one workgroup per compute unit; kMore, each further workgroup per
+// compute unit.  kWhole: one workgroup at a time fills a compute unit (LDS or
+// registers), so a grid takes whole rounds.
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, int kOne, int kMore, bool kWhole>
+struct Shape {
+  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>;
+
+  // Estimated time; tokens are taken as spread evenly over the experts, each
+  // adding half a partial tile.
+  static double cost(const MxArgs &a) {
+    const double active = a.offsets ? (a.n_expert < a.places ? a.n_expert : a.places) : 1;
+    const double each = a.places / active;
+    double tm = a.offsets ? (each + 0.5 * S::TM) / S::TM : (double)((a.places + S::TM - 1) / S::TM);
+    if (tm < 1.0) tm = 1.0;
+    double per_cu = active * tm * ((a.n + S::TN - 1) / S::TN) / 256.0;
+    if (kWhole) per_cu = (double)(int64_t)(per_cu + 0.999);
+    return (kOne + (per_cu > 1.0 ? (per_cu - 1.0) * kMore : 0.0)) * a.nb;
+  }
+  static hipError_t launch(const MxArgs &a, hipStream_t stream) {
+    return launch_tile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>(a, stream);
+  }
+};
+
+// The shape with the least estimated time.
+template <typename... Shapes>
+hipError_t launch_cheapest(const MxArgs &a, hipStream_t stream) {
+  const double costs[] = {Shapes::cost(a)...};
+  hipError_t (*const launches[])(const MxArgs &, hipStream_t) = {Shapes::launch...};
+  int best = 0;
+  for (int i = 1; i < (int)sizeof...(Shapes); ++i)
+    if (costs[i] < costs[best]) best = i;
+  return launches[best](a, stream);
+}
+
+template <int XK, bool PAIR> struct Shapes;
+
+template <> struct Shapes<kFp4, false> {
+  static constexpr auto run = launch_cheapest<Shape<kFp4, false, 2, 1, 1, 1, 4, 4, 2, 52, 19, false>,
+                                              Shape<kFp4, false, 2, 2, 1, 1, 4, 4, 2, 68, 28, false>,
+                                              Shape<kFp4, false, 2, 4, 2, 1, 2, 4, 1, 115, 66, false>,
+                                              Shape<kFp4, false, 4, 4, 4, 2, 1, 2, 2, 260, 330, true>,
+                                              Shape<kFp4, false, 4, 8, 4, 2, 1, 1, 2, 450, 450, true>>;
+};
+template <> struct Shapes<kFp4, true> {
+  static constexpr auto run = launch_cheapest<Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 23, false>,
+                                              Shape<kFp4, true, 1, 4, 2, 1, 2, 4, 1, 115, 56, false>,
+                                              Shape<kFp4, true, 1, 4, 4, 1, 1, 2, 1, 175, 105, false>,
+                                              Shape<kFp4, true, 2, 4, 4, 2, 1, 2, 2, 260, 300, true>>;
+};
+template <> struct Shapes<kBf16, false> {
+  static constexpr auto run = launch_cheapest<Shape<kBf16, false, 2, 1, 1, 1, 8, 8, 2, 72, 62, true>,
+                                              Shape<kBf16, false, 2, 2, 4, 1, 1, 2, 1, 210, 130, false>,
+                                              Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 300, true>,
+                                              Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 630, 630, true>>;
+};
+template <> struct Shapes<kBf16, true> {
+  static constexpr auto run = launch_cheapest<Shape<kBf16, true, 1, 1, 1, 1, 4, 4, 1, 75, 40, false>,
+                                              Shape<kBf16, true, 1, 2, 4, 1, 1, 2, 1, 200, 120, false>,
+                                              Shape<kBf16, true, 2, 4, 4, 2, 1, 1, 2, 530, 530, true>,
+                                              Shape<kBf16, true, 4, 3, 2, 4, 1, 1, 2, 720, 720, true>>;
+};
+template <> struct Shapes<kF16, false> {
+  static constexpr auto run = launch_cheapest<Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 95, 90, true>,
+                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 250, 200, false>,
+                                              Shape<kF16, false, 4, 4, 8, 1, 1, 1, 1, 1000, 1000, true>>;
+};
+template <> struct Shapes<kF16, true> {
+  static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 100, 60, false>,
+                                              Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 240, 180, false>,
+                                              Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
+};
+template <> struct Shapes<kF32, false> {
+  static constexpr auto run = launch_cheapest<Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 105, 115, true>,
+                                              Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 160, false>,
+                                              Shape<kF32, false, 4, 2, 4, 2, 1, 1, 2, 850, 850, true>,
+                                              Shape<kF32, false, 4, 4, 8, 1, 1, 1, 1, 1350, 1550, true>>;
+};
+template <> struct Shapes<kF32, true> {
+  static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 80, false>,
+                                              Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 260, 152, false>,
+                                              Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 410, 247, false>,
+                                              Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>>;
+};
+
 template <int XK>
 hipError_t launch_mx(const MxArgs &a, hipStream_t stream) {
-  const int64_t avg = a.offsets ? (a.places + a.n_expert - 1) / a.n_expert : a.places;
-  if (a.w2) {
-    if (avg <= 16) return launch_tile<XK, true, 1, 1, 4, 1>(a, stream);
-    return launch_tile<XK, true, 2, 4, 4, 1>(a, stream);
-  }
-  if (avg <= 16) return launch_tile<XK, false, 2, 1, 4, 1>(a, stream);
-  return launch_tile<XK, false, 2, 4, 4, 1>(a, stream);
+  return a.w2 ? Shapes<XK, true>::run(a, stream) : Shapes<XK, false>::run(a, stream);
 }
 
 }  // namespace qgemv_mx

@@ -38,6 +38,8 @@ template <> struct Elem<QG_BF16> {
   __device__ static inline Raw from(float v) { return (__bf16)v; }
 };
 
+typedef u32x4 __attribute__((aligned(2))) u32x4_2;  // 16 bytes at any element
+
 // N values from / to any element-aligned address, as one access of N elements.
 template <int T, int N>
 __device__ __forceinline__ void load_n(const void *p, float (&v)[N]) {
@@ -146,39 +148,58 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *w, int n
 // Workgroup e < n_expert places the slots of expert e: its first pass counts
 // the ids below e (the expert's offset) and equal to e per wave, its second
 // writes each slot's place, in slot order (a lane's four ids, then the lanes,
-// then the waves).  Workgroup n_expert does the same for the dropped slots:
-// pos -1, and slots -1 behind the last kept one.  No atomics, no workspace,
-// one launch; every workgroup reads all ids from L2.
-constexpr int kSortWaves = 16;
+// then the groups of 256, then the waves).  Workgroup n_expert does the same
+// for the dropped slots: pos -1, and slots -1 behind the last kept one.  No
+// atomics, no workspace, one launch; every workgroup reads all ids from L2,
+// eight groups of 256 at a time so that their loads overlap (kept in registers
+// between the passes where a wave has no more).  32768 slots of 128 experts:
+// 7 us, 14 with the loads one by one.
+constexpr int kSortWaves = 16, kSortGroups = 8;
 __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(const int32_t *ids, int n, int n_expert,
                                                                int32_t *offsets, int32_t *slots, int32_t *pos) {
   __shared__ int below[kSortWaves], equal[kSortWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = blockIdx.x;
-  const bool rest = e == n_expert;
-  // whole groups of 256 ids per wave
   const int groups = (n + 255) / 256, per = (groups + kSortWaves - 1) / kSortWaves;
   const int g0 = min(wave * per, groups), g1 = min(g0 + per, groups);
-  auto load4 = [&](int g, int (&v)[4]) {
-    const int at = 256 * g + 4 * lane;
-    if (at + 4 <= n) {
-      __builtin_memcpy(v, ids + at, 16);
-    } else {
+  int v[kSortGroups][4];
+  auto load = [&](int g) {  // groups g .. g + 7 of the wave; ids past the end are no expert's
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = at + k < n ? ids[at + k] : 0x7fffffff;
+    for (int j = 0; j < kSortGroups; ++j) {
+      const int at = 256 * (g + j) + 4 * lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[j][k] = 0x7fffffff;
+      if (g + j >= g1) continue;
+      if (at + 4 <= n) {
+        __builtin_memcpy(v[j], ids + at, 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at + k < n) v[j][k] = ids[at + k];
+      }
     }
   };
-  auto mine = [&](int id) { return rest ? (id < 0 || id >= n_expert) : id == e; };
-  int nb = 0, ne = 0;
-  for (int g = g0; g < g1; ++g) {
-    int v[4];
-    load4(g, v);
+  // sums of counts up to 32 over the lanes, bit by bit
+  auto lanes_sum = [](int c) {
+    int sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      nb += __popcll(__ballot(v[k] >= 0 && v[k] < e));
-      ne += __popcll(__ballot(mine(v[k])));
-    }
+    for (int b = 0; b < 6; ++b) sum += __popcll(__ballot(c >> b & 1)) << b;
+    return sum;
+  };
+  int nb = 0, ne = 0;
+  for (int g = g0; g < g1; g += kSortGroups) {
+    load(g);
+    int cb = 0, ce = 0;
+#pragma unroll
+    for (int j = 0; j < kSortGroups; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        cb += (uint32_t)v[j][k] < (uint32_t)e;
+        ce += v[j][k] == e;
+      }
+    nb += lanes_sum(cb);
+    ne += lanes_sum(ce);
   }
   if (lane == 0) {
     below[wave] = nb;
@@ -186,46 +207,52 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(const int32_t *id
   }
   __syncthreads();
   int base = 0, before = 0;
+#pragma unroll
   for (int w = 0; w < kSortWaves; ++w) {
     base += below[w];
     if (w < wave) before += equal[w];
   }
   if (threadIdx.x == 0) offsets[e] = base;
-  if (rest) {
-    for (int p = base + threadIdx.x; p < n; p += 64 * kSortWaves) slots[p] = -1;
+  if (e == n_expert) {
+    for (int p = base + (int)threadIdx.x; p < n; p += 64 * kSortWaves) slots[p] = -1;
+    for (int i = (int)threadIdx.x; i < n; i += 64 * kSortWaves)
+      if ((uint32_t)ids[i] >= (uint32_t)n_expert) pos[i] = -1;
+    return;
   }
+  if (ne == 0) return;
   int at = base + before;
   const uint64_t lower = (1ull << lane) - 1;
-  for (int g = g0; g < g1; ++g) {
-    int v[4];
-    load4(g, v);
-    int rank = 0, all = 0;
-    bool m[4];
+  for (int g = g0; g < g1; g += kSortGroups) {
+    if (g1 - g0 > kSortGroups) load(g);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      m[k] = mine(v[k]) && 256 * g + 4 * lane + k < n;
-      const uint64_t b = __ballot(m[k]);
-      rank += __popcll(b & lower);
-      all += __popcll(b);
-    }
+    for (int j = 0; j < kSortGroups; ++j) {
+      uint64_t b[4], any = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!m[k]) continue;
-      const int slot = 256 * g + 4 * lane + k;
-      if (rest) {
-        pos[slot] = -1;
-      } else {
-        slots[at + rank] = slot;
-        pos[slot] = at + rank;
+      for (int k = 0; k < 4; ++k) any |= b[k] = __ballot(v[j][k] == e);
+      if (!any) continue;
+      int rank = at;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        rank += __popcll(b[k] & lower);
+        at += __popcll(b[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (v[j][k] != e) continue;
+        const int slot = 256 * (g + j) + 4 * lane + k;
+        slots[rank] = slot;
+        pos[slot] = rank;
         ++rank;
       }
     }
-    at += all;
   }
 }
 
 // A wave copies one row at a time, 16 bytes per lane, then the row's last bytes
-// by elements of 2.
+// by elements of 2.  Past: more rows than the caches hold with what the next
+// kernels read are written past them (32768 rows of 5760 bytes: 54 us either
+// way, and the weighted sum of as many rows behind it 38 us instead of 62).
+template <bool kPast>
 __global__ void __launch_bounds__(256) gather_kernel(const uint8_t *x, int64_t x_bytes, int64_t x_rows, int64_t row,
                                                      const int32_t *slots, int n_sel, int64_t n, uint8_t *out,
                                                      int64_t out_bytes) {
@@ -238,59 +265,65 @@ __global__ void __launch_bounds__(256) gather_kernel(const uint8_t *x, int64_t x
     uint8_t *dst = out + p * out_bytes;
     const int64_t whole = row & ~15ll;
     for (int64_t o = 16 * lane; o < whole; o += 1024) {
-      u32x4 v;
-      __builtin_memcpy(&v, src + o, 16);
-      __builtin_memcpy(dst + o, &v, 16);
+      const u32x4 v = *(const u32x4_2 *)(src + o);
+      if (kPast) __builtin_nontemporal_store(v, (u32x4_2 *)(dst + o));
+      else *(u32x4_2 *)(dst + o) = v;
     }
-    for (int64_t o = whole + 2 * lane; o < row; o += 128) {
-      uint16_t v;
-      __builtin_memcpy(&v, src + o, 2);
-      __builtin_memcpy(dst + o, &v, 2);
-    }
+    for (int64_t o = whole + 2 * lane; o < row; o += 128) *(uint16_t *)(dst + o) = *(const uint16_t *)(src + o);
   }
 }
 
-// Columns of one token, kCols at a time per lane: the places' rows are added
-// one after the other in s order.
+// A wave takes 64 kCols columns of one token.  The places and weights of four
+// choices are wave-uniform; their rows are loaded together, then added one
+// after the other in s order.  8192 tokens of four bf16 rows of 2880: 48 us
+// (4.9 TB/s), 67 with the rows loaded one by one.
 constexpr int kCols = 8;
 template <int TY, int TO>
 __global__ void __launch_bounds__(256) combine_kernel(const uint8_t *y, int64_t y_stride, int64_t y_rows,
                                                       const int32_t *pos, const float *w, int n_sel, int64_t n_cols,
-                                                      uint8_t *out, int64_t out_stride) {
-  constexpr int EY = Elem<TY>::kSize, EO = Elem<TO>::kSize;
-  const int64_t t = blockIdx.x;
+                                                      uint8_t *out, int64_t out_stride, int64_t n_tok,
+                                                      int waves_per_token) {
+  constexpr int EY = Elem<TY>::kSize, EO = Elem<TO>::kSize, kAt = 4;
+  const int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = task / waves_per_token;
+  const int64_t col = ((task - t * waves_per_token) * 64 + (threadIdx.x & 63)) * kCols;
+  if (t >= n_tok || col >= n_cols) return;
   pos += t * n_sel;
-  const int64_t groups = (n_cols + kCols - 1) / kCols;
-  for (int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x; c < groups; c += (int64_t)gridDim.y * 256) {
-    const int64_t col = kCols * c;
-    float acc[kCols];
+  float acc[kCols];
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
-    const bool whole = col + kCols <= n_cols;
-    for (int s = 0; s < n_sel; ++s) {
-      const int64_t p = pos[s];
-      if (p < 0 || p >= y_rows) continue;
-      const float ws = w ? w[t * n_sel + s] : 1.0f;
+  for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+  const bool whole = col + kCols <= n_cols;
+  for (int s0 = 0; s0 < n_sel; s0 += kAt) {
+    bool there[kAt];
+    float ws[kAt], v[kAt][kCols];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int p = s0 + j < n_sel ? __builtin_amdgcn_readfirstlane(pos[s0 + j]) : -1;
+      there[j] = p >= 0 && p < y_rows;
+      if (!there[j]) continue;
+      ws[j] = w ? w[t * n_sel + s0 + j] : 1.0f;
       const uint8_t *src = y + (p * y_stride + col) * EY;
-      float v[kCols];
-      if (whole) load_n<TY>(src, v);
+      if (whole) load_n<TY>(src, v[j]);
       else
         for (int k = 0; k < kCols; ++k) {
           float o[1] = {0.0f};
           if (col + k < n_cols) load_n<TY>(src + k * EY, o);
-          v[k] = o[0];
+          v[j][k] = o[0];
         }
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) acc[k] = fmaf(ws, v[k], acc[k]);
     }
-    uint8_t *dst = out + (t * out_stride + col) * EO;
-    if (whole) store_n<TO>(dst, acc);
-    else
-      for (int k = 0; k < kCols; ++k) {
-        const float o[1] = {acc[k]};
-        if (col + k < n_cols) store_n<TO>(dst + k * EO, o);
-      }
+#pragma unroll
+    for (int j = 0; j < kAt; ++j)
+      if (there[j])
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = fmaf(ws[j], v[j][k], acc[k]);
   }
+  uint8_t *dst = out + (t * out_stride + col) * EO;
+  if (whole) store_n<TO>(dst, acc);
+  else
+    for (int k = 0; k < kCols; ++k) {
+      const float o[1] = {acc[k]};
+      if (col + k < n_cols) store_n<TO>(dst + k * EO, o);
+    }
 }
 
 // One workgroup per (token, choice): dy's row and the dot product, summed by
@@ -560,8 +593,10 @@ int qgemv_expert_gather(const qg_tensor *x, const int32_t *slots, int32_t n_sel,
   if (!slots) return QG_E_NULL;
   const int es = elem_size(x->type);
   const unsigned grid = (unsigned)std::min<int64_t>((out->n_rows + 3) / 4, 1 << 20);
-  hipLaunchKernelGGL(gather_kernel, dim3(grid), dim3(256), 0, stream, (const uint8_t *)x->data, x->stride * es,
-                     x->n_rows, x->n_cols * es, slots, n_sel, out->n_rows, (uint8_t *)out->data, out->stride * es);
+  // (the memory-side cache holds 256 MB)
+  const auto kernel = out->n_rows * out->n_cols * es > (64ll << 20) ? gather_kernel<true> : gather_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, (const uint8_t *)x->data, x->stride * es, x->n_rows,
+                     x->n_cols * es, slots, n_sel, out->n_rows, (uint8_t *)out->data, out->stride * es);
   MX_HIP(hipGetLastError());
   return QG_OK;
 }
@@ -574,13 +609,13 @@ int qgemv_expert_combine(const qg_tensor *y, const int32_t *pos, const float *w,
   if (n_sel < 0) return QG_E_ARG;
   if (out->n_rows == 0 || out->n_cols == 0) return QG_OK;
   if (n_sel > 0 && !pos) return QG_E_NULL;
-  const int64_t groups = (out->n_cols + kCols - 1) / kCols;
-  const dim3 grid((unsigned)out->n_rows, (unsigned)std::min<int64_t>((groups + 255) / 256, 64));
+  const int64_t waves = (out->n_cols + 64 * kCols - 1) / (64 * kCols), grid = (out->n_rows * waves + 3) / 4;
+  if (grid > kMaxDim) return QG_E_SHAPE;
   with_type(y->type, [&](auto TY) {
     with_type(out->type, [&](auto TO) {
-      hipLaunchKernelGGL((combine_kernel<decltype(TY)::value, decltype(TO)::value>), grid, dim3(256), 0, stream,
-                         (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel, out->n_cols,
-                         (uint8_t *)out->data, out->stride);
+      hipLaunchKernelGGL((combine_kernel<decltype(TY)::value, decltype(TO)::value>), dim3((unsigned)grid), dim3(256),
+                         0, stream, (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel, out->n_cols,
+                         (uint8_t *)out->data, out->stride, out->n_rows, (int)waves);
     });
   });
   MX_HIP(hipGetLastError());

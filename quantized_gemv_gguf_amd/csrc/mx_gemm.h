@@ -322,15 +322,21 @@ __device__ __forceinline__ void each(F f) {
 // added in order through LDS at the end.  A stage is KS such groups: the next
 // stage's blocks and activations are loaded into registers while the current
 // one, in LDS, is multiplied.  NBUF = 2: two stages in LDS, one barrier each.
+// COLS: the bf16 terms of a few tokens lie in matrix columns of their own (five
+// fp32 tokens, or eight fp16, in 16 columns) and are added at the end: a single
+// token costs one matrix instruction, not one per term.
 // LDS: codes [group][row][block], 16 bytes each, so a wave's fragment of 16
 // rows is 1 KB read without conflicts; scale bytes of four fragments of 16
 // rows in one word; float x as [term][group][fragment][word j][token][block],
 // the planes of words 64 bytes apart beyond their 1 KB so that a token's
 // sixteen pieces are written to sixteen bank groups.
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF>
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS = false>
 struct MxTile {
   static constexpr int kThreads = 64 * WN * WM * WK;
-  static constexpr int TN = 16 * FN * WN, TM = 16 * FM * WM;
+  static constexpr int TN = 16 * FN * WN;
+  static constexpr int kTerms = XK == kFp4 || COLS ? 1 : XK;   // of x in one matrix column
+  static constexpr int kCols = COLS ? XK : 1;                  // matrix columns of one token
+  static constexpr int TM = 16 * FM * WM / kCols;              // tokens
   static constexpr int kMats = PAIR ? 2 : 1;
   static constexpr int kWRows = TN * kMats;
   static constexpr int kBlk = 4 * KS;                          // blocks of a row per stage
@@ -342,9 +348,8 @@ struct MxTile {
   static constexpr int kWSGroup = (kWRows + 63) / 64 * 256;    // its scales
   static constexpr int kPlane = 1024 + 64;                     // one word of 16 tokens, padded
   static constexpr int kXFrag = 4 * kPlane;
-  static constexpr int kXGroup = XK == kFp4 ? TM * 64 + 256 / KS : (TM / 16) * kXFrag;
+  static constexpr int kXGroup = XK == kFp4 ? TM * 64 + 256 / KS : FM * WM * kXFrag;
   static constexpr int kXSGroup = XK == kFp4 ? (TM + 63) / 64 * 256 : 0;
-  static constexpr int kTerms = XK == kFp4 ? 1 : XK;
   static constexpr int kOffWS = KS * kWGroup, kOffX = kOffWS + KS * kWSGroup, kOffXS = kOffX + kTerms * KS * kXGroup;
   static constexpr int kStage = kOffXS + KS * kXSGroup;
   static constexpr int kRed = (WK - 1) * WN * WM * kMats * FN * FM * 1024;
@@ -353,11 +358,12 @@ struct MxTile {
   static_assert(kRowStep % 4 == 0, "so do its activations, and a thread's rows share their alignment");
   static_assert(!PAIR || TN % kRowStep == 0, "a load's rows are of one matrix");
   static_assert(KS % WK == 0 && kLds <= 160 * 1024, "");
+  static_assert(!COLS || (XK >= kF16 && FM == 1 && WM == 1), "columns of one fragment");
 };
 
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF>
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS>
 __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs a) {
-  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>;
+  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>;
   constexpr int TN = S::TN, TM = S::TM, NW = S::NW, NX = S::NX;
   __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
 
@@ -469,8 +475,10 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
       u32x4 t[XF];
       x_terms<XF>(xr[j], t);
 #pragma unroll
-      for (int k = 0; k < XF; ++k)
-        *(u32x4 *)(cx + off + k * KS * S::kXGroup + (tok >> 4) * S::kXFrag + 64 * (tok & 15)) = t[k];
+      for (int k = 0; k < XF; ++k) {
+        const int col = COLS ? XF * tok + k : tok;
+        *(u32x4 *)(cx + off + (COLS ? 0 : k * KS * S::kXGroup) + (col >> 4) * S::kXFrag + 64 * (col & 15)) = t[k];
+      }
     }
   };
   constexpr int P = NW + NX;
@@ -504,46 +512,44 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
           ws[u][n] = *(const uint32_t *)(buf + S::kOffWS + grp * S::kWSGroup + 256 * (f >> 2) + (at >> 2)) >>
                      (8 * (f & 3));
         }
-      // x of this group (MXFP4), or of the part after the current one (floats),
-      // is read ahead of the LDS writes between the parts.
+      // x of the part after the current one is read ahead of the LDS writes
+      // between the parts.
       const uint8_t *bx = buf + S::kOffX + grp * S::kXGroup + at;
-      u32x4 xc[XK == kFp4 ? FM : 1];
-      uint32_t xs[XK == kFp4 ? FM : 1];
-      bf16x8 xb[2][XK == kFp4 ? 1 : FM][XF];
+      u32x4 xc[2];
+      uint32_t xs[2];
+      bf16x8 xb[2][XK == kFp4 ? 1 : FM][S::kTerms];
       auto read_x = [&](auto part_) {
         constexpr int part = decltype(part_)::value;
-#pragma unroll
-        for (int m = 0; m < FM; ++m)
-#pragma unroll
-          for (int k = 0; k < XF; ++k)
-            xb[part & 1][XK == kFp4 ? 0 : m][k] =
-                *(const bf16x8 *)(bx + k * KS * S::kXGroup + (wm * FM + m) * S::kXFrag + part * S::kPlane);
-      };
-      if constexpr (XK == kFp4) {
-#pragma unroll
-        for (int m = 0; m < FM; ++m) {
-          const int f = wm * FM + m;
-          xc[m] = *(const u32x4 *)(bx + 1024 * f);
-          xs[m] =
+        if constexpr (XK == kFp4) {
+          const int f = wm * FM + part;
+          xc[part & 1] = *(const u32x4 *)(bx + 1024 * f);
+          xs[part & 1] =
               *(const uint32_t *)(buf + S::kOffXS + grp * S::kXSGroup + 256 * (f >> 2) + (at >> 2)) >> (8 * (f & 3));
+        } else {
+#pragma unroll
+          for (int m = 0; m < FM; ++m)
+#pragma unroll
+            for (int k = 0; k < S::kTerms; ++k)
+              xb[part & 1][XK == kFp4 ? 0 : m][k] =
+                  *(const bf16x8 *)(bx + k * KS * S::kXGroup + (wm * FM + m) * S::kXFrag + part * S::kPlane);
         }
-      } else {
-        read_x(std::integral_constant<int, 0>());
-      }
+      };
+      read_x(std::integral_constant<int, 0>());
       each<kParts>([&](auto part_) {
         constexpr int part = decltype(part_)::value;
+        if constexpr (part + 1 < kParts) read_x(std::integral_constant<int, part + 1>());
         if constexpr (XK == kFp4) {
-          const i32x8 B = {(int)xc[part].x, (int)xc[part].y, (int)xc[part].z, (int)xc[part].w, 0, 0, 0, 0};
+          const u32x4 c = xc[part & 1];
+          const i32x8 B = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
 #pragma unroll
           for (int u = 0; u < S::kMats; ++u)
 #pragma unroll
             for (int n = 0; n < FN; ++n) {
               const i32x8 A = {(int)wc[u][n].x, (int)wc[u][n].y, (int)wc[u][n].z, (int)wc[u][n].w, 0, 0, 0, 0};
               acc[u][n][part] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc[u][n][part], 4, 4, 0,
-                                                                                 (int)ws[u][n], 0, (int)xs[part]);
+                                                                                 (int)ws[u][n], 0, (int)xs[part & 1]);
             }
         } else {
-          if constexpr (part + 1 < kParts) read_x(std::integral_constant<int, part + 1>());
 #pragma unroll
           for (int u = 0; u < S::kMats; ++u)
 #pragma unroll
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
 #pragma unroll
               for (int m = 0; m < FM; ++m)
 #pragma unroll
-                for (int k = 0; k < XF; ++k)
+                for (int k = 0; k < S::kTerms; ++k)
                   acc[u][n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, xb[part & 1][m][k], acc[u][n][m], 0, 0, 0);
             }
         }
@@ -564,7 +570,6 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
   auto pieces = [&](auto slot, auto f) {
     constexpr int s = decltype(slot)::value, p0 = s * P / kSlots, p1 = (s + 1) * P / kSlots;
     each<p1 - p0>([&](auto q) { f(std::integral_constant<int, p0 + decltype(q)::value>()); });
-    __builtin_amdgcn_sched_barrier(0x38f);  // everything but global memory instructions may pass
   };
   const std::true_type last;
   const std::false_type inner;
@@ -631,10 +636,24 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
           for (int w = 0; w < WK - 1; ++w) acc[u][n][m] += red[w * kPart + ((u * FN + n) * FM + m) * 64];
   }
 
+  if constexpr (COLS) {
+    // a token's columns to its first one, the largest term first
+#pragma unroll
+    for (int u = 0; u < S::kMats; ++u)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = acc[u][n][0][e];
+          float sum = v + __shfl_down(v, 1);
+          if constexpr (S::kCols == 3) sum += __shfl_down(v, 2);
+          acc[u][n][0][e] = sum;
+        }
+  }
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
-    const int p = tile.m0 + 16 * (wm * FM + m) + i;
-    if (p >= tile.m_end) continue;
+    const int p = tile.m0 + (COLS ? i / S::kCols : 16 * (wm * FM + m) + i);
+    if (p >= tile.m_end || (COLS && (i % S::kCols != 0 || i / S::kCols >= TM))) continue;
     // a source that x does not have
     const bool absent = a.slots && (uint32_t)(a.slots[p] < 0 ? -1 : a.slots[p] / a.n_sel) >= (uint32_t)a.x_rows;
 #pragma unroll
@@ -650,9 +669,9 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
   }
 }
 
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF>
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS = false>
 hipError_t launch_tile(MxArgs a, hipStream_t stream) {
-  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>;
+  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>;
   const int64_t tn = ((int64_t)a.n + S::TN - 1) / S::TN;
   // experts: a partial tile each beyond the whole ones, as far as places go
   const int64_t tm = a.offsets ? a.places / S::TM + (int64_t)(a.n_expert < a.places ? a.n_expert : a.places)
@@ -660,7 +679,7 @@ hipError_t launch_tile(MxArgs a, hipStream_t stream) {
   if (tn * tm > 0x7ffffff0) return hipErrorInvalidConfiguration;
   a.tiles_n = (int)tn;
   a.tiles = (int)(tn * tm);
-  hipLaunchKernelGGL((mx_tile_kernel<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>),
+  hipLaunchKernelGGL((mx_tile_kernel<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>),
                      dim3((unsigned)((tn * tm + 7) / 8 * 8)), dim3(S::kThreads), 0, stream, a);
   return hipGetLastError();
 }

@@ -9,9 +9,10 @@ namespace qgemv_mx {
 // at most one workgroup per compute unit; kMore, each further workgroup per
 // compute unit.  kWhole: one workgroup at a time fills a compute unit (LDS or
 // registers), so a grid takes whole rounds.
-template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, int kOne, int kMore, bool kWhole>
+template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, int kOne, int kMore, bool kWhole,
+          bool COLS = false>
 struct Shape {
-  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>;
+  using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>;
 
   // Estimated time; tokens are taken as spread evenly over the experts, each
   // adding half a partial tile.
@@ -25,7 +26,7 @@ struct Shape {
     return (kOne + (per_cu > 1.0 ? (per_cu - 1.0) * kMore : 0.0)) * a.nb;
   }
   static hipError_t launch(const MxArgs &a, hipStream_t stream) {
-    return launch_tile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF>(a, stream);
+    return launch_tile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>(a, stream);
   }
 };
 
@@ -68,23 +69,29 @@ template <> struct Shapes<kBf16, true> {
                                               Shape<kBf16, true, 4, 3, 2, 4, 1, 1, 2, 720, 720, true>>;
 };
 template <> struct Shapes<kF16, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 95, 90, true>,
-                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 250, 200, false>,
+  static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 2, 42, 42, true, true>,
+                                              Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 48, true, true>,
+                                              Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 95, 90, true>,
+                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 250, 170, false>,
                                               Shape<kF16, false, 4, 4, 8, 1, 1, 1, 1, 1000, 1000, true>>;
 };
 template <> struct Shapes<kF16, true> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 100, 60, false>,
+  static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 80, 33, false, true>,
+                                              Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 100, 60, false>,
                                               Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 240, 180, false>,
                                               Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
 };
 template <> struct Shapes<kF32, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 105, 115, true>,
-                                              Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 160, false>,
+  static constexpr auto run = launch_cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 2, 42, 42, true, true>,
+                                              Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 55, 40, true, true>,
+                                              Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 97, 115, true>,
+                                              Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 145, false>,
                                               Shape<kF32, false, 4, 2, 4, 2, 1, 1, 2, 850, 850, true>,
                                               Shape<kF32, false, 4, 4, 8, 1, 1, 1, 1, 1350, 1550, true>>;
 };
 template <> struct Shapes<kF32, true> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 80, false>,
+  static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
+                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 80, false>,
                                               Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 260, 152, false>,
                                               Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 410, 247, false>,
                                               Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>>;

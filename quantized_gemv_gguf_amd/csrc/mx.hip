@@ -248,45 +248,45 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(const int32_t *id
   }
 }
 
-// A wave copies one row at a time, 16 bytes per lane, then the row's last bytes
-// by elements of 2.  Past: more rows than the caches hold with what the next
+// `lanes` lanes (a power of two, up to a wave) copy one row at a time, 16 bytes
+// each, then the row's last bytes by elements of 2.  Past: more rows than the caches hold with what the next
 // kernels read are written past them (32768 rows of 5760 bytes: 54 us either
 // way, and the weighted sum of as many rows behind it 38 us instead of 62).
 template <bool kPast>
 __global__ void __launch_bounds__(256) gather_kernel(const uint8_t *x, int64_t x_bytes, int64_t x_rows, int64_t row,
                                                      const int32_t *slots, int n_sel, int64_t n, uint8_t *out,
-                                                     int64_t out_bytes) {
-  const int lane = threadIdx.x & 63;
-  const int64_t waves = (int64_t)gridDim.x * 4;
-  for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < n; p += waves) {
+                                                     int64_t out_bytes, int lanes) {
+  const int lane = threadIdx.x & (lanes - 1), per_group = 256 / lanes;
+  const int64_t step = (int64_t)gridDim.x * per_group;
+  for (int64_t p = (int64_t)blockIdx.x * per_group + threadIdx.x / (unsigned)lanes; p < n; p += step) {
     const int s = slots[p];
     if (s < 0 || s / n_sel >= x_rows) continue;
     const uint8_t *src = x + (int64_t)(s / n_sel) * x_bytes;
     uint8_t *dst = out + p * out_bytes;
     const int64_t whole = row & ~15ll;
-    for (int64_t o = 16 * lane; o < whole; o += 1024) {
+    for (int64_t o = 16 * lane; o < whole; o += 16 * lanes) {
       const u32x4 v = *(const u32x4_2 *)(src + o);
       if (kPast) __builtin_nontemporal_store(v, (u32x4_2 *)(dst + o));
       else *(u32x4_2 *)(dst + o) = v;
     }
-    for (int64_t o = whole + 2 * lane; o < row; o += 128) *(uint16_t *)(dst + o) = *(const uint16_t *)(src + o);
+    for (int64_t o = whole + 2 * lane; o < row; o += 2 * lanes) *(uint16_t *)(dst + o) = *(const uint16_t *)(src + o);
   }
 }
 
-// A wave takes 64 kCols columns of one token.  The places and weights of four
-// choices are wave-uniform; their rows are loaded together, then added one
-// after the other in s order.  8192 tokens of four bf16 rows of 2880: 48 us
-// (4.9 TB/s), 67 with the rows loaded one by one.
+// `lanes` lanes (a power of two, up to a wave) take kCols columns of one token
+// each; `parts` of them cover its row.  The rows of four choices are loaded
+// together, then added one after the other in s order.  8192 tokens of four
+// bf16 rows of 2880, written just before: 38 us (6.3 TB/s).
 constexpr int kCols = 8;
 template <int TY, int TO>
 __global__ void __launch_bounds__(256) combine_kernel(const uint8_t *y, int64_t y_stride, int64_t y_rows,
                                                       const int32_t *pos, const float *w, int n_sel, int64_t n_cols,
-                                                      uint8_t *out, int64_t out_stride, int64_t n_tok,
-                                                      int waves_per_token) {
+                                                      uint8_t *out, int64_t out_stride, int64_t n_tok, int lanes,
+                                                      int parts) {
   constexpr int EY = Elem<TY>::kSize, EO = Elem<TO>::kSize, kAt = 4;
-  const int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = task / waves_per_token;
-  const int64_t col = ((task - t * waves_per_token) * 64 + (threadIdx.x & 63)) * kCols;
+  const int64_t task = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / (unsigned)lanes;
+  const int64_t t = parts == 1 ? task : task / parts;
+  const int64_t col = ((task - t * parts) * lanes + (threadIdx.x & (lanes - 1))) * kCols;
   if (t >= n_tok || col >= n_cols) return;
   pos += t * n_sel;
   float acc[kCols];
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint8_t *y, int64_t 
     float ws[kAt], v[kAt][kCols];
 #pragma unroll
     for (int j = 0; j < kAt; ++j) {
-      const int p = s0 + j < n_sel ? __builtin_amdgcn_readfirstlane(pos[s0 + j]) : -1;
+      const int p = s0 + j < n_sel ? pos[s0 + j] : -1;
       there[j] = p >= 0 && p < y_rows;
       if (!there[j]) continue;
       ws[j] = w ? w[t * n_sel + s0 + j] : 1.0f;
@@ -326,56 +326,60 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint8_t *y, int64_t 
     }
 }
 
-// One workgroup per (token, choice): dy's row and the dot product, summed by
-// lane, then over the lanes, then over the waves.
+// A (token, choice) slot's row of dy and its dot product: by a workgroup
+// (lanes = 256), or by a power of two of lanes where a row is at most a wave's
+// kCols columns each.  The sum goes by lane, then over the lanes, then over the
+// waves.
 template <int TD, int TY>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const uint8_t *dout, int64_t d_stride, const uint8_t *y,
                                                            int64_t y_stride, int64_t y_rows, const int32_t *pos,
-                                                           const float *w, int n_sel, int64_t n_cols, uint8_t *dy,
-                                                           int64_t dy_stride, float *dw) {
+                                                           const float *w, int n_sel, int64_t n_slots, int64_t n_cols,
+                                                           uint8_t *dy, int64_t dy_stride, float *dw, int lanes) {
   constexpr int ED = Elem<TD>::kSize, EY = Elem<TY>::kSize;
   __shared__ float part[4];
-  const int64_t slot = blockIdx.x;
-  const int64_t t = slot / n_sel;
-  const int64_t p = pos[slot];
-  if (p < 0 || p >= y_rows) {
-    if (threadIdx.x == 0) dw[slot] = 0.0f;
-    return;
-  }
-  const float ws = w[slot];
+  const int lane = threadIdx.x & (lanes - 1);
+  const int64_t slot = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / (unsigned)lanes;
+  const int64_t p = slot < n_slots ? pos[slot] : -1;
+  const bool there = p >= 0 && p < y_rows;
   float sum = 0.0f;
-  const int64_t groups = (n_cols + kCols - 1) / kCols;
-  for (int64_t c = threadIdx.x; c < groups; c += 256) {
-    const int64_t col = kCols * c;
-    const uint8_t *d = dout + (t * d_stride + col) * ED;
-    const uint8_t *src = y + (p * y_stride + col) * EY;
-    uint8_t *dst = dy + (p * dy_stride + col) * EY;
-    if (col + kCols <= n_cols) {
-      float a[kCols], b[kCols], o[kCols];
-      load_n<TD>(d, a);
-      load_n<TY>(src, b);
+  if (there) {
+    const int64_t t = slot / n_sel;
+    const float ws = w[slot];
+    const int64_t groups = (n_cols + kCols - 1) / kCols;
+    for (int64_t c = lane; c < groups; c += lanes) {
+      const int64_t col = kCols * c;
+      const uint8_t *d = dout + (t * d_stride + col) * ED;
+      const uint8_t *src = y + (p * y_stride + col) * EY;
+      uint8_t *dst = dy + (p * dy_stride + col) * EY;
+      if (col + kCols <= n_cols) {
+        float a[kCols], b[kCols], o[kCols];
+        load_n<TD>(d, a);
+        load_n<TY>(src, b);
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) {
-        sum = fmaf(a[k], b[k], sum);
-        o[k] = ws * a[k];
-      }
-      store_n<TY>(dst, o);
-    } else {
-      for (int k = 0; col + k < n_cols; ++k) {
-        float a[1], b[1];
-        load_n<TD>(d + k * ED, a);
-        load_n<TY>(src + k * EY, b);
-        sum = fmaf(a[0], b[0], sum);
-        const float o[1] = {ws * a[0]};
-        store_n<TY>(dst + k * EY, o);
+        for (int k = 0; k < kCols; ++k) {
+          sum = fmaf(a[k], b[k], sum);
+          o[k] = ws * a[k];
+        }
+        store_n<TY>(dst, o);
+      } else {
+        for (int k = 0; col + k < n_cols; ++k) {
+          float a[1], b[1];
+          load_n<TD>(d + k * ED, a);
+          load_n<TY>(src + k * EY, b);
+          sum = fmaf(a[0], b[0], sum);
+          const float o[1] = {ws * a[0]};
+          store_n<TY>(dst + k * EY, o);
+        }
       }
     }
   }
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) dw[slot] = (part[0] + part[1]) + (part[2] + part[3]);
+  for (int m = 1; m < min(lanes, 64); m <<= 1) sum += __shfl_xor(sum, m);
+  if (lanes == 256) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = (part[0] + part[1]) + (part[2] + part[3]);
+  }
+  if (lane == 0 && slot < n_slots) dw[slot] = there ? sum : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -433,6 +437,13 @@ int launch(int32_t x_type, const MxArgs &a, hipStream_t stream) {
     default: return QG_E_FMT;
   }
   return QG_OK;
+}
+
+// Lanes for a row of n pieces: the power of two that covers it, up to a wave.
+int row_lanes(int64_t n) {
+  int lanes = 1;
+  while (lanes < n && lanes < 64) lanes *= 2;
+  return lanes;
 }
 
 int64_t row_bytes(const qg_tensor *x) {
@@ -592,11 +603,12 @@ int qgemv_expert_gather(const qg_tensor *x, const int32_t *slots, int32_t n_sel,
   if (out->n_rows == 0 || out->n_cols == 0) return QG_OK;
   if (!slots) return QG_E_NULL;
   const int es = elem_size(x->type);
-  const unsigned grid = (unsigned)std::min<int64_t>((out->n_rows + 3) / 4, 1 << 20);
+  const int lanes = row_lanes((out->n_cols * es + 15) / 16);
+  const unsigned grid = (unsigned)std::min<int64_t>((out->n_rows * lanes + 255) / 256, 1 << 20);
   // (the memory-side cache holds 256 MB)
   const auto kernel = out->n_rows * out->n_cols * es > (64ll << 20) ? gather_kernel<true> : gather_kernel<false>;
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, (const uint8_t *)x->data, x->stride * es, x->n_rows,
-                     x->n_cols * es, slots, n_sel, out->n_rows, (uint8_t *)out->data, out->stride * es);
+                     x->n_cols * es, slots, n_sel, out->n_rows, (uint8_t *)out->data, out->stride * es, lanes);
   MX_HIP(hipGetLastError());
   return QG_OK;
 }
@@ -609,13 +621,15 @@ int qgemv_expert_combine(const qg_tensor *y, const int32_t *pos, const float *w,
   if (n_sel < 0) return QG_E_ARG;
   if (out->n_rows == 0 || out->n_cols == 0) return QG_OK;
   if (n_sel > 0 && !pos) return QG_E_NULL;
-  const int64_t waves = (out->n_cols + 64 * kCols - 1) / (64 * kCols), grid = (out->n_rows * waves + 3) / 4;
+  const int lanes = row_lanes((out->n_cols + kCols - 1) / kCols);
+  const int64_t parts = (out->n_cols + lanes * kCols - 1) / (lanes * kCols);
+  const int64_t grid = (out->n_rows * parts * lanes + 255) / 256;
   if (grid > kMaxDim) return QG_E_SHAPE;
   with_type(y->type, [&](auto TY) {
     with_type(out->type, [&](auto TO) {
       hipLaunchKernelGGL((combine_kernel<decltype(TY)::value, decltype(TO)::value>), dim3((unsigned)grid), dim3(256),
                          0, stream, (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel, out->n_cols,
-                         (uint8_t *)out->data, out->stride, out->n_rows, (int)waves);
+                         (uint8_t *)out->data, out->stride, out->n_rows, lanes, (int)parts);
     });
   });
   MX_HIP(hipGetLastError());
@@ -635,12 +649,14 @@ int qgemv_expert_combine_grad(const qg_tensor *dout, const qg_tensor *y, const i
   if (y->n_rows > 0 && y->data == dy->data && y->n_cols > 0) return QG_E_ARG;
   if (dout->n_rows == 0) return QG_OK;
   if (!pos || !w || !dw) return QG_E_NULL;
+  const int64_t groups = (y->n_cols + kCols - 1) / kCols, slots = dout->n_rows * n_sel;
+  const int lanes = groups > 64 ? 256 : row_lanes(groups);
   with_type(dout->type, [&](auto TD) {
     with_type(y->type, [&](auto TY) {
       hipLaunchKernelGGL((combine_grad_kernel<decltype(TD)::value, decltype(TY)::value>),
-                         dim3((unsigned)(dout->n_rows * n_sel)), dim3(256), 0, stream, (const uint8_t *)dout->data,
-                         dout->stride, (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel,
-                         dout->n_cols, (uint8_t *)dy->data, dy->stride, dw);
+                         dim3((unsigned)((slots * lanes + 255) / 256)), dim3(256), 0, stream,
+                         (const uint8_t *)dout->data, dout->stride, (const uint8_t *)y->data, y->stride, y->n_rows,
+                         pos, w, (int)n_sel, slots, dout->n_cols, (uint8_t *)dy->data, dy->stride, dw, lanes);
     });
   });
   MX_HIP(hipGetLastError());

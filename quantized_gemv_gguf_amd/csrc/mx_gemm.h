@@ -174,6 +174,52 @@ __device__ __forceinline__ void store4(const MxArgs &a, int place, int n, int le
   }
 }
 
+// A workgroup's outputs through LDS, a row of fragments (16 tokens of each of
+// the WM waves) at a time, so that a store instruction writes whole lines of
+// y: a lane's own eight bytes would leave each line to eight instructions.
+// (4096 x 24576 bf16 outputs of MXFP4 tokens, k = 6144: 480 us with the lanes'
+// own stores, 411 so; below 64 tokens a workgroup, 128 of float tokens, the
+// lanes' own stores are no slower and leave more registers.)  ES: bytes of an output.
+template <typename S, int ES, typename V, typename A>
+__device__ __forceinline__ void store_rows(const MxArgs &a, const Tile &tile, uint8_t *lds, int wn, int wm, int i, int g,
+                                           V outputs, A absent) {
+  constexpr int kPitch = S::TN * ES + 16, kLanes = S::TN * ES / 16;  // 16-byte pieces of a token's row
+  constexpr int kTokens = 16 * S::kWM;
+  const int left = a.n - tile.n0;
+#pragma unroll
+  for (int m = 0; m < S::kFM; ++m) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < S::kFN; ++n) {
+      const f32x4 v = outputs(n, m);
+      uint8_t *at = lds + (16 * wm + i) * kPitch + (16 * (wn * S::kFN + n) + 4 * g) * ES;
+      if constexpr (ES == 4) {
+        *(f32x4 *)at = v;
+      } else {
+        const bool h = a.y_type == QG_F16;
+        *(u32x2 *)at = u32x2{h ? pack_f16(v.x, v.y) : pack_bf16(v.x, v.y), h ? pack_f16(v.z, v.w) : pack_bf16(v.z, v.w)};
+      }
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < kTokens * kLanes; q += S::kThreads) {
+      const int tok = q / kLanes, piece = q % kLanes, col = piece * (16 / ES);
+      const int p = tile.m0 + 16 * ((tok >> 4) * S::kFM + m) + (tok & 15);
+      if (p >= tile.m_end || col >= left) continue;
+      u32x4 v = *(const u32x4 *)(lds + tok * kPitch + 16 * piece);
+      if (absent(p)) v = u32x4{0, 0, 0, 0};
+      uint8_t *y = (uint8_t *)a.y + ((int64_t)p * a.y_stride + tile.n0 + col) * ES;
+      if (col + 16 / ES <= left) __builtin_memcpy(y, &v, 16);
+      else
+#pragma unroll
+        for (int k = 0; k < 16 / ES - 1; ++k)
+          if (col + k < left) {
+            if constexpr (ES == 4) ((uint32_t *)y)[k] = v[k];
+            else ((uint16_t *)y)[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+          }
+    }
+  }
+}
+
 // The bf16 terms of eight values in the lane order of the codes' word: element
 // pairs (lo[b], hi[b]), lo = four values from 4q, hi = four from 16 + 4q.
 // Terms are cut, not rounded: the rest is exact.
@@ -353,7 +399,12 @@ struct MxTile {
   static constexpr int kOffWS = KS * kWGroup, kOffX = kOffWS + KS * kWSGroup, kOffXS = kOffX + kTerms * KS * kXGroup;
   static constexpr int kStage = kOffXS + KS * kXSGroup;
   static constexpr int kRed = (WK - 1) * WN * WM * kMats * FN * FM * 1024;
-  static constexpr int kLds = NBUF * kStage > kRed ? NBUF * kStage : kRed;
+  // larger tiles store their outputs by rows (store_rows)
+  static constexpr bool kRows = WK == 1 && FM * WM > (XK == kFp4 ? 2 : 4);
+  static constexpr int kFN = FN, kFM = FM, kWM = WM;
+  static constexpr int kOut = kRows ? 16 * WM * (4 * TN + 16) : 0;
+  static constexpr int kMost = kRed > kOut ? kRed : kOut;
+  static constexpr int kLds = NBUF * kStage > kMost ? NBUF * kStage : kMost;
   static_assert(kThreads % kBlk == 0 && kWRows % kRowStep == 0, "a stage's blocks divide over the threads");
   static_assert(kRowStep % 4 == 0, "so do its activations, and a thread's rows share their alignment");
   static_assert(!PAIR || TN % kRowStep == 0, "a load's rows are of one matrix");
@@ -650,21 +701,33 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
           acc[u][n][0][e] = sum;
         }
   }
+  // The outputs of fragment (n, m): four of consecutive n for this lane's token.
+  auto outputs = [&](int n, int m) {
+    f32x4 v = acc[0][n][m];
+    if constexpr (PAIR)
 #pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    const int p = tile.m0 + (COLS ? i / S::kCols : 16 * (wm * FM + m) + i);
-    if (p >= tile.m_end || (COLS && (i % S::kCols != 0 || i / S::kCols >= TM))) continue;
-    // a source that x does not have
-    const bool absent = a.slots && (uint32_t)(a.slots[p] < 0 ? -1 : a.slots[p] / a.n_sel) >= (uint32_t)a.x_rows;
+      for (int e = 0; e < 4; ++e) v[e] = silu_times(v[e], acc[S::kMats - 1][n][m][e]);
+    return v;
+  };
+  // a place whose source x does not have
+  auto absent = [&](int p) {
+    return a.slots && (uint32_t)(a.slots[p] < 0 ? -1 : a.slots[p] / a.n_sel) >= (uint32_t)a.x_rows;
+  };
+  if constexpr (S::kRows) {
+    if (a.y_type == QG_F32) store_rows<S, 4>(a, tile, lds, wn, wm, i, g, outputs, absent);
+    else store_rows<S, 2>(a, tile, lds, wn, wm, i, g, outputs, absent);
+  } else {
 #pragma unroll
-    for (int n = 0; n < FN; ++n) {
-      const int r = tile.n0 + 16 * (wn * FN + n) + 4 * g;
-      f32x4 v = acc[0][n][m];
-      if constexpr (PAIR)
+    for (int m = 0; m < FM; ++m) {
+      const int p = tile.m0 + (COLS ? i / S::kCols : 16 * (wm * FM + m) + i);
+      if (p >= tile.m_end || (COLS && (i % S::kCols != 0 || i / S::kCols >= TM))) continue;
+      const bool none = absent(p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = silu_times(v[e], acc[1][n][m][e]);
-      if (absent) v = f32x4{0, 0, 0, 0};
-      if (r < a.n) store4(a, p, r, a.n - r, v);
+      for (int n = 0; n < FN; ++n) {
+        const int r = tile.n0 + 16 * (wn * FN + n) + 4 * g;
+        const f32x4 v = outputs(n, m);
+        if (r < a.n) store4(a, p, r, a.n - r, none ? f32x4{0, 0, 0, 0} : v);
+      }
     }
   }
 }

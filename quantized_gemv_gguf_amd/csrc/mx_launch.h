@@ -48,24 +48,24 @@ template <> struct Shapes<kFp4, false> {
                                               Shape<kFp4, false, 2, 2, 1, 1, 4, 4, 2, 68, 28, false>,
                                               Shape<kFp4, false, 2, 4, 2, 1, 2, 4, 1, 115, 66, false>,
                                               Shape<kFp4, false, 4, 4, 4, 2, 1, 2, 2, 260, 330, true>,
-                                              Shape<kFp4, false, 4, 8, 4, 2, 1, 1, 2, 450, 450, true>>;
+                                              Shape<kFp4, false, 4, 4, 4, 4, 1, 1, 2, 420, 440, true>>;
 };
 template <> struct Shapes<kFp4, true> {
-  static constexpr auto run = launch_cheapest<Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 23, false>,
+  static constexpr auto run = launch_cheapest<Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 25, false>,
                                               Shape<kFp4, true, 1, 4, 2, 1, 2, 4, 1, 115, 56, false>,
-                                              Shape<kFp4, true, 1, 4, 4, 1, 1, 2, 1, 175, 105, false>,
-                                              Shape<kFp4, true, 2, 4, 4, 2, 1, 2, 2, 260, 300, true>>;
+                                              Shape<kFp4, true, 1, 4, 4, 1, 1, 2, 1, 160, 97, false>,
+                                              Shape<kFp4, true, 1, 4, 8, 2, 1, 2, 2, 280, 290, true>>;
 };
 template <> struct Shapes<kBf16, false> {
   static constexpr auto run = launch_cheapest<Shape<kBf16, false, 2, 1, 1, 1, 8, 8, 2, 72, 62, true>,
                                               Shape<kBf16, false, 2, 2, 4, 1, 1, 2, 1, 210, 130, false>,
-                                              Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 300, true>,
-                                              Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 630, 630, true>>;
+                                              Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 340, true>,
+                                              Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 560, 610, true>>;
 };
 template <> struct Shapes<kBf16, true> {
   static constexpr auto run = launch_cheapest<Shape<kBf16, true, 1, 1, 1, 1, 4, 4, 1, 75, 40, false>,
                                               Shape<kBf16, true, 1, 2, 4, 1, 1, 2, 1, 200, 120, false>,
-                                              Shape<kBf16, true, 2, 4, 4, 2, 1, 1, 2, 530, 530, true>,
+                                              Shape<kBf16, true, 2, 2, 8, 2, 1, 1, 2, 500, 500, true>,
                                               Shape<kBf16, true, 4, 3, 2, 4, 1, 1, 2, 720, 720, true>>;
 };
 template <> struct Shapes<kF16, false> {
@@ -73,7 +73,7 @@ template <> struct Shapes<kF16, false> {
                                               Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 48, true, true>,
                                               Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 95, 90, true>,
                                               Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 250, 170, false>,
-                                              Shape<kF16, false, 4, 4, 8, 1, 1, 1, 1, 1000, 1000, true>>;
+                                              Shape<kF16, false, 4, 2, 8, 2, 1, 1, 1, 930, 950, true>>;
 };
 template <> struct Shapes<kF16, true> {
   static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 80, 33, false, true>,
@@ -87,14 +87,15 @@ template <> struct Shapes<kF32, false> {
                                               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 97, 115, true>,
                                               Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 145, false>,
                                               Shape<kF32, false, 4, 2, 4, 2, 1, 1, 2, 850, 850, true>,
-                                              Shape<kF32, false, 4, 4, 8, 1, 1, 1, 1, 1350, 1550, true>>;
+                                              Shape<kF32, false, 4, 2, 8, 2, 1, 1, 1, 1250, 1350, true>>;
 };
 template <> struct Shapes<kF32, true> {
   static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
                                               Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 80, false>,
                                               Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 260, 152, false>,
                                               Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 410, 247, false>,
-                                              Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>>;
+                                              Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>,
+                                              Shape<kF32, true, 2, 1, 8, 2, 1, 1, 2, 750, 750, true>>;
 };
 
 template <int XK>

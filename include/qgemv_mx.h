@@ -44,7 +44,8 @@ enum qg_float { QG_F32 = 32, QG_F16 = 33, QG_BF16 = 34 };
  * r * stride of data, elements contiguous, data aligned to one element; an
  * input may have any stride >= 0, an output's must be >= n_cols where it has
  * more than one row.  QG_MXFP4 (inputs of the products only): rows of
- * n_cols / 32 blocks, back to back, data 16-byte aligned, stride == n_cols.
+ * n_cols / 32 blocks, back to back, data 16-byte aligned, stride == n_cols;
+ * as of weights, the whole 16-byte granule of the last byte may be read.
  * Inputs and outputs of one call must not overlap. */
 typedef struct qg_tensor {
   void *data;

@@ -82,6 +82,7 @@ __device__ __forceinline__ bool find_tile(const MxArgs &a, int tn_rows, Tile *t)
   int mine = 0, upto = 0, tiles = a.tiles;
   if (a.offsets) {
     int o = e0 < e1 ? at(e0) : 0;
+#pragma unroll 4
     for (int i = e0; i < e1; ++i) {
       const int q = at(i + 1);
       mine += (max(q - o, 0) + TM - 1) / TM;

@@ -206,6 +206,88 @@ def test_rows_shared_x_and_no_tokens(dev):
     near(host(y), ref, bound, "f32")
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
+@pytest.mark.parametrize("tok", [1, 3, 33, 70])
+def test_rows_largest_k(dev, kind, tok):
+    rng = np.random.default_rng(tok)
+    n, k = 19, 49152
+    wb = mxref.random_blocks(rng, n, k)
+    x, xv = activations(rng, tok, k, kind, dev)
+    y = nan_buffer(tok, n, "f32", dev)
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, x, y)
+    ref, bound = mxref.product(xv, mxref.values(wb, k), kind)
+    near(host(y), ref, bound, "f32")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tok,n,k", [(2, 40, 96), (50, 300, 224), (300, 520, 160)])
+def test_rows_at_odd_addresses(dev, kind, tok, n, k):
+    """x and y start one element into their buffers and have odd strides: aligned to one element alone."""
+    import torch
+    rng = np.random.default_rng(tok)
+    wb = mxref.random_blocks(rng, n, k)
+    xs, ys = k + 1 + tok % 2, n + 3
+    x = torch.zeros(1 + tok * xs, dtype=T(kind), device=dev)
+    x.copy_(dput(rng.standard_normal(x.shape).astype(np.float32), dev, kind))
+    x = torch.as_strided(x, (tok, k), (xs, 1), 1)
+    buf = torch.full((1 + tok * ys,), float("nan"), dtype=T(kind), device=dev)
+    y = torch.as_strided(buf, (tok, n), (ys, 1), 1)
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, x, y)
+    ref, bound = mxref.product(host(x), mxref.values(wb, k), kind)
+    near(host(y), ref, bound, kind)
+    rest = host(buf)[1:].reshape(tok, ys)[:, n:]
+    assert np.isnan(rest).all() and np.isnan(host(buf)[0]), "wrote outside the rows"
+
+
+def test_offsets_past_32_bits(dev):
+    """Rows of x and y gigabytes apart, and a stack of experts above 4 GiB."""
+    import torch
+    rng = np.random.default_rng(12)
+    n, k, tok, apart = 70, 96, 40, (1 << 26) + 8
+    wb = mxref.random_blocks(rng, n, k)
+    xbuf = torch.empty(tok * apart, dtype=torch.bfloat16, device=dev)
+    ybuf = torch.empty(tok * apart, dtype=torch.bfloat16, device=dev)
+    x, y = torch.as_strided(xbuf, (tok, k), (apart, 1)), torch.as_strided(ybuf, (tok, n), (apart, 1))
+    x.copy_(dput(rng.standard_normal((tok, k)).astype(np.float32), dev, "bf16"))
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, x, y)
+    ref, bound = mxref.product(host(x), mxref.values(wb, k), "bf16")
+    near(host(y), ref, bound, "bf16")
+    out = torch.empty_like(x.contiguous())
+    q.qgemv_expert_gather(x, torch.arange(tok, dtype=torch.int32, device=dev), 1, out)
+    assert torch.equal(out, x)
+    back = torch.as_strided(ybuf, (tok, k), (apart, 1))
+    q.qgemv_expert_combine(x, torch.arange(tok, dtype=torch.int32, device=dev).view(tok, 1), back)
+    assert torch.equal(back, x)
+    del xbuf, ybuf, x, y, out, back
+    n_expert, n, k = 1024, 2880, 2880
+    w = torch.randint(0, 256, (n_expert * n, k // 32 * 17), dtype=torch.uint8, device=dev)
+    w[:, ::17] = 118
+    assert w.numel() > 1 << 32
+    tok = 30
+    offsets = torch.full((n_expert + 1,), tok, dtype=torch.int32, device=dev)
+    offsets[0], offsets[1:n_expert] = 0, 7   # seven tokens at the first expert, the others at the last
+    x = torch.randn(tok, k, device=dev)
+    y = nan_buffer(tok, n, "f32", dev)
+    q.qgemv_expert_mx(q.Matrix(w, q.MXFP4, n_expert * n, k), n_expert, x, offsets, y)
+    for lo, hi, e in ((0, 7, 0), (7, tok, n_expert - 1)):
+        ref, bound = mxref.product(host(x[lo:hi]), mxref.values(w[e * n:(e + 1) * n].cpu().numpy(), k), "f32")
+        near(host(y[lo:hi]), ref, bound, "f32")
+
+
+def test_quantize_past_32_bits(dev):
+    import torch
+    n, k = (1 << 26) + 3, 96  # 6.4 billion values, 3.4 GB of blocks
+    x = torch.empty(n, k, dtype=torch.bfloat16, device=dev).normal_()
+    m = q.Matrix(torch.empty(n * k // 32 * 17, dtype=torch.uint8, device=dev), q.MXFP4, n, k)
+    q.qgemv_mx_quantize(x, m)
+    back = torch.empty_like(x)
+    q.qgemv_mx_dequantize(m, 0, n, back)
+    for r in (0, 12345, n // 2, n - 5):
+        b = m.data.view(n, -1)[r:r + 5].cpu().numpy()
+        assert np.array_equal(b, mxref.quantize(host(x[r:r + 5])))
+        assert np.array_equal(host(back[r:r + 5]), mxref.values(b, k))
+
+
 # --- experts ---------------------------------------------------------------------------
 
 def expert_case(rng, tok, sel, n_expert, dropped):

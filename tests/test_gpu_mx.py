@@ -239,6 +239,55 @@ def test_rows_at_odd_addresses(dev, kind, tok, n, k):
     assert np.isnan(rest).all() and np.isnan(host(buf)[0]), "wrote outside the rows"
 
 
+# places, rows of W, experts (0: dense): grids large enough for the tiles of many tokens and rows, each kind's
+LARGE = [(2049, 130, 0), (700, 1030, 0), (2049, 1030, 0), (2049, 2050, 0), (700, 4100, 0), (65, 8200, 0),
+         (200, 8200, 0), (700, 8200, 0), (129, 12300, 0), (200, 12300, 0), (700, 520, 3), (513, 12300, 3),
+         (2049, 520, 3), (200, 8200, 8), (2049, 520, 40), (2049, 1030, 40)]
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
+@pytest.mark.parametrize("places,n,n_expert", LARGE)
+def test_large_grids(dev, kind, pair, places, n, n_expert):
+    """As test_rows and test_experts; the 64-bit products on the device."""
+    import torch
+    rng = np.random.default_rng(places + n)
+    k, e = (416, 1) if n_expert == 0 else (224, n_expert)
+    out = ["bf16", "f32", "f16"][(n + pair) % 3]
+    x, xv = activations(rng, places, k, kind, dev)
+    wbs = [mxref.random_blocks(rng, e * n, k, 115, 121) for _ in range(1 + pair)]
+    ws = [blocks(b, k, dev) for b in wbs]
+    y = nan_buffer(places, n, out, dev, 8)
+    if n_expert:
+        cuts = np.sort(rng.integers(0, places - 20, e - 1))
+        offsets = np.concatenate([[0], cuts, [places - 3]])
+        call = q.qgemv_expert_mx_swiglu if pair else q.qgemv_expert_mx
+        call(*ws, e, x, dput(offsets.astype(np.int32), dev), y[:, :n])
+    else:
+        offsets = np.array([0, places])
+        (q.qgemv_rows_mx_swiglu if pair else q.qgemv_rows_mx)(*ws, 0, n, x, y[:, :n])
+    got, xd, kept = y.double(), torch.from_numpy(xv).to(dev), int(offsets[-1])
+    assert torch.isnan(got[kept:]).all() and torch.isnan(got[:, n:]).all(), "wrote beyond the places"
+    step = 4 * np.ceil(mxref.STEPS[kind] * k) * 2.0 ** -23
+    for i in range(e):
+        lo, hi = int(offsets[i]), int(offsets[i + 1])
+        if lo == hi:
+            continue
+        r = []
+        for b in wbs:
+            w = torch.from_numpy(mxref.values(b[i * n:(i + 1) * n], k)).to(dev)
+            r.append((xd[lo:hi] @ w.T, step * (xd[lo:hi].abs() @ w.abs().T)))
+        ref, bound = r[0]
+        if pair:
+            (g, dg), (u, du) = r
+            silu = g / (1 + torch.exp(-g))
+            ref = silu * u
+            bound = 1.1 * dg * (u.abs() + du) + silu.abs() * du + (g.abs() + 8) * 2.0 ** -24 * ref.abs()
+        err = (got[lo:hi, :n] - ref).abs()
+        allowed = bound + mxref.HALF[out] * (ref.abs() + bound) + mxref.TINY[out]
+        assert bool((err <= allowed).all()), f"expert {i}: worst {float((err / allowed).max()):.3g} times the bound"
+
+
 def test_offsets_past_32_bits(dev):
     """Rows of x and y gigabytes apart, and a stack of experts above 4 GiB."""
     import torch

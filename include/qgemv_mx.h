@@ -51,8 +51,8 @@ typedef struct qg_tensor {
   void *data;
   int32_t type;     /* enum qg_float, or QG_MXFP4 */
   int32_t reserved; /* must be 0 */
-  int64_t n_rows;   /* 0 .. 2^31 - 1 */
-  int64_t n_cols;   /* 0 .. 2^31 - 1 */
+  int64_t n_rows;   /* 0 .. 2^31 - 2^16 (QG_E_SHAPE above, as of a matrix' rows) */
+  int64_t n_cols;   /* 0 .. 2^31 - 2^16 */
   int64_t stride;   /* elements between rows */
 } qg_tensor;
 
@@ -146,7 +146,7 @@ int qgemv_expert_gather(const qg_tensor *x, const int32_t *slots, int32_t n_sel,
  * n_sel; w: device, the same shape, or NULL for weights of 1, which is also
  * the gradient of qgemv_expert_gather (dx from dout).  Places that are
  * negative or beyond y's rows add nothing; a token without any gets zeros.
- * n_sel >= 0. */
+ * 0 <= n_sel <= 2^30. */
 int qgemv_expert_combine(const qg_tensor *y, const int32_t *pos, const float *w, int32_t n_sel,
                          const qg_tensor *out, qg_stream_t stream);
 

@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const uint8_t *dout, 
     if (e_ != hipSuccess) return qgemv_detail::record_hip_error(e_, #call); \
   } while (0)
 
-constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxDim = 0x7fff0000;  // rows and columns: an index past a tile's end stays an int
 constexpr int64_t kMaxStride = 1ll << 40;
 
 int elem_size(int32_t type) { return type == QG_F32 ? 4 : type == QG_F16 || type == QG_BF16 ? 2 : 0; }
@@ -619,6 +619,7 @@ int qgemv_expert_combine(const qg_tensor *y, const int32_t *pos, const float *w,
   if ((rc = check_tensor(y, false, false)) || (rc = check_tensor(out, false, true))) return rc;
   if (y->n_cols != out->n_cols) return QG_E_SHAPE;
   if (n_sel < 0) return QG_E_ARG;
+  if (n_sel > 1 << 30) return QG_E_SHAPE;
   if (out->n_rows == 0 || out->n_cols == 0) return QG_OK;
   if (n_sel > 0 && !pos) return QG_E_NULL;
   const int lanes = row_lanes((out->n_cols + kCols - 1) / kCols);

@@ -94,6 +94,24 @@ def test_products_refuse():
     assert L.qgemv_rows_mx(mat(), 0, 8, ten(rows=0, data=0), ten(rows=0, cols=8, data=0), None) == 0
 
 
+def test_largest_sizes():
+    """Past 2^31 - 2^16 rows or columns, where a tile's last index would leave 32 bits, and past 2^30 choices."""
+    L = q.lib()
+    for rows in (2 ** 31 - 2 ** 16 + 1, 2 ** 31 - 1):
+        assert L.qgemv_rows_mx(mat(), 0, 8, ten(rows=rows), ten(rows=rows, cols=8), None) == E_SHAPE
+        assert L.qgemv_rows_mx(mat(rows), 0, rows, ten(), ten(cols=rows), None) == E_SHAPE
+        assert L.qgemv_expert_mx(mat(16), 2, ten(), FAKE, FAKE, 2, ten(rows=rows, cols=8), None) == E_SHAPE
+        assert L.qgemv_mx_quantize(ten(rows=rows), mat(rows), None) == E_SHAPE
+        assert L.qgemv_mx_dequantize(mat(rows), 0, rows, ten(rows=rows), None) == E_SHAPE
+        assert L.qgemv_expert_gather(ten(), FAKE, 2, ten(rows=rows), None) == E_SHAPE
+        assert L.qgemv_expert_combine(ten(cols=rows), FAKE, FAKE, 2, ten(cols=rows), None) == E_SHAPE
+    assert L.qgemv_expert_combine(ten(), FAKE, FAKE, 2 ** 30 + 1, ten(rows=1), None) == E_SHAPE
+    # (the largest that are taken, without work)
+    most = 2 ** 31 - 2 ** 16
+    assert L.qgemv_rows_mx(mat(most), 5, 5, ten(), ten(cols=0, data=0), None) == 0
+    assert L.qgemv_expert_combine(ten(cols=0), FAKE, FAKE, 2 ** 30, ten(cols=0), None) == 0
+
+
 def test_expert_products_refuse():
     L = q.lib()
 

@@ -84,7 +84,8 @@ int qgemv_mx_dequantize(const qg_matrix *q, int64_t row_start, int64_t row_end, 
  * token's weight traffic).  x->n_cols = w->k; y->n_rows = x->n_rows, y->n_cols
  * = row_end - row_start, y a float type.  x may be
  *   QG_F32, QG_F16, QG_BF16  taken exactly: a weight is exact in bf16, and x
- *             is the exact sum of three, two or one bf16 terms;
+ *             is the exact sum of three, two or one bf16 terms (but for bits
+ *             of QG_F32 below 2^-133, where bf16's subnormals end: cut off);
  *   QG_MXFP4  4-bit activations (qgemv_mx_quantize), codes and scales of both
  *             sides multiplied by the scaled 4-bit matrix instructions.
  * Products are exact, sums are fp32 in the matrix cores' order, y is rounded

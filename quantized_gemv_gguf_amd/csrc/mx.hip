@@ -65,13 +65,15 @@ __device__ __forceinline__ void store_n(void *p, const float (&v)[N]) {
 
 constexpr int kQBlocks = 256;  // blocks per workgroup: 4352 bytes, 272 granules
 
+// (group0, here and below: the launch's first workgroup of all, see in_grids)
+
 template <int T>
 __global__ void __launch_bounds__(256) quantize_kernel(const uint8_t *x, int64_t stride, int nb, int64_t blocks,
-                                                       uint8_t *out) {
+                                                       uint8_t *out, int64_t group0) {
   __shared__ __attribute__((aligned(16))) uint8_t buf[kQBlocks * 17];
   constexpr int ES = Elem<T>::kSize;
   const int tid = threadIdx.x, q = tid & 3;
-  const int64_t first = (int64_t)blockIdx.x * kQBlocks;
+  const int64_t first = (group0 + blockIdx.x) * kQBlocks;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int bl = 64 * v + (tid >> 2);
@@ -122,10 +124,10 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint8_t *x, int64_t
 
 template <int T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *w, int nb, int64_t blocks, uint8_t *out,
-                                                         int64_t stride) {
+                                                         int64_t stride, int64_t group0) {
   constexpr int ES = Elem<T>::kSize;
   const int q = threadIdx.x & 3;
-  const int64_t b = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
+  const int64_t b = (group0 + blockIdx.x) * 64 + (threadIdx.x >> 2);
   if (b >= blocks) return;
   const uint8_t *p = w + b * 17;
   uint32_t c;
@@ -282,9 +284,9 @@ template <int TY, int TO>
 __global__ void __launch_bounds__(256) combine_kernel(const uint8_t *y, int64_t y_stride, int64_t y_rows,
                                                       const int32_t *pos, const float *w, int n_sel, int64_t n_cols,
                                                       uint8_t *out, int64_t out_stride, int64_t n_tok, int lanes,
-                                                      int parts) {
+                                                      int parts, int64_t group0) {
   constexpr int EY = Elem<TY>::kSize, EO = Elem<TO>::kSize, kAt = 4;
-  const int64_t task = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / (unsigned)lanes;
+  const int64_t task = (group0 + blockIdx.x) * (256 / lanes) + threadIdx.x / (unsigned)lanes;
   const int64_t t = parts == 1 ? task : task / parts;
   const int64_t col = ((task - t * parts) * lanes + (threadIdx.x & (lanes - 1))) * kCols;
   if (t >= n_tok || col >= n_cols) return;
@@ -334,11 +336,12 @@ template <int TD, int TY>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const uint8_t *dout, int64_t d_stride, const uint8_t *y,
                                                            int64_t y_stride, int64_t y_rows, const int32_t *pos,
                                                            const float *w, int n_sel, int64_t n_slots, int64_t n_cols,
-                                                           uint8_t *dy, int64_t dy_stride, float *dw, int lanes) {
+                                                           uint8_t *dy, int64_t dy_stride, float *dw, int lanes,
+                                                           int64_t group0) {
   constexpr int ED = Elem<TD>::kSize, EY = Elem<TY>::kSize;
   __shared__ float part[4];
   const int lane = threadIdx.x & (lanes - 1);
-  const int64_t slot = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / (unsigned)lanes;
+  const int64_t slot = (group0 + blockIdx.x) * (256 / lanes) + threadIdx.x / (unsigned)lanes;
   const int64_t p = slot < n_slots ? pos[slot] : -1;
   const bool there = p >= 0 && p < y_rows;
   float sum = 0.0f;
@@ -392,6 +395,14 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const uint8_t *dout, 
     if (e_ != hipSuccess) return qgemv_detail::record_hip_error(e_, #call); \
   } while (0)
 
+// f(first, count) for all workgroups of 256 threads, a launch at a time: a
+// grid holds fewer than 2^32 threads.
+template <typename F>
+void in_grids(int64_t groups, F f) {
+  constexpr int64_t kMost = 1 << 23;
+  for (int64_t first = 0; first < groups; first += kMost) f(first, (unsigned)std::min(groups - first, kMost));
+}
+
 constexpr int64_t kMaxDim = 0x7fff0000;  // rows and columns: an index past a tile's end stays an int
 constexpr int64_t kMaxStride = 1ll << 40;
 
@@ -429,14 +440,11 @@ int check_window(int64_t n_rows, int64_t r0, int64_t r1) {
 }
 
 int launch(int32_t x_type, const MxArgs &a, hipStream_t stream) {
-  switch (x_type) {
-    case QG_F32: MX_HIP(launch_mx<kF32>(a, stream)); break;
-    case QG_F16: MX_HIP(launch_mx<kF16>(a, stream)); break;
-    case QG_BF16: MX_HIP(launch_mx<kBf16>(a, stream)); break;
-    case QG_MXFP4: MX_HIP(launch_mx<kFp4>(a, stream)); break;
-    default: return QG_E_FMT;
-  }
-  return QG_OK;
+  const auto run = x_type == QG_F32 ? launch_mx<kF32> : x_type == QG_F16 ? launch_mx<kF16>
+                   : x_type == QG_BF16 ? launch_mx<kBf16> : launch_mx<kFp4>;
+  bool fits = true;
+  MX_HIP(run(a, stream, &fits));
+  return fits ? QG_OK : QG_E_SHAPE;
 }
 
 // Lanes for a row of n pieces: the power of two that covers it, up to a wave.
@@ -530,10 +538,11 @@ int qgemv_mx_quantize(const qg_tensor *x, const qg_matrix *q, qg_stream_t stream
   if (x->n_rows == 0) return QG_OK;
   const int nb = (int)(q->k / 32);
   const int64_t blocks = q->n_rows * nb, grid = (blocks + kQBlocks - 1) / kQBlocks;
-  if (grid > kMaxDim) return QG_E_SHAPE;
   with_type(x->type, [&](auto T) {
-    hipLaunchKernelGGL(quantize_kernel<decltype(T)::value>, dim3((unsigned)grid), dim3(256), 0, stream,
-                       (const uint8_t *)x->data, x->stride, nb, blocks, (uint8_t *)q->data);
+    in_grids(grid, [&](int64_t first, unsigned count) {
+      hipLaunchKernelGGL(quantize_kernel<decltype(T)::value>, dim3(count), dim3(256), 0, stream,
+                         (const uint8_t *)x->data, x->stride, nb, blocks, (uint8_t *)q->data, first);
+    });
   });
   MX_HIP(hipGetLastError());
   return QG_OK;
@@ -549,10 +558,12 @@ int qgemv_mx_dequantize(const qg_matrix *q, int64_t row_start, int64_t row_end, 
   if (out->n_rows == 0) return QG_OK;
   const int nb = (int)(q->k / 32);
   const int64_t blocks = out->n_rows * nb, grid = (blocks + 63) / 64;
-  if (grid > kMaxDim) return QG_E_SHAPE;
   with_type(out->type, [&](auto T) {
-    hipLaunchKernelGGL(dequantize_kernel<decltype(T)::value>, dim3((unsigned)grid), dim3(256), 0, stream,
-                       (const uint8_t *)q->data + row_start * nb * 17, nb, blocks, (uint8_t *)out->data, out->stride);
+    in_grids(grid, [&](int64_t first, unsigned count) {
+      hipLaunchKernelGGL(dequantize_kernel<decltype(T)::value>, dim3(count), dim3(256), 0, stream,
+                         (const uint8_t *)q->data + row_start * nb * 17, nb, blocks, (uint8_t *)out->data, out->stride,
+                         first);
+    });
   });
   MX_HIP(hipGetLastError());
   return QG_OK;
@@ -625,12 +636,13 @@ int qgemv_expert_combine(const qg_tensor *y, const int32_t *pos, const float *w,
   const int lanes = row_lanes((out->n_cols + kCols - 1) / kCols);
   const int64_t parts = (out->n_cols + lanes * kCols - 1) / (lanes * kCols);
   const int64_t grid = (out->n_rows * parts * lanes + 255) / 256;
-  if (grid > kMaxDim) return QG_E_SHAPE;
   with_type(y->type, [&](auto TY) {
     with_type(out->type, [&](auto TO) {
-      hipLaunchKernelGGL((combine_kernel<decltype(TY)::value, decltype(TO)::value>), dim3((unsigned)grid), dim3(256),
-                         0, stream, (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel, out->n_cols,
-                         (uint8_t *)out->data, out->stride, out->n_rows, lanes, (int)parts);
+      in_grids(grid, [&](int64_t first, unsigned count) {
+        hipLaunchKernelGGL((combine_kernel<decltype(TY)::value, decltype(TO)::value>), dim3(count), dim3(256), 0,
+                           stream, (const uint8_t *)y->data, y->stride, y->n_rows, pos, w, (int)n_sel, out->n_cols,
+                           (uint8_t *)out->data, out->stride, out->n_rows, lanes, (int)parts, first);
+      });
     });
   });
   MX_HIP(hipGetLastError());
@@ -654,10 +666,12 @@ int qgemv_expert_combine_grad(const qg_tensor *dout, const qg_tensor *y, const i
   const int lanes = groups > 64 ? 256 : row_lanes(groups);
   with_type(dout->type, [&](auto TD) {
     with_type(y->type, [&](auto TY) {
-      hipLaunchKernelGGL((combine_grad_kernel<decltype(TD)::value, decltype(TY)::value>),
-                         dim3((unsigned)((slots * lanes + 255) / 256)), dim3(256), 0, stream,
-                         (const uint8_t *)dout->data, dout->stride, (const uint8_t *)y->data, y->stride, y->n_rows,
-                         pos, w, (int)n_sel, slots, dout->n_cols, (uint8_t *)dy->data, dy->stride, dw, lanes);
+      in_grids((slots * lanes + 255) / 256, [&](int64_t first, unsigned count) {
+        hipLaunchKernelGGL((combine_grad_kernel<decltype(TD)::value, decltype(TY)::value>), dim3(count), dim3(256), 0,
+                           stream, (const uint8_t *)dout->data, dout->stride, (const uint8_t *)y->data, y->stride,
+                           y->n_rows, pos, w, (int)n_sel, slots, dout->n_cols, (uint8_t *)dy->data, dy->stride, dw,
+                           lanes, first);
+      });
     });
   });
   MX_HIP(hipGetLastError());

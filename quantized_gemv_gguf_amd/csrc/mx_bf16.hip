@@ -2,5 +2,5 @@
 #include "mx_launch.h"
 
 namespace qgemv_mx {
-template hipError_t launch_mx<kBf16>(const MxArgs &a, hipStream_t stream);
+template hipError_t launch_mx<kBf16>(const MxArgs &a, hipStream_t stream, bool *fits);
 }

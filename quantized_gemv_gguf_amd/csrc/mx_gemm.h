@@ -16,7 +16,8 @@
 //             times a power of two), and x is laid into LDS in that order.
 //             fp32 x is the exact sum of three bf16 terms (8 bits each,
 //             truncated, so no term rounds), fp16 of two, bf16 of one: every
-//             product is exact and only the fp32 sums round.
+//             product is exact and only the fp32 sums round.  (Bits of fp32 x
+//             below 2^-133, the least bf16 subnormal, are cut off.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -733,22 +734,34 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
   }
 }
 
+// Tiles along the rows of W, and all of the grid.
+template <typename S>
+struct Grid {
+  int64_t tn, all;
+  explicit Grid(const MxArgs &a) {
+    tn = ((int64_t)a.n + S::TN - 1) / S::TN;
+    // experts: a partial tile each beyond the whole ones, as far as places go
+    const int64_t tm = a.offsets ? a.places / S::TM + (int64_t)(a.n_expert < a.places ? a.n_expert : a.places)
+                                 : ((int64_t)a.places + S::TM - 1) / S::TM;
+    all = tn * tm;
+  }
+  // a grid holds fewer than 2^32 threads
+  bool fits() const { return all < (1ll << 32) / S::kThreads - 8; }
+};
+
 template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS = false>
 hipError_t launch_tile(MxArgs a, hipStream_t stream) {
   using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>;
-  const int64_t tn = ((int64_t)a.n + S::TN - 1) / S::TN;
-  // experts: a partial tile each beyond the whole ones, as far as places go
-  const int64_t tm = a.offsets ? a.places / S::TM + (int64_t)(a.n_expert < a.places ? a.n_expert : a.places)
-                               : ((int64_t)a.places + S::TM - 1) / S::TM;
-  if (tn * tm > 0x7ffffff0) return hipErrorInvalidConfiguration;
-  a.tiles_n = (int)tn;
-  a.tiles = (int)(tn * tm);
+  const Grid<S> grid(a);
+  a.tiles_n = (int)grid.tn;
+  a.tiles = (int)grid.all;
   hipLaunchKernelGGL((mx_tile_kernel<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>),
-                     dim3((unsigned)((tn * tm + 7) / 8 * 8)), dim3(S::kThreads), 0, stream, a);
+                     dim3((unsigned)((grid.all + 7) / 8 * 8)), dim3(S::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-// The variants of one activation kind (one translation unit each).
-template <int XK> hipError_t launch_mx(const MxArgs &a, hipStream_t stream);
+// The variants of one activation kind (one translation unit each).  *fits:
+// false, and nothing launched, if no variant's grid holds the product.
+template <int XK> hipError_t launch_mx(const MxArgs &a, hipStream_t stream, bool *fits);
 
 }  // namespace qgemv_mx

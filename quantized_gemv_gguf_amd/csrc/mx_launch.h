@@ -5,6 +5,8 @@
 
 namespace qgemv_mx {
 
+constexpr double kNever = 1e300;  // the time of a grid that cannot be launched
+
 // A tile shape with its measured times, in 0.1 us at k = 4096: kOne, a grid of
 // at most one workgroup per compute unit; kMore, each further workgroup per
 // compute unit.  kWhole: one workgroup at a time fills a compute unit (LDS or
@@ -17,11 +19,12 @@ struct Shape {
   // Estimated time; tokens are taken as spread evenly over the experts, each
   // adding half a partial tile.
   static double cost(const MxArgs &a) {
+    if (!Grid<S>(a).fits()) return kNever;
     const double active = a.offsets ? (a.n_expert < a.places ? a.n_expert : a.places) : 1;
     const double each = a.places / active;
-    double tm = a.offsets ? (each + 0.5 * S::TM) / S::TM : (double)((a.places + S::TM - 1) / S::TM);
+    double tm = a.offsets ? (each + 0.5 * S::TM) / S::TM : (double)((a.places - 1) / S::TM + 1);
     if (tm < 1.0) tm = 1.0;
-    double per_cu = active * tm * ((a.n + S::TN - 1) / S::TN) / 256.0;
+    double per_cu = active * tm * ((a.n - 1) / S::TN + 1) / 256.0;
     if (kWhole) per_cu = (double)(int64_t)(per_cu + 0.999);
     return (kOne + (per_cu > 1.0 ? (per_cu - 1.0) * kMore : 0.0)) * a.nb;
   }
@@ -32,13 +35,14 @@ struct Shape {
 
 // The shape with the least estimated time.
 template <typename... Shapes>
-hipError_t launch_cheapest(const MxArgs &a, hipStream_t stream) {
+hipError_t launch_cheapest(const MxArgs &a, hipStream_t stream, bool *fits) {
   const double costs[] = {Shapes::cost(a)...};
   hipError_t (*const launches[])(const MxArgs &, hipStream_t) = {Shapes::launch...};
   int best = 0;
   for (int i = 1; i < (int)sizeof...(Shapes); ++i)
     if (costs[i] < costs[best]) best = i;
-  return launches[best](a, stream);
+  *fits = costs[best] < kNever;
+  return *fits ? launches[best](a, stream) : hipSuccess;
 }
 
 template <int XK, bool PAIR> struct Shapes;
@@ -99,8 +103,8 @@ template <> struct Shapes<kF32, true> {
 };
 
 template <int XK>
-hipError_t launch_mx(const MxArgs &a, hipStream_t stream) {
-  return a.w2 ? Shapes<XK, true>::run(a, stream) : Shapes<XK, false>::run(a, stream);
+hipError_t launch_mx(const MxArgs &a, hipStream_t stream, bool *fits) {
+  return a.w2 ? Shapes<XK, true>::run(a, stream, fits) : Shapes<XK, false>::run(a, stream, fits);
 }
 
 }  // namespace qgemv_mx

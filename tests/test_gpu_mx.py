@@ -192,6 +192,31 @@ def test_rows_f32_keeps_all_bits(dev):
         assert np.array_equal(host(y), x[:t].astype(np.float64))
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tok", [1, 4, 40, 300])
+def test_rows_subnormal(dev, kind, tok):
+    """Subnormal x, and for float32 normal values whose lower bf16 terms are subnormal, times weights of 2^100: one
+    nonzero value of x a token, so that every output is one exact product."""
+    rng = np.random.default_rng(tok)
+    n, k = 70, 96
+    x = np.zeros((tok, k))
+    at = rng.integers(0, k, tok)
+    low = {"f32": 2.0 ** -149, "f16": 2.0 ** -24, "bf16": 2.0 ** -133}[kind]
+    # (bf16 and fp16: as many bits as a subnormal has)
+    x[np.arange(tok), at] = low * rng.integers(1, {"f32": 2 ** 24, "f16": 2 ** 10, "bf16": 2 ** 7}[kind], tok)
+    wb = mxref.random_blocks(rng, n, k, 227, 228)
+    xd = dput(x.astype(np.float32), dev, kind)
+    assert np.array_equal(host(xd), x)
+    y = nan_buffer(tok, n, "f32", dev)
+    q.qgemv_rows_mx(blocks(wb, k, dev), 0, n, xd, y)
+    # a 24-bit value times an E2M1 significand (1 or 3): its three terms' products are added with two roundings.
+    # bf16's subnormals end at 2^-133, so the float32 terms, which are cut there, leave less than that out of x.
+    v = mxref.values(wb, k)
+    ref = x @ v.T
+    cut = 2.0 ** -133 * np.abs(v[:, at]).T if kind == "f32" else 0.0
+    near(host(y), ref, 2.0 ** -23 * np.abs(ref) + cut, "f32")
+
+
 def test_rows_shared_x_and_no_tokens(dev):
     rng = np.random.default_rng(5)
     n, k = 40, 128
@@ -321,6 +346,71 @@ def test_offsets_past_32_bits(dev):
     for lo, hi, e in ((0, 7, 0), (7, tok, n_expert - 1)):
         ref, bound = mxref.product(host(x[lo:hi]), mxref.values(w[e * n:(e + 1) * n].cpu().numpy(), k), "f32")
         near(host(y[lo:hi]), ref, bound, "f32")
+
+
+def test_more_workgroups_than_a_grid(dev):
+    """Calls whose threads one launch does not hold (2^32 and more of them)."""
+    import torch
+
+    def ones(rows, cols, e):  # every code 1.0, scale e
+        w = torch.full((rows, cols // 32 * 17), 0x22, dtype=torch.uint8, device=dev)
+        w[:, ::17] = e
+        return q.Matrix(w, q.MXFP4, rows, cols)
+
+    # one token, 2^29 + 3 rows of one block
+    n = 2 ** 29 + 3
+    w = ones(n, 32, 127)
+    w.data[n - 1, 0], w.data[2 ** 29 - 1, 0] = 128, 126
+    y = torch.full((1, n), -1.0, dtype=torch.bfloat16, device=dev)
+    q.qgemv_rows_mx(w, 0, n, torch.ones(1, 32, device=dev), y)
+    assert y[0, n - 1] == 64 and y[0, 2 ** 29 - 1] == 16
+    y[0, n - 1] = y[0, 2 ** 29 - 1] = 32
+    assert bool((y == 32).all())
+    del w, y
+    torch.cuda.empty_cache()
+    # 2^30 + 96 blocks back
+    n, k = 2 ** 15 + 1, 2 ** 15
+    w = ones(n, k, 127)
+    w.data[n - 1, ::17] = 130
+    out = torch.zeros(n, k, dtype=torch.bfloat16, device=dev)
+    q.qgemv_mx_dequantize(w, 0, n, out)
+    assert bool((out[:n - 1] == 1).all()) and bool((out[n - 1] == 8).all())
+    # ... and 2^32 + 2^17 of them from a row that is repeated
+    del w, out
+    torch.cuda.empty_cache()
+    n, k = 2 ** 22 + 128, 2 ** 15
+    x = torch.full((1, k), 3.0, dtype=torch.bfloat16, device=dev)
+    w = torch.zeros(n, k // 32 * 17, dtype=torch.uint8, device=dev)
+    q.qgemv_mx_quantize(x.expand(n, k), q.Matrix(w, q.MXFP4, n, k))
+    for lo in range(0, n, 2 ** 19):
+        part = w[lo:lo + 2 ** 19].view(-1, 17)
+        assert bool((part[:, 0] == 126).all()) and bool((part[:, 1:] == 0x77).all())
+    del w, part
+    torch.cuda.empty_cache()
+    # 2^25 tokens of a row of 513: 128 threads each
+    n, cols = 2 ** 25 + 5, 513
+    y = torch.full((4, cols), 2.0, dtype=torch.bfloat16, device=dev)
+    out = torch.zeros(n, cols, dtype=torch.bfloat16, device=dev)
+    pos = torch.zeros(n, 1, dtype=torch.int32, device=dev)
+    pos[n - 1] = -1
+    out[n - 1] = 7
+    q.qgemv_expert_combine(y, pos, out)
+    assert bool((out[:n - 1] == 2).all()) and bool((out[n - 1] == 0).all())
+    del out
+    torch.cuda.empty_cache()
+    # 2^24 slots of a workgroup each, two of them kept
+    n = 2 ** 24 + 9
+    pos = torch.full((n, 1), -1, dtype=torch.int32, device=dev)
+    pos[1], pos[n - 2] = 0, 3
+    wts = torch.full((n, 1), 3.0, device=dev)
+    dw = torch.full((n, 1), -1.0, device=dev)
+    dy = torch.full_like(y, 5.0)
+    q.qgemv_expert_combine_grad(y[:1].expand(n, cols), y, pos, wts, dy, dw)
+    assert bool((dy[0] == 6).all()) and bool((dy[1:3] == 5).all()) and bool((dy[3] == 6).all())
+    assert dw[1] == 4 * cols and dw[n - 2] == 4 * cols
+    dw[1] = dw[n - 2] = 0
+    assert not dw.any()
+    torch.cuda.empty_cache()
 
 
 def test_quantize_past_32_bits(dev):

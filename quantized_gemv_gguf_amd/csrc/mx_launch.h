@@ -69,8 +69,8 @@ template <> struct Shapes<kBf16, false> {
 template <> struct Shapes<kBf16, true> {
   static constexpr auto run = launch_cheapest<Shape<kBf16, true, 1, 1, 1, 1, 4, 4, 1, 75, 40, false>,
                                               Shape<kBf16, true, 1, 2, 4, 1, 1, 2, 1, 200, 120, false>,
-                                              Shape<kBf16, true, 2, 2, 8, 2, 1, 1, 2, 500, 500, true>,
-                                              Shape<kBf16, true, 4, 3, 2, 4, 1, 1, 2, 720, 720, true>>;
+                                              Shape<kBf16, true, 2, 2, 8, 2, 1, 1, 2, 620, 670, true>,
+                                              Shape<kBf16, true, 4, 3, 4, 2, 1, 1, 2, 770, 830, true>>;
 };
 template <> struct Shapes<kF16, false> {
   static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 2, 42, 42, true, true>,

@@ -404,6 +404,8 @@ struct MxTile {
   // larger tiles store their outputs by rows (store_rows)
   static constexpr bool kRows = WK == 1 && FM * WM > (XK == kFp4 ? 2 : 4);
   static constexpr int kFN = FN, kFM = FM, kWM = WM;
+  // MXFP4 x, 128 registers of sums a lane: one loop for every stage (see there)
+  static constexpr bool kOneLoop = XK == kFp4 && NBUF == 2 && kMats * FN * FM >= 32;
   static constexpr int kOut = kRows ? 16 * WM * (4 * TN + 16) : 0;
   static constexpr int kMost = kRed > kOut ? kRed : kOut;
   static constexpr int kLds = NBUF * kStage > kMost ? NBUF * kStage : kMost;
@@ -635,8 +637,25 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
       // stage t + 1 goes from registers to LDS, and t + 2 into the registers,
       // while t is multiplied
       each<P>([&](auto p) { stage(p, last, 0, 0); });
-      if (stages > 1) each<P>([&](auto p) { fetch(p, S::kBlk); });
+      if (S::kOneLoop || stages > 1) each<P>([&](auto p) { fetch(p, S::kBlk); });
       __syncthreads();
+      if constexpr (S::kOneLoop) {
+        // The last two stages in the same code as the others: loads past the
+        // row's end read its first blocks, and what they put into LDS is not
+        // multiplied.  Code of their own, below, leaves no register free and
+        // spills (4096 x 24576 products of k = 6144: 592 us, 377 so), but
+        // where it fits saves those loads and the checks (4 x 4 fragments of a
+        // wave: 385 us, 405 so).
+        for (; t < stages; ++t) {
+          multiply(t & 1, [&](auto slot) {
+            pieces(slot, [&](auto p) {
+              stage(p, last, (t + 1) * S::kBlk, (t + 1) & 1);
+              fetch(p, (t + 2) * S::kBlk);
+            });
+          });
+          __syncthreads();
+        }
+      }
       for (; t + 2 < stages; ++t) {
         multiply(t & 1, [&](auto slot) {
           pieces(slot, [&](auto p) {

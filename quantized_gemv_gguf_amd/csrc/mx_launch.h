@@ -76,14 +76,12 @@ template <> struct Shapes<kBf16, true> {
 };
 template <> struct Shapes<kF16, false> {
   static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 2, 42, 42, true, true>,
-                                              Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 48, true, true>,
-                                              Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 95, 90, true>,
-                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 250, 170, false>,
-                                              Shape<kF16, false, 4, 2, 8, 2, 1, 1, 1, 930, 950, true>>;
+                                              Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 41, true, true>,
+                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 300, 170, false>,
+                                              Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 920, true>>;
 };
 template <> struct Shapes<kF16, true> {
   static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 80, 33, false, true>,
-                                              Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 100, 60, false>,
                                               Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 240, 180, false>,
                                               Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
 };

@@ -181,7 +181,8 @@ __device__ __forceinline__ void store4(const MxArgs &a, int place, int n, int le
 // y: a lane's own eight bytes would leave each line to eight instructions.
 // (4096 x 24576 bf16 outputs of MXFP4 tokens, k = 6144: 480 us with the lanes'
 // own stores, 411 so; below 64 tokens a workgroup, 128 of float tokens, the
-// lanes' own stores are no slower and leave more registers.)  ES: bytes of an output.
+// lanes' own stores are no slower and leave more registers.)  ES: bytes of an
+// output.
 template <typename S, int ES, typename V, typename A>
 __device__ __forceinline__ void store_rows(const MxArgs &a, const Tile &tile, uint8_t *lds, int wn, int wm, int i, int g,
                                            V outputs, A absent) {
@@ -378,6 +379,19 @@ __device__ __forceinline__ void each(F f) {
 // rows in one word; float x as [term][group][fragment][word j][token][block],
 // the planes of words 64 bytes apart beyond their 1 KB so that a token's
 // sixteen pieces are written to sixteen bank groups.
+//
+// What bounds it.  MXFP4 tokens, 4096 x 24576 outputs of k = 6144: 410 us, 3.0
+// PFLOP/s (a bf16 library product of 8192^3 runs at 1.1).  LDS is busy for 61%
+// of that, the matrix cores for 36%, and 5.2 GB pass from L2 to the compute
+// units, 13 TB/s: a stage's 136 bytes of a row are two lines of 128, of which
+// the next stage fetches one again (stages of 128 values: 7.2 GB).  bf16 tokens,
+// 2048 x 8192 outputs of k = 4096: 127 us, 1.1 PFLOP/s, a library product's
+// rate.  fp32 tokens take three times the matrix instructions, 268 us.  4096
+// MXFP4 tokens x 4 of 128 experts, pair of 2880 x 2880: 520 us, LDS 42% busy
+// and 4.9 GB from L2; a sixth of it is the weights' way from memory (470 us
+// instead of 570, in another shape, with one expert's weights for all).  Few
+// tokens: the blocks' latency and, for fp32, the terms, which every workgroup
+// makes anew.
 template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS = false>
 struct MxTile {
   static constexpr int kThreads = 64 * WN * WM * WK;

@@ -34,7 +34,11 @@ struct Shape {
   }
 };
 
-// The shape with the least estimated time.
+// The shape with the least estimated time.  Timed against every shape of its
+// kind for 25 problems each (1 to 4096 tokens, dense, and of 8 to 128 experts;
+// k = 2880 to 11008), the chosen one took at most 1.12 times the best, mostly
+// 1.00 to 1.03.  No one shape does: bf16 tokens, 5 x 11008 outputs of k = 4096,
+// 11 us in the smallest shape and 54 in the largest; 2048 x 8192, 786 and 133.
 template <typename... Shapes>
 hipError_t launch_cheapest(const MxArgs &a, hipStream_t stream, bool *fits) {
   const double costs[] = {Shapes::cost(a)...};

@@ -79,9 +79,9 @@ template <> struct Shapes<kBf16, true> {
                                               Shape<kBf16, true, 4, 3, 4, 2, 1, 1, 2, 770, 830, true>>;
 };
 template <> struct Shapes<kF16, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 2, 42, 42, true, true>,
+  static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 1, 44, 24, false, true>,
                                               Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 41, true, true>,
-                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 300, 170, false>,
+                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 300, 195, false>,
                                               Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 920, true>>;
 };
 template <> struct Shapes<kF16, true> {
@@ -90,7 +90,7 @@ template <> struct Shapes<kF16, true> {
                                               Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
 };
 template <> struct Shapes<kF32, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 2, 42, 42, true, true>,
+  static constexpr auto run = launch_cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 1, 44, 24, false, true>,
                                               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 55, 40, true, true>,
                                               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 97, 115, true>,
                                               Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 145, false>,

@@ -60,7 +60,8 @@ template <> struct Shapes<kFp4, false> {
                                               Shape<kFp4, false, 4, 8, 4, 2, 1, 2, 2, 415, 430, true>>;
 };
 template <> struct Shapes<kFp4, true> {
-  static constexpr auto run = launch_cheapest<Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 25, false>,
+  static constexpr auto run = launch_cheapest<Shape<kFp4, true, 1, 1, 1, 1, 4, 4, 2, 60, 23, false>,
+                                              Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 25, false>,
                                               Shape<kFp4, true, 1, 4, 2, 1, 2, 4, 1, 115, 56, false>,
                                               Shape<kFp4, true, 1, 4, 4, 1, 1, 2, 1, 160, 97, false>,
                                               Shape<kFp4, true, 2, 4, 4, 2, 1, 2, 2, 270, 275, true>,
@@ -73,7 +74,8 @@ template <> struct Shapes<kBf16, false> {
                                               Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 560, 610, true>>;
 };
 template <> struct Shapes<kBf16, true> {
-  static constexpr auto run = launch_cheapest<Shape<kBf16, true, 1, 1, 1, 1, 4, 4, 1, 75, 40, false>,
+  static constexpr auto run = launch_cheapest<Shape<kBf16, true, 1, 1, 1, 1, 8, 8, 2, 62, 60, true>,
+                                              Shape<kBf16, true, 1, 1, 2, 1, 4, 4, 1, 88, 60, false>,
                                               Shape<kBf16, true, 1, 2, 4, 1, 1, 2, 1, 200, 120, false>,
                                               Shape<kBf16, true, 2, 2, 8, 2, 1, 1, 2, 620, 670, true>,
                                               Shape<kBf16, true, 4, 3, 4, 2, 1, 1, 2, 770, 830, true>>;

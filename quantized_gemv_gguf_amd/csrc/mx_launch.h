@@ -87,7 +87,8 @@ template <> struct Shapes<kF16, false> {
                                               Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 920, true>>;
 };
 template <> struct Shapes<kF16, true> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 4, 4, 1, 80, 33, false, true>,
+  static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 8, 8, 1, 66, 38, false, true>,
+                                              Shape<kF16, true, 1, 1, 2, 1, 4, 4, 1, 112, 58, false, true>,
                                               Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 240, 180, false>,
                                               Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
 };
@@ -100,8 +101,10 @@ template <> struct Shapes<kF32, false> {
                                               Shape<kF32, false, 4, 2, 8, 2, 1, 1, 1, 1250, 1350, true>>;
 };
 template <> struct Shapes<kF32, true> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
-                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 80, false>,
+  static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 1, 1, 8, 8, 1, 72, 42, false, true>,
+                                              Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
+                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 125, 64, false, true>,
+                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 115, true>,
                                               Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 260, 152, false>,
                                               Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 410, 247, false>,
                                               Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>,

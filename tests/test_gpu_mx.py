@@ -267,7 +267,8 @@ def test_rows_at_odd_addresses(dev, kind, tok, n, k):
 # places, rows of W, experts (0: dense): grids large enough for the tiles of many tokens and rows, each kind's
 LARGE = [(2049, 130, 0), (700, 1030, 0), (2049, 1030, 0), (2049, 2050, 0), (700, 4100, 0), (65, 8200, 0),
          (200, 8200, 0), (700, 8200, 0), (129, 12300, 0), (200, 12300, 0), (700, 520, 3), (513, 12300, 3),
-         (2049, 520, 3), (200, 8200, 8), (2049, 520, 40), (2049, 1030, 40)]
+         (2049, 520, 3), (200, 8200, 8), (2049, 520, 40), (2049, 1030, 40), (90, 1030, 0), (23, 4100, 0), (33, 1030, 8),
+         (40, 2050, 3)]
 
 
 @pytest.mark.parametrize("pair", [False, True])

@@ -314,6 +314,34 @@ def test_large_grids(dev, kind, pair, places, n, n_expert):
         assert bool((err <= allowed).all()), f"expert {i}: worst {float((err / allowed).max()):.3g} times the bound"
 
 
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_large_gathered(dev, kind, pair, out):
+    """Tiles of many tokens that gather x through slots: tokens named more than once, slots of tokens that x does not
+    have (rows of zeros), an expert without a place, offsets below zero and beyond the places."""
+    import torch
+    rng = np.random.default_rng(21)
+    tok, sel, places, n, k, e = 700, 2, 2049, 523, 160, 3
+    x, xv = activations(rng, tok, k, kind, dev)
+    wbs = [mxref.random_blocks(rng, e * n, k, 117, 121) for _ in range(1 + pair)]
+    slots = rng.integers(0, sel * tok, places)
+    foreign = rng.choice(places, 40, replace=False)
+    slots[foreign] = rng.choice([-1, -2 ** 31, sel * tok, 2 ** 31 - 1], 40)
+    call = q.qgemv_expert_mx_swiglu if pair else q.qgemv_expert_mx
+    y = nan_buffer(places, n, out, dev, 3)
+    call(*[blocks(b, k, dev) for b in wbs], e, x, dput(np.array([-7, 600, 600, 5000], np.int32), dev), y[:, :n],
+         slots=dput(slots.astype(np.int32), dev), n_sel=sel)
+    xs = xv[np.clip(slots // sel, 0, tok - 1)]
+    xs[foreign] = 0
+    got = host(y)
+    assert np.isnan(got[:, n:]).all()
+    for i, lo, hi in ((0, 0, 600), (2, 600, places)):
+        r = [mxref.product(xs[lo:hi], mxref.values(b[i * n:(i + 1) * n], k), kind) for b in wbs]
+        ref, bound = mxref.swiglu(*r[0], *r[1]) if pair else r[0]
+        near(got[lo:hi, :n], ref, bound, out)
+
+
 def test_offsets_past_32_bits(dev):
     """Rows of x and y gigabytes apart, and a stack of experts above 4 GiB."""
     import torch

@@ -376,7 +376,9 @@ __device__ __forceinline__ void each(F f) {
 // token costs one matrix instruction, not one per term.
 // LDS: codes [group][row][block], 16 bytes each, so a wave's fragment of 16
 // rows is 1 KB read without conflicts; scale bytes of four fragments of 16
-// rows in one word; float x as [term][group][fragment][word j][token][block],
+// rows in one word; groups of both padded so that what a wave writes at a time
+// falls into different banks (23 bf16 tokens, 4096 rows of 11008: 14.7 us with
+// the scales' groups in the same ones, 14.2 so); float x as [term][group][fragment][word j][token][block],
 // the planes of words 64 bytes apart beyond their 1 KB so that a token's
 // sixteen pieces are written to sixteen bank groups.
 //
@@ -407,11 +409,12 @@ struct MxTile {
   static constexpr int kTokStep = XK == kFp4 ? kRowStep : kRowStep / 4;
   static constexpr int NX = (TM + kTokStep - 1) / kTokStep;
   static constexpr int kWGroup = kWRows * 64 + 256 / KS;       // codes of one group, padded
-  static constexpr int kWSGroup = (kWRows + 63) / 64 * 256;    // its scales
+  static constexpr int kWSPad = KS > 1 ? 256 / KS : 0;
+  static constexpr int kWSGroup = (kWRows + 63) / 64 * 256 + kWSPad;  // its scales
   static constexpr int kPlane = 1024 + 64;                     // one word of 16 tokens, padded
   static constexpr int kXFrag = 4 * kPlane;
   static constexpr int kXGroup = XK == kFp4 ? TM * 64 + 256 / KS : FM * WM * kXFrag;
-  static constexpr int kXSGroup = XK == kFp4 ? (TM + 63) / 64 * 256 : 0;
+  static constexpr int kXSGroup = XK == kFp4 ? (TM + 63) / 64 * 256 + kWSPad : 0;
   static constexpr int kOffWS = KS * kWGroup, kOffX = kOffWS + KS * kWSGroup, kOffXS = kOffX + kTerms * KS * kXGroup;
   static constexpr int kStage = kOffXS + KS * kXSGroup;
   static constexpr int kRed = (WK - 1) * WN * WM * kMats * FN * FM * 1024;

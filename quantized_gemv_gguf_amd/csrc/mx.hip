@@ -253,6 +253,135 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(const int32_t *id
   }
 }
 
+// Many slots, in four launches over chunks of at most kChunk slots (and at
+// least QG_MAX_EXPERTS), which keep their tables in the outputs:
+//   count    a chunk's slots of each expert, to the chunk's part of slots;
+//   before   workgroup e: e's slots in the chunks before each, to their parts of
+//            pos, and e's total, to offsets;
+//   total    the offsets;
+//   scatter  a chunk's places, in slot order: its waves' counts, then lane by
+//            lane within groups of 64, whose lanes of one expert find each
+//            other bit by bit.  It has read its part of pos before it writes it,
+//            and slots is no longer read.
+// 262144 slots of 128 experts: 12 us, 45 by sort_kernel, whose every workgroup
+// reads every id.
+constexpr int64_t kOneLaunch = 65536;
+constexpr int kChunk = 2048, kChunkWaves = kChunk / 256;
+struct Chunks {  // of `least` slots, the first `more` of one more
+  int count, least, more;
+  __device__ __forceinline__ int start(int c) const { return c * least + min(c, more); }
+};
+
+__global__ void __launch_bounds__(512) sort_count_kernel(const int32_t *ids, Chunks chunks, int n_expert,
+                                                         int32_t *slots) {
+  __shared__ int counts[QG_MAX_EXPERTS];
+  const int i0 = chunks.start((int)blockIdx.x), i1 = chunks.start((int)blockIdx.x + 1);
+  for (int e = (int)threadIdx.x; e < n_expert; e += 512) counts[e] = 0;
+  __syncthreads();
+  for (int i = i0 + (int)threadIdx.x; i < i1; i += 512)
+    if ((uint32_t)ids[i] < (uint32_t)n_expert) atomicAdd(&counts[ids[i]], 1);
+  __syncthreads();
+  for (int e = (int)threadIdx.x; e < n_expert; e += 512) slots[i0 + e] = counts[e];
+}
+
+// Inclusive sum over a workgroup of WAVES waves.
+template <int WAVES>
+__device__ __forceinline__ int scan_add(int v, int *part) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  if (lane == 63) part[wave] = v;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) v += part[w];
+  return v;
+}
+
+__global__ void __launch_bounds__(256) sort_before_kernel(const int32_t *slots, Chunks chunks, int32_t *offsets,
+                                                          int32_t *pos) {
+  __shared__ int part[4];
+  const int e = blockIdx.x, per = (chunks.count + 255) / 256;  // each thread's run of chunks
+  const int c0 = min((int)threadIdx.x * per, chunks.count), c1 = min(c0 + per, chunks.count);
+  int mine = 0;
+  for (int c = c0; c < c1; ++c) mine += slots[chunks.start(c) + e];
+  const int upto = scan_add<4>(mine, part);
+  int at = upto - mine;
+  for (int c = c0; c < c1; ++c) {
+    const int i = chunks.start(c) + e;
+    pos[i] = at;
+    at += slots[i];
+  }
+  if (threadIdx.x == 255) offsets[e + 1] = upto;
+}
+
+__global__ void __launch_bounds__(QG_MAX_EXPERTS) sort_total_kernel(int32_t *offsets, int n_expert) {
+  __shared__ int part[QG_MAX_EXPERTS / 64];
+  const int e = (int)threadIdx.x;
+  const int upto = scan_add<QG_MAX_EXPERTS / 64>(e < n_expert ? offsets[e + 1] : 0, part);
+  if (e == 0) offsets[0] = 0;
+  if (e < n_expert) offsets[e + 1] = upto;
+}
+
+__global__ void __launch_bounds__(64 * kChunkWaves) sort_scatter_kernel(const int32_t *ids, Chunks chunks,
+                                                                        int n_expert, const int32_t *offsets,
+                                                                        int32_t *slots, int32_t *pos) {
+  __shared__ int next[kChunkWaves][QG_MAX_EXPERTS];
+  constexpr int kThreads = 64 * kChunkWaves;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i0 = chunks.start((int)blockIdx.x), i1 = chunks.start((int)blockIdx.x + 1);
+  for (int e = (int)threadIdx.x; e < n_expert; e += kThreads)
+#pragma unroll
+    for (int w = 0; w < kChunkWaves; ++w) next[w][e] = 0;
+  int v[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + 256 * wave + 64 * r + lane;
+    v[r] = i < i1 ? ids[i] : -1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if ((uint32_t)v[r] < (uint32_t)n_expert) atomicAdd(&next[wave][v[r]], 1);
+  __syncthreads();
+  for (int e = (int)threadIdx.x; e < n_expert; e += kThreads) {
+    int at = offsets[e] + pos[i0 + e];
+#pragma unroll
+    for (int w = 0; w < kChunkWaves; ++w) {
+      const int here = next[w][e];
+      next[w][e] = at;
+      at += here;
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz((uint32_t)n_expert);
+  const uint64_t lower = (1ull << lane) - 1;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + 256 * wave + 64 * r + lane, e = v[r];
+    const bool kept = (uint32_t)e < (uint32_t)n_expert;
+    uint64_t same = __ballot(kept);
+    for (int b = 0; b < bits; ++b) {
+      const bool one = e >> b & 1;
+      const uint64_t ones = __ballot(one);
+      same &= one ? ones : ~ones;
+    }
+    const int rank = __popcll(same & lower);
+    if (kept) {
+      const int at = next[wave][e] + rank;
+      slots[at] = i;
+      pos[i] = at;
+    } else if (i < i1) {
+      pos[i] = -1;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (kept && rank == 0) next[wave][e] += __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  const int kept = offsets[n_expert];
+  for (int p = max(i0, kept) + (int)threadIdx.x; p < i1; p += kThreads) slots[p] = -1;
+}
+
 // `lanes` lanes (a power of two, up to a wave) copy one row at a time, 16 bytes
 // each, then the row's last bytes by elements of 2.  Past: more rows than the
 // caches hold with what the next kernels read are written past them (32768
@@ -604,8 +733,23 @@ int qgemv_expert_sort(const int32_t *ids, int64_t n_tok, int32_t n_sel, int64_t 
   if (n_expert < 1 || n_expert > QG_MAX_EXPERTS || n_tok > (1ll << 30) / n_sel) return QG_E_SHAPE;
   const int64_t n = n_tok * n_sel;
   if (!offsets || (n > 0 && (!ids || !slots || !pos))) return QG_E_NULL;
-  hipLaunchKernelGGL(sort_kernel, dim3((unsigned)n_expert + 1), dim3(64 * kSortWaves), 0, stream, ids, (int)n,
-                     (int)n_expert, offsets, slots, pos);
+  // One launch's workgroups read every id each, a round of 256 experts at a
+  // time (65536 slots of 128 experts 15 us, of 1024 38; 16384 of 1024 about 14);
+  // four launches take 10 to 13 up to a million slots, and more of the host.
+  if (n * ((n_expert + 255) / 256) <= kOneLaunch) {
+    hipLaunchKernelGGL(sort_kernel, dim3((unsigned)n_expert + 1), dim3(64 * kSortWaves), 0, stream, ids, (int)n,
+                       (int)n_expert, offsets, slots, pos);
+  } else {
+    const int count = (int)((n + kChunk - 1) / kChunk);
+    const Chunks chunks = {count, (int)n / count, (int)n % count};
+    constexpr int64_t kLeast = kOneLaunch / ((QG_MAX_EXPERTS + 255) / 256) + 1;
+    static_assert(kLeast / ((kLeast + kChunk - 1) / kChunk) >= QG_MAX_EXPERTS, "a chunk holds its table");
+    hipLaunchKernelGGL(sort_count_kernel, dim3(chunks.count), dim3(512), 0, stream, ids, chunks, (int)n_expert, slots);
+    hipLaunchKernelGGL(sort_before_kernel, dim3((unsigned)n_expert), dim3(256), 0, stream, slots, chunks, offsets, pos);
+    hipLaunchKernelGGL(sort_total_kernel, dim3(1), dim3(QG_MAX_EXPERTS), 0, stream, offsets, (int)n_expert);
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3(chunks.count), dim3(64 * kChunkWaves), 0, stream, ids, chunks,
+                       (int)n_expert, offsets, slots, pos);
+  }
   MX_HIP(hipGetLastError());
   return QG_OK;
 }

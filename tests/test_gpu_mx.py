@@ -541,6 +541,29 @@ def test_sort(dev, tok, sel, n_expert, dropped):
         assert np.array_equal(buf.cpu().numpy(), np.concatenate([ref.ravel(), [77] * 4]))
 
 
+@pytest.mark.parametrize("tok,sel,n_expert,dropped", [(65536, 1, 16, 0.1), (65537, 1, 16, 0.1), (16385, 4, 128, 0.0),
+                                                      (70001, 1, 1024, 0.3), (40000, 2, 1, 0.5), (33000, 2, 1000, 1.0),
+                                                      (21900, 3, 7, 0.02), (150001, 8, 60, 0.0), (300000, 4, 129, 0.01),
+                                                      (4096, 4, 1024, 0.1), (4097, 4, 1024, 0.1), (6554, 5, 257, 0.0)])
+def test_sort_many_slots(dev, tok, sel, n_expert, dropped):
+    """As test_sort, around and above the size from which chunks of slots are sorted in several launches; twice."""
+    import torch
+    rng = np.random.default_rng(tok + sel)
+    ids = np.minimum((n_expert * rng.random(tok * sel) ** 2).astype(np.int64), n_expert - 1)   # uneven
+    out = rng.random(tok * sel) < dropped
+    ids[out] = rng.choice([-1, -2 ** 31, n_expert, 2 ** 31 - 1], out.sum())
+    n, kept = tok * sel, (ids >= 0) & (ids < n_expert)
+    order = np.argsort(np.where(kept, ids, n_expert), kind="stable")
+    slots, pos = np.where(np.arange(n) < kept.sum(), order, -1), np.full(n, -1)
+    pos[order[:kept.sum()]] = np.arange(kept.sum())
+    offsets = np.searchsorted(ids[order[:kept.sum()]], np.arange(n_expert + 1))
+    bufs = [torch.full((m + 4,), 77, dtype=torch.int32, device=dev) for m in (n_expert + 1, n, n)]
+    for _ in range(2):
+        q.qgemv_expert_sort(dput(ids.astype(np.int32), dev).view(tok, sel), n_expert, *bufs)
+        for buf, ref in zip(bufs, (offsets, slots, pos)):
+            assert np.array_equal(buf.cpu().numpy(), np.concatenate([ref, [77] * 4]))
+
+
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("tok,sel,cols", [(1, 4, 2880), (5, 1, 1), (9, 2, 7), (33, 3, 64), (40, 4, 250), (20, 2, 2049)])
 def test_gather(dev, kind, tok, sel, cols):

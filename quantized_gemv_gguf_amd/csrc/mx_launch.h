@@ -27,7 +27,11 @@ struct Shape {
     if (tm < 1.0) tm = 1.0;
     double per_cu = active * tm * ((a.n - 1) / S::TN + 1) / 256.0;
     if (kWhole) per_cu = (double)(int64_t)(per_cu + 0.999);
-    return (kOne + (per_cu > 1.0 ? (per_cu - 1.0) * kMore : 0.0)) * a.nb;
+    // whole stages, and a workgroup's start and end (measured: the time of 0.3
+    // to 1.1 stages, of the largest 0.8 to 2.6)
+    constexpr double kEnds = kWhole ? 1.5 : 0.7;
+    const double length = ((a.nb + S::kBlk - 1) / S::kBlk + kEnds) / (128.0 / S::kBlk + kEnds);
+    return (kOne + (per_cu > 1.0 ? (per_cu - 1.0) * kMore : 0.0)) * length;
   }
   static hipError_t launch(const MxArgs &a, hipStream_t stream) {
     return launch_tile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>(a, stream);
@@ -35,10 +39,11 @@ struct Shape {
 };
 
 // The shape with the least estimated time.  Timed against every shape of its
-// kind for 25 problems each (1 to 4096 tokens, dense, and of 8 to 128 experts;
-// k = 2880 to 11008), the chosen one took at most 1.12 times the best, mostly
-// 1.00 to 1.03.  No one shape does: bf16 tokens, 5 x 11008 outputs of k = 4096,
-// 11 us in the smallest shape and 54 in the largest; 2048 x 8192, 786 and 133.
+// kind for 37 problems each (1 to 4096 tokens, dense, and of 8 to 147 experts;
+// k = 64 to 12480), the chosen one took 1.01 times the best (geometric mean; 1.3
+// to 1.4 in three calls of 9 to 17 us).  No one shape does: bf16 tokens, 5 x
+// 11008 outputs of k = 4096, 11 us in the smallest shape and 54 in the largest;
+// 2048 x 8192, 786 and 133.
 template <typename... Shapes>
 hipError_t launch_cheapest(const MxArgs &a, hipStream_t stream, bool *fits) {
   const double costs[] = {Shapes::cost(a)...};
@@ -55,7 +60,7 @@ template <int XK, bool PAIR> struct Shapes;
 template <> struct Shapes<kFp4, false> {
   static constexpr auto run = launch_cheapest<Shape<kFp4, false, 2, 1, 1, 1, 4, 4, 2, 52, 19, false>,
                                               Shape<kFp4, false, 2, 2, 1, 1, 4, 4, 2, 68, 28, false>,
-                                              Shape<kFp4, false, 2, 4, 2, 1, 2, 4, 1, 115, 66, false>,
+                                              Shape<kFp4, false, 2, 4, 2, 1, 2, 4, 1, 125, 62, false>,
                                               Shape<kFp4, false, 4, 4, 4, 2, 1, 2, 2, 285, 270, true>,
                                               Shape<kFp4, false, 4, 8, 4, 2, 1, 2, 2, 415, 430, true>>;
 };
@@ -70,7 +75,7 @@ template <> struct Shapes<kFp4, true> {
 template <> struct Shapes<kBf16, false> {
   static constexpr auto run = launch_cheapest<Shape<kBf16, false, 2, 1, 1, 1, 8, 8, 2, 72, 62, true>,
                                               Shape<kBf16, false, 2, 2, 4, 1, 1, 2, 1, 210, 130, false>,
-                                              Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 340, true>,
+                                              Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 365, true>,
                                               Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 560, 610, true>>;
 };
 template <> struct Shapes<kBf16, true> {
@@ -81,19 +86,19 @@ template <> struct Shapes<kBf16, true> {
                                               Shape<kBf16, true, 4, 3, 4, 2, 1, 1, 2, 770, 830, true>>;
 };
 template <> struct Shapes<kF16, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 1, 44, 24, false, true>,
+  static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 1, 44, 28, false, true>,
                                               Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 41, true, true>,
                                               Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 300, 195, false>,
-                                              Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 920, true>>;
+                                              Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 1080, true>>;
 };
 template <> struct Shapes<kF16, true> {
   static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 8, 8, 1, 66, 38, false, true>,
-                                              Shape<kF16, true, 1, 1, 2, 1, 4, 4, 1, 112, 58, false, true>,
-                                              Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 240, 180, false>,
+                                              Shape<kF16, true, 1, 1, 2, 1, 4, 4, 1, 118, 58, false, true>,
+                                              Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 296, 180, false>,
                                               Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
 };
 template <> struct Shapes<kF32, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 1, 44, 24, false, true>,
+  static constexpr auto run = launch_cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 1, 44, 28, false, true>,
                                               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 55, 40, true, true>,
                                               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 97, 115, true>,
                                               Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 145, false>,
@@ -104,9 +109,9 @@ template <> struct Shapes<kF32, true> {
   static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 1, 1, 8, 8, 1, 72, 42, false, true>,
                                               Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
                                               Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 125, 64, false, true>,
-                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 115, true>,
-                                              Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 260, 152, false>,
-                                              Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 410, 247, false>,
+                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 112, true>,
+                                              Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 305, 152, false>,
+                                              Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 435, 247, false>,
                                               Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>,
                                               Shape<kF32, true, 2, 1, 8, 2, 1, 1, 2, 750, 750, true>>;
 };

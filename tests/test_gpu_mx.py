@@ -108,7 +108,7 @@ def test_dequantize_every_code_and_scale(dev, kind):
 
 # tokens, rows, k: single values; one block; tails of the four blocks of a step; rows and tokens around the tiles
 SHAPES = [(1, 1, 32), (1, 2880, 2880), (2, 17, 64), (5, 70, 96), (16, 128, 128), (17, 129, 160), (33, 63, 2880),
-          (64, 65, 256), (65, 200, 544), (130, 257, 1024), (300, 130, 288), (513, 300, 416), (7, 40, 11008)]
+          (64, 65, 256), (65, 200, 544), (130, 257, 1024), (300, 130, 288), (513, 300, 416), (7, 40, 11008), (16, 8192, 2880)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "mxfp4"])
@@ -268,7 +268,7 @@ def test_rows_at_odd_addresses(dev, kind, tok, n, k):
 LARGE = [(2049, 130, 0), (700, 1030, 0), (2049, 1030, 0), (2049, 2050, 0), (700, 4100, 0), (65, 8200, 0),
          (200, 8200, 0), (700, 8200, 0), (129, 12300, 0), (200, 12300, 0), (700, 520, 3), (513, 12300, 3),
          (2049, 520, 3), (200, 8200, 8), (2049, 520, 40), (2049, 1030, 40), (90, 1030, 0), (23, 4100, 0), (33, 1030, 8),
-         (40, 2050, 3)]
+         (40, 2050, 3), (129, 2600, 0), (20, 2600, 0), (12, 2600, 0)]
 
 
 @pytest.mark.parametrize("pair", [False, True])

@@ -73,8 +73,9 @@ int qgemv_mx_quantize(const qg_tensor *x, const qg_matrix *q, qg_stream_t stream
 
 /* The values of rows [row_start, row_end) of q, rounded once to out's type
  * (out->n_rows = row_end - row_start, out->n_cols = q->k): exact in QG_F32
- * and QG_BF16 (6 * 2^127 and 4 * 2^127, above their range, give infinities),
- * rounded in QG_F16. */
+ * and QG_BF16 (but for magnitudes of 2^128 and more, which are above their range
+ * and give infinities: 2, 3, 4 and 6 at scale 254, 4 and 6 at 253), rounded in
+ * QG_F16. */
 int qgemv_mx_dequantize(const qg_matrix *q, int64_t row_start, int64_t row_end, const qg_tensor *out,
                         qg_stream_t stream);
 
@@ -83,13 +84,16 @@ int qgemv_mx_dequantize(const qg_matrix *q, int64_t row_start, int64_t row_end, 
  * taught us": tokens that share one pass over the weights cost about one
  * token's weight traffic).  x->n_cols = w->k; y->n_rows = x->n_rows, y->n_cols
  * = row_end - row_start, y a float type.  x may be
- *   QG_F32, QG_F16, QG_BF16  taken exactly: a weight is exact in bf16, and x
- *             is the exact sum of three, two or one bf16 terms (but for bits
- *             of QG_F32 below 2^-133, where bf16's subnormals end: cut off);
+ *   QG_F32, QG_F16, QG_BF16  taken exactly: a weight below 2^128 is exact in
+ *             bf16, and x is the exact sum of three, two or one bf16 terms (but
+ *             for bits of QG_F32 below 2^-133, where bf16's subnormals end: cut
+ *             off).  Rows with weights of 2^128 and more (scales 253 and 254,
+ *             which qgemv_mx_quantize never writes) are summed in 64 bits, and
+ *             slowly;
  *   QG_MXFP4  4-bit activations (qgemv_mx_quantize), codes and scales of both
  *             sides multiplied by the scaled 4-bit matrix instructions.
  * Products are exact, sums are fp32 in the matrix cores' order, y is rounded
- * once.  An output is the same for any stream and run; its order of sums may
+ * once (a sum past fp32's range is infinite).  An output is the same for any stream and run; its order of sums may
  * differ for another number of tokens.  Non-finite values follow IEEE
  * arithmetic of x times W, with the scale 255 as NaN.  No rows or no tokens
  * do nothing. */

@@ -17,7 +17,8 @@
 //             fp32 x is the exact sum of three bf16 terms (8 bits each,
 //             truncated, so no term rounds), fp16 of two, bf16 of one: every
 //             product is exact and only the fp32 sums round.  (Bits of fp32 x
-//             below 2^-133, the least bf16 subnormal, are cut off.)
+//             below 2^-133, the least bf16 subnormal, are cut off.)  Weights of
+//             2^128 and more, which bf16 does not hold: see huge_block.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -356,6 +357,36 @@ __device__ __forceinline__ float scale_of(uint32_t bytes, int f) {
   return __uint_as_float(((bytes >> (8 * f)) & 0xffu) << 23);
 }
 
+// Whether a block holds a value of 2^128 or more (codes 2, 3, 4 and 6 at scale
+// 254, 4 and 6 at 253), an infinity in bf16.
+__device__ __forceinline__ bool huge_block(const uint8_t *block) {
+  const int e = block[0];
+  if (e != 253 && e != 254) return false;
+  uint32_t any = 0;
+  for (int j = 1; j < 17; ++j) any |= e == 254 ? block[j] : block[j] & (block[j] << 1);  // codes' third bit (and second)
+  return any & 0x44u;
+}
+
+// One output from the values in memory, in 64 bits: nb blocks against a row of x.
+template <int XK>
+__device__ __forceinline__ float one_output(const uint8_t *w, const uint8_t *x, int nb) {
+  typedef std::conditional_t<XK == kF32, float, std::conditional_t<XK == kF16, _Float16, __bf16>> X;
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  double sum = 0.0;
+#pragma unroll 1
+  for (int b = 0; b < nb; ++b, w += 17, x += 32 * sizeof(X)) {
+    const uint64_t e = w[0];
+    const double scale = __builtin_bit_cast(double, (e == 255 ? 0x7ffull : e + 896) << 52 | (e == 255));
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+      const f2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[1 + j], 1.0f, 0);  // the low nibble's value and the high one's
+      sum = fma((double)((const X *)x)[j], v.x * scale, sum);
+      sum = fma((double)((const X *)x)[16 + j], v.y * scale, sum);
+    }
+  }
+  return (float)sum;
+}
+
 // f(integral_constant<0>) ... f(integral_constant<N - 1>)
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void each(F f) {
@@ -433,8 +464,13 @@ struct MxTile {
   static_assert(!COLS || (XK >= kF16 && FM == 1 && WM == 1), "columns of one fragment");
 };
 
+// Waves to a SIMD that the compiler has to leave registers for (0: its own
+// choice).  bf16 tokens in eight waves: three workgroups to a compute unit, by
+// itself it takes two registers more and leaves two.
+constexpr int waves(int xk, int wk) { return xk == kBf16 && wk == 4 ? 6 : 0; }
+
 template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS>
-__global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs a) {
+__global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kernel(const MxArgs a) {
   using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>;
   constexpr int TN = S::TN, TM = S::TM, NW = S::NW, NX = S::NX;
   __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
@@ -453,7 +489,8 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
   const int rows_left = a.n - tile.n0;
 
   // This thread's blocks of a stage: row tid / kBlk + kRowStep v of the tile,
-  // block tid % kBlk.  Rows past the matrix read its last row, tokens past the
+  // block tid % kBlk.  Rows past the matrix read the row of its last four that
+  // lies like them (of fewer than four rows the first), tokens past the
   // tile's end its first token; their sums are not stored.  A stage is a
   // multiple of four blocks and of four rows a step, so a thread's blocks all
   // start at the same byte of their first word.
@@ -462,8 +499,11 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
   const uint32_t wphase = (w_odd + (uint32_t)wrow * (uint32_t)a.row_bytes + wfirst) & 3u;
   uint32_t woff[NW];
 #pragma unroll
-  for (int v = 0; v < NW; ++v)
-    woff[v] = (w_odd + (uint32_t)min((wrow + S::kRowStep * v) % TN, rows_left - 1) * (uint32_t)a.row_bytes + wfirst) & ~3u;
+  for (int v = 0; v < NW; ++v) {
+    int row = (wrow + S::kRowStep * v) % TN;
+    if (row >= rows_left) row -= (row - rows_left + 4) & ~3;
+    woff[v] = (w_odd + (uint32_t)max(row, 0) * (uint32_t)a.row_bytes + wfirst) & ~3u;
+  }
   // A piece of x: a block (MXFP4), or a quarter of one (floats).
   const int xblk = XK == kFp4 ? wblk : (tid >> 2) % S::kBlk;
   const int xtok = XK == kFp4 ? wrow : (tid >> 2) / S::kBlk;
@@ -751,20 +791,81 @@ __global__ void __launch_bounds__(64 * WN * WM * WK) mx_tile_kernel(const MxArgs
   auto absent = [&](int p) {
     return a.slots && (uint32_t)(a.slots[p] < 0 ? -1 : a.slots[p] / a.n_sel) >= (uint32_t)a.x_rows;
   };
+  // the place of this lane's token m, or one past the tile's end
+  auto place = [&](int m) {
+    if (COLS) return i % S::kCols == 0 && i / S::kCols < TM ? tile.m0 + i / S::kCols : tile.m_end;
+    return tile.m0 + 16 * (wm * FM + m) + i;
+  };
+  const bool huge = XK != kFp4 && [&] {
+    // whether one of the wave's sums is an infinity or NaN (or their products
+    // pass fp32's range: then the rows are looked through for nothing)
+    float all = 0.0f;
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      float some = 0.0f;
+#pragma unroll
+      for (int u = 0; u < S::kMats; ++u)
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          const f32x4 v = acc[u][n][m];
+          some = fmaf(v.x, v.y, fmaf(v.z, v.w, some));
+        }
+      if (place(m) < tile.m_end) all += some;
+    }
+    return __ballot(!__builtin_isfinite(all)) != 0;
+  }();
   if constexpr (S::kRows) {
     if (a.y_type == QG_F32) store_rows<S, 4>(a, tile, lds, wn, wm, i, g, outputs, absent);
     else store_rows<S, 2>(a, tile, lds, wn, wm, i, g, outputs, absent);
+    if (XK != kFp4) __syncthreads();  // (other waves have stored these outputs)
   } else {
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
-      const int p = tile.m0 + (COLS ? i / S::kCols : 16 * (wm * FM + m) + i);
-      if (p >= tile.m_end || (COLS && (i % S::kCols != 0 || i / S::kCols >= TM))) continue;
+      const int p = place(m);
+      if (p >= tile.m_end) continue;
       const bool none = absent(p);
 #pragma unroll
       for (int n = 0; n < FN; ++n) {
         const int r = tile.n0 + 16 * (wn * FN + n) + 4 * g;
         const f32x4 v = outputs(n, m);
         if (r < a.n) store4(a, p, r, a.n - r, none ? f32x4{0, 0, 0, 0} : v);
+      }
+    }
+  }
+  if constexpr (XK != kFp4) {
+    // Weights of 2^128 and more were infinities above, so every token's sum of
+    // their row is one or NaN: such rows are found by that, and computed again
+    // one output a lane (slowly; no quantisation of fp32 values writes such
+    // scales, and without one a tile pays the check of its sums).
+    if (!huge) return;
+    constexpr int kTokens = COLS ? TM : 16 * FM;  // of this wave
+    const int p0 = tile.m0 + (COLS ? 0 : 16 * FM * wm), p1 = min(p0 + kTokens, tile.m_end);
+    // (lane and address anew: kept from the start they would cost the main loop registers)
+    const int64_t first = tile.expert * a.expert_bytes + (int64_t)__builtin_amdgcn_readfirstlane(tile.n0) * a.row_bytes;
+    const uint8_t *w = a.w + first, *w2 = PAIR ? a.w2 + first : nullptr;
+    const int here = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+#pragma unroll 1
+    for (int n = 0; n < FN; ++n) {
+      const int r0 = 16 * (wn * FN + n), row = r0 + (here & 15);
+      bool any = false;
+      if (row < rows_left)
+#pragma unroll 1
+        for (int b = here >> 4; b < a.nb; b += 4) {
+          const int64_t at_block = (int64_t)row * a.row_bytes + 17 * b;
+          any |= huge_block(w + at_block) || (PAIR && huge_block(w2 + at_block));
+        }
+      const uint64_t lanes = __ballot(any);
+      uint32_t rows = (uint32_t)(lanes | lanes >> 16 | lanes >> 32 | lanes >> 48) & 0xffffu;
+      for (; rows; rows &= rows - 1) {
+        const int r = r0 + __builtin_ctz(rows);
+#pragma unroll 1
+        for (int p = p0 + here; p < p1; p += 64) {
+          if (absent(p)) continue;
+          const uint8_t *x = a.x + (int64_t)(a.slots ? a.slots[p] / a.n_sel : p) * a.x_bytes;
+          float v = one_output<XK>(w + (int64_t)r * a.row_bytes, x, a.nb);
+          if (PAIR) v = silu_times(v, one_output<XK>(w2 + (int64_t)r * a.row_bytes, x, a.nb));
+          store4(a, p, tile.n0 + r, 1, f32x4{v, 0, 0, 0});
+        }
       }
     }
   }

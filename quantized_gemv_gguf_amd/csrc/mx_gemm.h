@@ -489,20 +489,21 @@ __global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kern
   const int rows_left = a.n - tile.n0;
 
   // This thread's blocks of a stage: row tid / kBlk + kRowStep v of the tile,
-  // block tid % kBlk.  Rows past the matrix read the row of its last four that
-  // lies like them (of fewer than four rows the first), tokens past the
-  // tile's end its first token; their sums are not stored.  A stage is a
-  // multiple of four blocks and of four rows a step, so a thread's blocks all
-  // start at the same byte of their first word.
+  // block tid % kBlk.  Rows past the matrix read one of its last four, tokens
+  // past the tile's end its first token; their sums are not stored.  A stage is
+  // a multiple of four blocks and of four rows a step, so a thread's blocks all
+  // start at the same byte of their first word, and rows past the matrix keep to
+  // rows that lie like them (wlike: of fewer than four rows, the first).
   const int wblk = tid % S::kBlk, wrow = tid / S::kBlk;
   const uint32_t wfirst = wblk < a.nb ? 17u * (uint32_t)wblk : 0u;
-  const uint32_t wphase = (w_odd + (uint32_t)wrow * (uint32_t)a.row_bytes + wfirst) & 3u;
+  const int wlike = (wrow & 3) < rows_left ? wrow : wrow & ~3;
+  const uint32_t wphase = (w_odd + (uint32_t)wlike * (uint32_t)a.row_bytes + wfirst) & 3u;
   uint32_t woff[NW];
 #pragma unroll
   for (int v = 0; v < NW; ++v) {
-    int row = (wrow + S::kRowStep * v) % TN;
+    int row = (wlike + S::kRowStep * v) % TN;
     if (row >= rows_left) row -= (row - rows_left + 4) & ~3;
-    woff[v] = (w_odd + (uint32_t)max(row, 0) * (uint32_t)a.row_bytes + wfirst) & ~3u;
+    woff[v] = (w_odd + (uint32_t)row * (uint32_t)a.row_bytes + wfirst) & ~3u;
   }
   // A piece of x: a block (MXFP4), or a quarter of one (floats).
   const int xblk = XK == kFp4 ? wblk : (tid >> 2) % S::kBlk;
@@ -837,7 +838,7 @@ __global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kern
     // their row is one or NaN: such rows are found by that, and computed again
     // one output a lane (slowly; no quantisation of fp32 values writes such
     // scales, and without one a tile pays the check of its sums).
-    if (!huge) return;
+    if (__builtin_expect(!huge, 1)) return;
     constexpr int kTokens = COLS ? TM : 16 * FM;  // of this wave
     const int p0 = tile.m0 + (COLS ? 0 : 16 * FM * wm), p1 = min(p0 + kTokens, tile.m_end);
     // (lane and address anew: kept from the start they would cost the main loop registers)

@@ -785,21 +785,28 @@ def qgemv_expert_sort(ids, n_expert: int, offsets, slots, pos, stream=None) -> N
                                    _i32s(pos, n, "pos"), _here_stream(stream)), "qgemv_expert_sort")
 
 
-def _expert_args(x, n_expert: int, offsets, y, slots, n_sel: int):
+def _expert_args(x, n_expert: int, offsets, y, slots, n_sel):
     yt = _rows(y, "y")
-    return (ctypes.byref(_rows(x, "x")), _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"),
-            _i32s(slots, yt.n_rows, "slots") if slots is not None else None, int(n_sel), ctypes.byref(yt))
+    if slots is None:
+        sp, n_sel = None, 1
+    elif n_sel is None:
+        raise ValueError("slots need n_sel, the choices of a token that the sort was given")
+    else:
+        sp = _i32s(slots, yt.n_rows, "slots")
+    return (ctypes.byref(_rows(x, "x")), _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"), sp, int(n_sel),
+            ctypes.byref(yt))
 
 
-def qgemv_expert_mx(w: Matrix, n_expert: int, x, offsets, y, slots=None, n_sel: int = 1, stream=None) -> None:
+def qgemv_expert_mx(w: Matrix, n_expert: int, x, offsets, y, slots=None, n_sel=None, stream=None) -> None:
     """y[p] = W_e . x[src] for the sorted places p of every expert e; src =
-    slots[p] // n_sel, or p without ``slots``.  Rows of y behind the last place stay."""
+    slots[p] // n_sel (required with ``slots``), or p without ``slots``.  Rows
+    of y behind the last place stay."""
     xt, op, sp, ns, yt = _expert_args(x, n_expert, offsets, y, slots, n_sel)
     _check(lib().qgemv_expert_mx(ctypes.byref(_blocks(w, "w")), int(n_expert), xt, op, sp, ns, yt,
                                  _here_stream(stream)), "qgemv_expert_mx")
 
 
-def qgemv_expert_mx_swiglu(gate: Matrix, up: Matrix, n_expert: int, x, offsets, h, slots=None, n_sel: int = 1,
+def qgemv_expert_mx_swiglu(gate: Matrix, up: Matrix, n_expert: int, x, offsets, h, slots=None, n_sel=None,
                            stream=None) -> None:
     """h[p] = silu(gate_e . x[src]) * (up_e . x[src]), as qgemv_expert_mx."""
     xt, op, sp, ns, ht = _expert_args(x, n_expert, offsets, h, slots, n_sel)

@@ -1,0 +1,37 @@
+"""What the binding of include/qgemv_mx.h refuses on the host (no GPU)."""
+from __future__ import annotations
+
+import pytest
+
+import quantized_gemv_gguf_amd as q
+
+
+@pytest.fixture
+def on_device(monkeypatch):
+    """CPU tensors pass for device tensors; the calls below are refused before any of them is used."""
+    torch = pytest.importorskip("torch")
+    q._torch_names()
+    monkeypatch.setattr(q, "_here", lambda t, name: 0x1000)
+    monkeypatch.setattr(q, "_here_stream", lambda stream: 0)
+    return torch
+
+
+def matrix(torch, rows, k):
+    return q.Matrix(torch.zeros(rows * (k // 32) * 17, dtype=torch.uint8), q.MXFP4, rows, k)
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_slots_need_the_number_of_choices(on_device, pair):
+    """Without it a slot would be taken for a token."""
+    torch = on_device
+    x, y = torch.zeros(4, 64), torch.zeros(8, 8)
+    offsets, slots = torch.zeros(3, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    ws = [matrix(torch, 16, 64)] * (1 + pair)
+    call = q.qgemv_expert_mx_swiglu if pair else q.qgemv_expert_mx
+    with pytest.raises(ValueError, match="n_sel"):
+        call(*ws, 2, x, offsets, y, slots=slots)
+    with pytest.raises(q.QgemvError, match="QG_E_ARG"):
+        call(*ws, 2, x, offsets, y, slots=slots, n_sel=0)
+    # without slots the number is not looked at: four rows of x for eight places
+    with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+        call(*ws, 2, x, offsets, y)

@@ -747,6 +747,14 @@ def _weights(t, n: int, name: str) -> int:
     return _array(t, n, name, _float32, "float32")
 
 
+def _per_choice(t, pos, name: str) -> int:
+    """The address of one float32 per (token, choice) of ``pos``: flat, or of rows of as many choices."""
+    n_tok, n_sel = pos.shape
+    if t.dim() > 1 and t.shape[-1] != n_sel and n_tok > 1 and n_sel > 1:
+        raise ValueError(f"{name} must be (tokens, choices)")
+    return _weights(t, n_tok * n_sel, name)
+
+
 def qgemv_mx_quantize(x, q: Matrix, stream=None) -> None:
     """Quantises the rows of ``x`` into the MXFP4 blocks of ``q`` (n_rows x k of x's shape)."""
     _check(lib().qgemv_mx_quantize(ctypes.byref(_rows(x, "x")), ctypes.byref(_blocks(q, "q")), _here_stream(stream)),
@@ -827,9 +835,8 @@ def qgemv_expert_combine(y, pos, out, w=None, stream=None) -> None:
     gather's gradient).  ``pos`` and ``w`` are (tokens, choices)."""
     if pos.dim() != 2 or pos.shape[0] != out.shape[0]:
         raise ValueError("pos must be (tokens, choices) with out's tokens")
-    n = pos.numel()
-    _check(lib().qgemv_expert_combine(ctypes.byref(_rows(y, "y")), _i32s(pos, n, "pos"),
-                                      _weights(w, n, "w") if w is not None else None, pos.shape[1],
+    _check(lib().qgemv_expert_combine(ctypes.byref(_rows(y, "y")), _i32s(pos, pos.numel(), "pos"),
+                                      _per_choice(w, pos, "w") if w is not None else None, pos.shape[1],
                                       ctypes.byref(_rows(out, "out")), _here_stream(stream)), "qgemv_expert_combine")
 
 
@@ -838,10 +845,10 @@ def qgemv_expert_combine_grad(dout, y, pos, w, dy, dw, stream=None) -> None:
     dw[t, s] = <dout[t], y[pos[t, s]]> (float32)."""
     if pos.dim() != 2 or pos.shape[0] != dout.shape[0]:
         raise ValueError("pos must be (tokens, choices) with dout's tokens")
-    n = pos.numel()
     _check(lib().qgemv_expert_combine_grad(ctypes.byref(_rows(dout, "dout")), ctypes.byref(_rows(y, "y")),
-                                           _i32s(pos, n, "pos"), _weights(w, n, "w"), pos.shape[1],
-                                           ctypes.byref(_rows(dy, "dy")), _weights(dw, n, "dw"), _here_stream(stream)),
+                                           _i32s(pos, pos.numel(), "pos"), _per_choice(w, pos, "w"), pos.shape[1],
+                                           ctypes.byref(_rows(dy, "dy")), _per_choice(dw, pos, "dw"),
+                                           _here_stream(stream)),
            "qgemv_expert_combine_grad")
 
 

@@ -35,3 +35,24 @@ def test_slots_need_the_number_of_choices(on_device, pair):
     # without slots the number is not looked at: four rows of x for eight places
     with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
         call(*ws, 2, x, offsets, y)
+
+
+def test_weights_by_choice_are_not_taken_transposed(on_device):
+    """(choices, tokens) holds as many values as (tokens, choices)."""
+    torch = on_device
+    tok, sel = 6, 4
+    y, out = torch.zeros(tok * sel, 8), torch.zeros(tok, 7)  # (7 columns: refused by the library after the binding)
+    pos, w = torch.zeros(tok, sel, dtype=torch.int32), torch.zeros(tok, sel)
+    wrong = torch.zeros(sel, tok)
+    with pytest.raises(ValueError, match="choices"):
+        q.qgemv_expert_combine(y, pos, out, w=wrong)
+    with pytest.raises(ValueError, match="choices"):
+        q.qgemv_expert_combine_grad(out, y, pos, wrong, torch.zeros_like(y), w)
+    with pytest.raises(ValueError, match="choices"):
+        q.qgemv_expert_combine_grad(out, y, pos, w, torch.zeros_like(y), wrong)
+    for fine in (None, w, w.flatten(), torch.zeros(tok + 3, sel)):
+        with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+            q.qgemv_expert_combine(y, pos, out, w=fine)
+    for fine in (w, w.flatten()):
+        with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+            q.qgemv_expert_combine_grad(out, y, pos, fine, torch.zeros_like(y), w)

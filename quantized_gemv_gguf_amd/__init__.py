@@ -747,6 +747,12 @@ def _weights(t, n: int, name: str) -> int:
     return _array(t, n, name, _float32, "float32")
 
 
+def _n_sel(n) -> int:
+    """A number of choices for a C int: past 32 bits, where ctypes would cut it, the largest, which is refused or
+    makes every slot the first token's as the number itself would."""
+    return max(min(int(n), 0x7fffffff), -1)
+
+
 def _per_choice(t, pos, name: str) -> int:
     """The address of one float32 per (token, choice) of ``pos``: flat, or of rows of as many choices."""
     n_tok, n_sel = pos.shape
@@ -788,7 +794,7 @@ def qgemv_expert_sort(ids, n_expert: int, offsets, slots, pos, stream=None) -> N
         raise ValueError("ids must be (tokens, choices)")
     n_tok, n_sel = ids.shape
     n = n_tok * n_sel
-    _check(lib().qgemv_expert_sort(_i32s(ids, n, "ids"), n_tok, n_sel, int(n_expert),
+    _check(lib().qgemv_expert_sort(_i32s(ids, n, "ids"), n_tok, _n_sel(n_sel), int(n_expert),
                                    _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"), _i32s(slots, n, "slots"),
                                    _i32s(pos, n, "pos"), _here_stream(stream)), "qgemv_expert_sort")
 
@@ -801,7 +807,7 @@ def _expert_args(x, n_expert: int, offsets, y, slots, n_sel):
         raise ValueError("slots need n_sel, the choices of a token that the sort was given")
     else:
         sp = _i32s(slots, yt.n_rows, "slots")
-    return (ctypes.byref(_rows(x, "x")), _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"), sp, int(n_sel),
+    return (ctypes.byref(_rows(x, "x")), _i32s(offsets, max(int(n_expert), 0) + 1, "offsets"), sp, _n_sel(n_sel),
             ctypes.byref(yt))
 
 
@@ -826,7 +832,7 @@ def qgemv_expert_mx_swiglu(gate: Matrix, up: Matrix, n_expert: int, x, offsets, 
 def qgemv_expert_gather(x, slots, n_sel: int, out, stream=None) -> None:
     """out[p] = x[slots[p] // n_sel]; rows with a negative slot stay."""
     ot = _rows(out, "out")
-    _check(lib().qgemv_expert_gather(ctypes.byref(_rows(x, "x")), _i32s(slots, ot.n_rows, "slots"), int(n_sel),
+    _check(lib().qgemv_expert_gather(ctypes.byref(_rows(x, "x")), _i32s(slots, ot.n_rows, "slots"), _n_sel(n_sel),
                                      ctypes.byref(ot), _here_stream(stream)), "qgemv_expert_gather")
 
 
@@ -836,7 +842,7 @@ def qgemv_expert_combine(y, pos, out, w=None, stream=None) -> None:
     if pos.dim() != 2 or pos.shape[0] != out.shape[0]:
         raise ValueError("pos must be (tokens, choices) with out's tokens")
     _check(lib().qgemv_expert_combine(ctypes.byref(_rows(y, "y")), _i32s(pos, pos.numel(), "pos"),
-                                      _per_choice(w, pos, "w") if w is not None else None, pos.shape[1],
+                                      _per_choice(w, pos, "w") if w is not None else None, _n_sel(pos.shape[1]),
                                       ctypes.byref(_rows(out, "out")), _here_stream(stream)), "qgemv_expert_combine")
 
 
@@ -846,7 +852,7 @@ def qgemv_expert_combine_grad(dout, y, pos, w, dy, dw, stream=None) -> None:
     if pos.dim() != 2 or pos.shape[0] != dout.shape[0]:
         raise ValueError("pos must be (tokens, choices) with dout's tokens")
     _check(lib().qgemv_expert_combine_grad(ctypes.byref(_rows(dout, "dout")), ctypes.byref(_rows(y, "y")),
-                                           _i32s(pos, pos.numel(), "pos"), _per_choice(w, pos, "w"), pos.shape[1],
+                                           _i32s(pos, pos.numel(), "pos"), _per_choice(w, pos, "w"), _n_sel(pos.shape[1]),
                                            ctypes.byref(_rows(dy, "dy")), _per_choice(dw, pos, "dw"),
                                            _here_stream(stream)),
            "qgemv_expert_combine_grad")

@@ -56,3 +56,23 @@ def test_weights_by_choice_are_not_taken_transposed(on_device):
     for fine in (w, w.flatten()):
         with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
             q.qgemv_expert_combine_grad(out, y, pos, fine, torch.zeros_like(y), w)
+
+
+def test_choices_past_32_bits(on_device):
+    """Numbers of choices that a C int does not hold are refused, not cut to their low bits."""
+    torch = on_device
+    n = 2 ** 32 + 1
+    many = torch.empty((1, n), dtype=torch.int32, device="meta")
+    with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+        q.qgemv_expert_sort(many, 2, torch.zeros(3, dtype=torch.int32), many, many)
+    y, out, w = torch.zeros(8, 8), torch.zeros(1, 8), torch.empty((1, n), device="meta")
+    with pytest.raises(q.QgemvError, match="QG_E_SHAPE"):
+        q.qgemv_expert_combine(y, many, out, w=w)
+    with pytest.raises(q.QgemvError, match="QG_E_SHAPE|QG_E_ARG"):
+        q.qgemv_expert_combine_grad(out, y, many, w, y, w)
+    slots = torch.zeros(8, dtype=torch.int32)
+    for bad in (-2 ** 32 + 1, -1, 0):
+        with pytest.raises(q.QgemvError, match="QG_E_ARG"):
+            q.qgemv_expert_gather(y, slots, bad, y)
+        with pytest.raises(q.QgemvError, match="QG_E_ARG"):
+            q.qgemv_expert_mx(matrix(torch, 16, 64), 2, torch.zeros(4, 64), slots, y, slots=slots, n_sel=bad)

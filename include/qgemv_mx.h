@@ -6,8 +6,8 @@
  * conventions, which hold here too (host-side validation before any HIP call,
  * a refused call enqueues nothing and leaves every output untouched, caller's
  * memory and stream, no waiting, no allocation, re-entrant calls, safe under
- * stream capture).  The caller's current device must be the buffers' and the
- * stream's device.
+ * stream capture), but for the products' order of sums (see qgemv_rows_mx).
+ * The caller's current device must be the buffers' and the stream's device.
  *
  * A prompt through a mixture of experts whose weights stay in their GGUF
  * blocks (neurostream README, "How it works": the router names the experts,
@@ -93,8 +93,10 @@ int qgemv_mx_dequantize(const qg_matrix *q, int64_t row_start, int64_t row_end, 
  *   QG_MXFP4  4-bit activations (qgemv_mx_quantize), codes and scales of both
  *             sides multiplied by the scaled 4-bit matrix instructions.
  * Products are exact, sums are fp32 in the matrix cores' order, y is rounded
- * once (a sum past fp32's range is infinite).  An output is the same for any stream and run; its order of sums may
- * differ for another number of tokens.  Non-finite values follow IEEE
+ * once (a sum past fp32's range is infinite).  An output is the same for any stream and run, and for windows of as
+ * many rows wherever they begin; unlike the calls of qgemv.h, its order of sums
+ * may differ for another number of tokens or of rows in the window, by which
+ * the kernel is chosen.  Non-finite values follow IEEE
  * arithmetic of x times W, with the scale 255 as NaN.  No rows or no tokens
  * do nothing. */
 int qgemv_rows_mx(const qg_matrix *w, int64_t row_start, int64_t row_end, const qg_tensor *x, const qg_tensor *y,
@@ -129,7 +131,9 @@ int qgemv_expert_sort(const int32_t *ids, int64_t n_tok, int32_t n_sel, int64_t 
  * Each weight is read once per tile of its expert's places; experts without a
  * token cost nothing.  Rows of y behind the last offset stay as they were.
  * Offsets are clamped to [0, y->n_rows]; a src outside x's rows gives a
- * row of zeros.  x, y and arithmetic as qgemv_rows_mx. */
+ * row of zeros.  x, y and arithmetic as qgemv_rows_mx; the order of sums may
+ * differ for another number of places, experts or rows of one, but does not
+ * depend on how the places are shared out. */
 int qgemv_expert_mx(const qg_matrix *w, int64_t n_expert, const qg_tensor *x, const int32_t *offsets,
                     const int32_t *slots, int32_t n_sel, const qg_tensor *y, qg_stream_t stream);
 

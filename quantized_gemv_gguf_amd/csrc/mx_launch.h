@@ -38,83 +38,94 @@ struct Shape {
   }
 };
 
-// The shape with the least estimated time.  Timed against every shape of its
-// kind for 37 problems each (1 to 4096 tokens, dense, and of 8 to 147 experts;
-// k = 64 to 12480), the chosen one took 1.01 times the best (geometric mean; 1.3
-// to 1.4 in three calls of 9 to 17 us).  No one shape does: bf16 tokens, 5 x
+// Of several shapes the one with the least estimated time.  Timed against every
+// shape of its kind for 37 problems each (1 to 4096 tokens, dense, and of 8 to 147
+// experts; k = 64 to 12480), the chosen one took 1.01 times the best (geometric
+// mean; 1.3 to 1.4 in three calls of 9 to 17 us).  No one shape does: bf16 tokens, 5 x
 // 11008 outputs of k = 4096, 11 us in the smallest shape and 54 in the largest;
 // 2048 x 8192, 786 and 133.
-template <typename... Shapes>
-hipError_t launch_cheapest(const MxArgs &a, hipStream_t stream, bool *fits) {
-  const double costs[] = {Shapes::cost(a)...};
-  hipError_t (*const launches[])(const MxArgs &, hipStream_t) = {Shapes::launch...};
-  int best = 0;
-  for (int i = 1; i < (int)sizeof...(Shapes); ++i)
-    if (costs[i] < costs[best]) best = i;
-  *fits = costs[best] < kNever;
-  return *fits ? launches[best](a, stream) : hipSuccess;
-}
+template <typename... Of>
+struct Cheapest {
+  static constexpr int kShapes = sizeof...(Of);
+  static int best(const MxArgs &a) {  // -1 if no shape's grid holds the product
+    const double costs[] = {Of::cost(a)...};
+    int at = 0;
+    for (int i = 1; i < kShapes; ++i)
+      if (costs[i] < costs[at]) at = i;
+    return costs[at] < kNever ? at : -1;
+  }
+  static int stage_blocks(int shape) {  // blocks of a row that a stage takes
+    const int blocks[] = {Of::S::kBlk...};
+    return blocks[shape];
+  }
+  static hipError_t run(const MxArgs &a, hipStream_t stream, bool *fits) {
+    hipError_t (*const launches[])(const MxArgs &, hipStream_t) = {Of::launch...};
+    const int shape = best(a);
+    *fits = shape >= 0;
+    return *fits ? launches[shape](a, stream) : hipSuccess;
+  }
+};
 
 template <int XK, bool PAIR> struct Shapes;
 
-template <> struct Shapes<kFp4, false> {
-  static constexpr auto run = launch_cheapest<Shape<kFp4, false, 2, 1, 1, 1, 4, 4, 2, 52, 19, false>,
-                                              Shape<kFp4, false, 2, 2, 1, 1, 4, 4, 2, 68, 28, false>,
-                                              Shape<kFp4, false, 2, 4, 2, 1, 2, 4, 1, 125, 62, false>,
-                                              Shape<kFp4, false, 4, 4, 4, 2, 1, 2, 2, 285, 270, true>,
-                                              Shape<kFp4, false, 4, 8, 4, 2, 1, 2, 2, 415, 430, true>>;
-};
-template <> struct Shapes<kFp4, true> {
-  static constexpr auto run = launch_cheapest<Shape<kFp4, true, 1, 1, 1, 1, 4, 4, 2, 60, 23, false>,
-                                              Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 25, false>,
-                                              Shape<kFp4, true, 1, 4, 2, 1, 2, 4, 1, 115, 56, false>,
-                                              Shape<kFp4, true, 1, 4, 4, 1, 1, 2, 1, 160, 97, false>,
-                                              Shape<kFp4, true, 2, 4, 4, 2, 1, 2, 2, 270, 275, true>,
-                                              Shape<kFp4, true, 2, 8, 4, 2, 1, 2, 2, 445, 450, true>>;
-};
-template <> struct Shapes<kBf16, false> {
-  static constexpr auto run = launch_cheapest<Shape<kBf16, false, 2, 1, 1, 1, 8, 8, 2, 72, 62, true>,
-                                              Shape<kBf16, false, 2, 2, 4, 1, 1, 2, 1, 210, 130, false>,
-                                              Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 365, true>,
-                                              Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 560, 610, true>>;
-};
-template <> struct Shapes<kBf16, true> {
-  static constexpr auto run = launch_cheapest<Shape<kBf16, true, 1, 1, 1, 1, 8, 8, 2, 62, 60, true>,
-                                              Shape<kBf16, true, 1, 1, 2, 1, 4, 4, 1, 88, 60, false>,
-                                              Shape<kBf16, true, 1, 2, 4, 1, 1, 2, 1, 200, 120, false>,
-                                              Shape<kBf16, true, 2, 2, 8, 2, 1, 1, 2, 620, 670, true>,
-                                              Shape<kBf16, true, 4, 3, 4, 2, 1, 1, 2, 770, 830, true>>;
-};
-template <> struct Shapes<kF16, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 1, 44, 28, false, true>,
-                                              Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 41, true, true>,
-                                              Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 300, 195, false>,
-                                              Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 1080, true>>;
-};
-template <> struct Shapes<kF16, true> {
-  static constexpr auto run = launch_cheapest<Shape<kF16, true, 1, 1, 1, 1, 8, 8, 1, 66, 38, false, true>,
-                                              Shape<kF16, true, 1, 1, 2, 1, 4, 4, 1, 118, 58, false, true>,
-                                              Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 296, 180, false>,
-                                              Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>>;
-};
-template <> struct Shapes<kF32, false> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 1, 44, 28, false, true>,
-                                              Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 55, 40, true, true>,
-                                              Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 97, 115, true>,
-                                              Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 145, false>,
-                                              Shape<kF32, false, 4, 2, 4, 2, 1, 1, 2, 850, 850, true>,
-                                              Shape<kF32, false, 4, 2, 8, 2, 1, 1, 1, 1250, 1350, true>>;
-};
-template <> struct Shapes<kF32, true> {
-  static constexpr auto run = launch_cheapest<Shape<kF32, true, 1, 1, 1, 1, 8, 8, 1, 72, 42, false, true>,
-                                              Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
-                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 125, 64, false, true>,
-                                              Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 112, true>,
-                                              Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 305, 152, false>,
-                                              Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 435, 247, false>,
-                                              Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>,
-                                              Shape<kF32, true, 2, 1, 8, 2, 1, 1, 2, 750, 750, true>>;
-};
+template <>
+struct Shapes<kFp4, false>
+    : Cheapest<Shape<kFp4, false, 2, 1, 1, 1, 4, 4, 2, 52, 19, false>,
+               Shape<kFp4, false, 2, 2, 1, 1, 4, 4, 2, 68, 28, false>,
+               Shape<kFp4, false, 2, 4, 2, 1, 2, 4, 1, 125, 62, false>,
+               Shape<kFp4, false, 4, 4, 4, 2, 1, 2, 2, 285, 270, true>,
+               Shape<kFp4, false, 4, 8, 4, 2, 1, 2, 2, 415, 430, true>> {};
+template <>
+struct Shapes<kFp4, true>
+    : Cheapest<Shape<kFp4, true, 1, 1, 1, 1, 4, 4, 2, 60, 23, false>,
+               Shape<kFp4, true, 1, 2, 1, 1, 4, 4, 2, 65, 25, false>,
+               Shape<kFp4, true, 1, 4, 2, 1, 2, 4, 1, 115, 56, false>,
+               Shape<kFp4, true, 1, 4, 4, 1, 1, 2, 1, 160, 97, false>,
+               Shape<kFp4, true, 2, 4, 4, 2, 1, 2, 2, 270, 275, true>,
+               Shape<kFp4, true, 2, 8, 4, 2, 1, 2, 2, 445, 450, true>> {};
+template <>
+struct Shapes<kBf16, false>
+    : Cheapest<Shape<kBf16, false, 2, 1, 1, 1, 8, 8, 2, 72, 62, true>,
+               Shape<kBf16, false, 2, 2, 4, 1, 1, 2, 1, 210, 130, false>,
+               Shape<kBf16, false, 2, 4, 8, 1, 1, 1, 2, 335, 365, true>,
+               Shape<kBf16, false, 4, 4, 4, 2, 1, 1, 2, 560, 610, true>> {};
+template <>
+struct Shapes<kBf16, true>
+    : Cheapest<Shape<kBf16, true, 1, 1, 1, 1, 8, 8, 2, 62, 60, true>,
+               Shape<kBf16, true, 1, 1, 2, 1, 4, 4, 1, 88, 60, false>,
+               Shape<kBf16, true, 1, 2, 4, 1, 1, 2, 1, 200, 120, false>,
+               Shape<kBf16, true, 2, 2, 8, 2, 1, 1, 2, 620, 670, true>,
+               Shape<kBf16, true, 4, 3, 4, 2, 1, 1, 2, 770, 830, true>> {};
+template <>
+struct Shapes<kF16, false>
+    : Cheapest<Shape<kF16, false, 1, 1, 1, 1, 8, 8, 1, 44, 28, false, true>,
+               Shape<kF16, false, 2, 1, 1, 1, 8, 8, 1, 52, 41, true, true>,
+               Shape<kF16, false, 2, 2, 4, 1, 1, 2, 1, 300, 195, false>,
+               Shape<kF16, false, 8, 2, 4, 2, 1, 1, 2, 900, 1080, true>> {};
+template <>
+struct Shapes<kF16, true>
+    : Cheapest<Shape<kF16, true, 1, 1, 1, 1, 8, 8, 1, 66, 38, false, true>,
+               Shape<kF16, true, 1, 1, 2, 1, 4, 4, 1, 118, 58, false, true>,
+               Shape<kF16, true, 1, 2, 4, 1, 1, 2, 1, 296, 180, false>,
+               Shape<kF16, true, 2, 4, 8, 1, 1, 1, 2, 1000, 1000, true>> {};
+template <>
+struct Shapes<kF32, false>
+    : Cheapest<Shape<kF32, false, 1, 1, 1, 1, 8, 8, 1, 44, 28, false, true>,
+               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 55, 40, true, true>,
+               Shape<kF32, false, 2, 1, 1, 1, 8, 8, 1, 97, 115, true>,
+               Shape<kF32, false, 2, 1, 4, 1, 1, 2, 1, 260, 145, false>,
+               Shape<kF32, false, 4, 2, 4, 2, 1, 1, 2, 850, 850, true>,
+               Shape<kF32, false, 4, 2, 8, 2, 1, 1, 1, 1250, 1350, true>> {};
+template <>
+struct Shapes<kF32, true>
+    : Cheapest<Shape<kF32, true, 1, 1, 1, 1, 8, 8, 1, 72, 42, false, true>,
+               Shape<kF32, true, 1, 1, 1, 1, 4, 4, 1, 80, 36, false, true>,
+               Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 125, 64, false, true>,
+               Shape<kF32, true, 1, 1, 2, 1, 4, 4, 1, 130, 112, true>,
+               Shape<kF32, true, 1, 1, 4, 1, 1, 2, 1, 305, 152, false>,
+               Shape<kF32, true, 1, 2, 4, 1, 1, 1, 1, 435, 247, false>,
+               Shape<kF32, true, 2, 2, 4, 2, 1, 1, 2, 730, 730, true>,
+               Shape<kF32, true, 2, 1, 8, 2, 1, 1, 2, 750, 750, true>> {};
 
 template <int XK>
 hipError_t launch_mx(const MxArgs &a, hipStream_t stream, bool *fits) {

@@ -21,6 +21,7 @@ HEADERS = ["qgemv_impl.h"]
 # mx.hip: the C ABI of qgemv_mx.h, quantisation and routing; the products of one
 # activation type each.
 MX_SOURCES = ["mx.hip", "mx_f32.hip", "mx_f16.hip", "mx_bf16.hip", "mx_fp4.hip"]
+MX_HEADERS = ["mx_gemm.h", "mx_launch.h"]
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqgemv.so")
 ARCH = "gfx950"
@@ -49,6 +50,11 @@ def source_paths():
     """Every file the GEMV kernels are built from (hashed by bench.py to tie HBM
     counter summaries to the code they were taken on)."""
     return [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+
+
+def mx_source_paths():
+    """Every file the MXFP4 prompt operators are built from (their profile names its hash)."""
+    return [os.path.join(CSRC, f) for f in MX_SOURCES + MX_HEADERS]
 
 
 def build(verbose: bool = False) -> str:

@@ -103,7 +103,8 @@ int qgemv_rows_mx(const qg_matrix *w, int64_t row_start, int64_t row_end, const 
                   qg_stream_t stream);
 
 /* h[t] = silu(gate[rows] . x[t]) * (up[rows] . x[t]), both products and the
- * SiLU (qgemv_silu_mul's) in fp32, rounded once.  gate and up match in n_rows
+ * SiLU in fp32 (qgemv_silu_mul's; below -87.3, where silu is less than 2^-119
+ * in magnitude, it gives 0), rounded once.  gate and up match in n_rows
  * and k (else QG_E_SHAPE); otherwise as qgemv_rows_mx. */
 int qgemv_rows_mx_swiglu(const qg_matrix *gate, const qg_matrix *up, int64_t row_start, int64_t row_end,
                          const qg_tensor *x, const qg_tensor *h, qg_stream_t stream);

@@ -362,8 +362,8 @@ __device__ __forceinline__ float scale_of(uint32_t bytes, int f) {
 __device__ __forceinline__ bool huge_block(const uint8_t *block) {
   const int e = block[0];
   if (e != 253 && e != 254) return false;
-  uint32_t any = 0;
-  for (int j = 1; j < 17; ++j) any |= e == 254 ? block[j] : block[j] & (block[j] << 1);  // codes' third bit (and second)
+  uint32_t any = 0;  // third bit of each code: that, or that and the second
+  for (int j = 1; j < 17; ++j) any |= e == 254 ? block[j] : block[j] & (block[j] << 1);
   return any & 0x44u;
 }
 
@@ -379,7 +379,7 @@ __device__ __forceinline__ float one_output(const uint8_t *w, const uint8_t *x, 
     const double scale = __builtin_bit_cast(double, (e == 255 ? 0x7ffull : e + 896) << 52 | (e == 255));
 #pragma unroll 4
     for (int j = 0; j < 16; ++j) {
-      const f2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[1 + j], 1.0f, 0);  // the low nibble's value and the high one's
+      const f2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[1 + j], 1.0f, 0);  // low nibble, high nibble
       sum = fma((double)((const X *)x)[j], v.x * scale, sum);
       sum = fma((double)((const X *)x)[16 + j], v.y * scale, sum);
     }
@@ -413,18 +413,18 @@ __device__ __forceinline__ void each(F f) {
 // the planes of words 64 bytes apart beyond their 1 KB so that a token's
 // sixteen pieces are written to sixteen bank groups.
 //
-// What bounds it.  MXFP4 tokens, 4096 x 24576 outputs of k = 6144: 410 us, 3.0
-// PFLOP/s (a bf16 library product of 8192^3 runs at 1.1).  LDS is busy for 61%
-// of that, the matrix cores for 36%, and 5.2 GB pass from L2 to the compute
+// What bounds it.  MXFP4 tokens, 4096 x 24576 outputs of k = 6144: 385 to 425 us,
+// 2.9 to 3.2 PFLOP/s (a bf16 library product of 8192^3 runs at 1.1).  LDS is busy
+// for 61% of that, the matrix cores for 36%, and 5.2 GB pass from L2 to the compute
 // units, 13 TB/s: a stage's 136 bytes of a row are two lines of 128, of which
 // the next stage fetches one again (stages of 128 values: 7.2 GB).  bf16 tokens,
-// 2048 x 8192 outputs of k = 4096: 127 us, 1.1 PFLOP/s, a library product's
-// rate.  fp32 tokens take three times the matrix instructions, 268 us.  4096
-// MXFP4 tokens x 4 of 128 experts, pair of 2880 x 2880: 520 us, LDS 42% busy
-// and 4.9 GB from L2; a sixth of it is the weights' way from memory (470 us
-// instead of 570, in another shape, with one expert's weights for all).  Few
-// tokens: the blocks' latency and, for fp32, the terms, which every workgroup
-// makes anew.
+// 2048 x 8192 outputs of k = 4096: 123 to 137 us, 1.0 to 1.1 PFLOP/s, a library
+// product's rate.  fp32 tokens take three times the matrix instructions, 270 to
+// 300 us.  4096 MXFP4 tokens x 4 of 128 experts, pair of 2880 x 2880: 530
+// us, LDS 42% busy and 4.9 GB from L2; a sixth of it is the weights' way from
+// memory (470 us instead of 570, in another shape, with one expert's weights for
+// all).  Few tokens: the blocks' latency and, for fp32, the terms, which every
+// workgroup makes anew.
 template <int XK, bool PAIR, int FN, int FM, int WN, int WM, int WK, int KS, int NBUF, bool COLS = false>
 struct MxTile {
   static constexpr int kThreads = 64 * WN * WM * WK;
@@ -489,22 +489,17 @@ __global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kern
   const int rows_left = a.n - tile.n0;
 
   // This thread's blocks of a stage: row tid / kBlk + kRowStep v of the tile,
-  // block tid % kBlk.  Rows past the matrix read one of its last four, tokens
-  // past the tile's end its first token; their sums are not stored.  A stage is
-  // a multiple of four blocks and of four rows a step, so a thread's blocks all
-  // start at the same byte of their first word, and rows past the matrix keep to
-  // rows that lie like them (wlike: of fewer than four rows, the first).
+  // block tid % kBlk.  Rows past the matrix read its last row (its bytes, wherever a
+  // block starts in them), tokens past the tile's end its first token; their sums
+  // are not stored.  A stage is a multiple of four blocks and of four rows a step,
+  // so a thread's blocks all start at the same byte of their first word.
   const int wblk = tid % S::kBlk, wrow = tid / S::kBlk;
   const uint32_t wfirst = wblk < a.nb ? 17u * (uint32_t)wblk : 0u;
-  const int wlike = (wrow & 3) < rows_left ? wrow : wrow & ~3;
-  const uint32_t wphase = (w_odd + (uint32_t)wlike * (uint32_t)a.row_bytes + wfirst) & 3u;
+  const uint32_t wphase = (w_odd + (uint32_t)wrow * (uint32_t)a.row_bytes + wfirst) & 3u;
   uint32_t woff[NW];
 #pragma unroll
-  for (int v = 0; v < NW; ++v) {
-    int row = (wlike + S::kRowStep * v) % TN;
-    if (row >= rows_left) row -= (row - rows_left + 4) & ~3;
-    woff[v] = (w_odd + (uint32_t)row * (uint32_t)a.row_bytes + wfirst) & ~3u;
-  }
+  for (int v = 0; v < NW; ++v)
+    woff[v] = (w_odd + (uint32_t)min((wrow + S::kRowStep * v) % TN, rows_left - 1) * (uint32_t)a.row_bytes + wfirst) & ~3u;
   // A piece of x: a block (MXFP4), or a quarter of one (floats).
   const int xblk = XK == kFp4 ? wblk : (tid >> 2) % S::kBlk;
   const int xtok = XK == kFp4 ? wrow : (tid >> 2) / S::kBlk;
@@ -701,9 +696,9 @@ __global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kern
         // The last two stages in the same code as the others: loads past the
         // row's end read its first blocks, and what they put into LDS is not
         // multiplied.  Code of their own, below, leaves no register free and
-        // spills (4096 x 24576 products of k = 6144: 592 us, 377 so), but
+        // spills (4096 x 24576 products of k = 6144: 598 us, 386 so), but
         // where it fits saves those loads and the checks (4 x 4 fragments of a
-        // wave: 385 us, 405 so).
+        // wave: 463 us, 513 so).
         for (; t < stages; ++t) {
           multiply(t & 1, [&](auto slot) {
             pieces(slot, [&](auto p) {
@@ -803,19 +798,26 @@ __global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kern
   // ordinary numbers pays no more.
   uint32_t odd[FN] = {}, any_odd = 0;
   if constexpr (XK != kFp4) {
-    float all = 0.0f;
+    auto sums = [&](auto ragged) {  // (rows past the matrix hold anything)
+      float all = 0.0f;
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      float some = 0.0f;
+      for (int m = 0; m < FM; ++m) {
+        float some = 0.0f;
 #pragma unroll
-      for (int u = 0; u < S::kMats; ++u)
+        for (int u = 0; u < S::kMats; ++u)
 #pragma unroll
-        for (int n = 0; n < FN; ++n) {
-          const f32x4 v = acc[u][n][m];
-          some = fmaf(v.x, v.y, fmaf(v.z, v.w, some));
-        }
-      if (place(m) < tile.m_end) all += some;
-    }
+          for (int n = 0; n < FN; ++n) {
+            f32x4 v = acc[u][n][m];
+            if constexpr (decltype(ragged)::value)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = 16 * (wn * FN + n) + 4 * g + e < rows_left ? v[e] : 0.0f;
+            some = fmaf(v.x, v.y, fmaf(v.z, v.w, some));
+          }
+        if (place(m) < tile.m_end) all += some;
+      }
+      return all;
+    };
+    const float all = rows_left < TN ? sums(std::true_type()) : sums(std::false_type());
     if (__builtin_expect(__ballot(!__builtin_isfinite(all)) != 0, 0)) {
 #pragma unroll
       for (int n = 0; n < FN; ++n) {
@@ -857,8 +859,8 @@ __global__ void __launch_bounds__(64 * WN * WM * WK, waves(XK, WK)) mx_tile_kern
     // their row is one or NaN: such rows are found among those, and computed
     // again, one output a lane.  (No quantisation of fp32 values writes such
     // scales.  333 bf16 tokens, 11008-row pair of k = 4096: 84 us, as many with a
-    // token of NaN, 133 with all tokens NaN, 370 with one large row; 60 products
-    // of ordinary values take 1.01 times what they do without the check.)
+    // token of NaN, 133 with all tokens NaN, 370 with one large row; 80 products
+    // of ordinary values take 1.005 times what they do without the check.)
     if (__builtin_expect(!any_odd, 1)) return;
     constexpr int kTokens = COLS ? TM : 16 * FM;  // of this wave
     const int p0 = tile.m0 + (COLS ? 0 : 16 * FM * wm), p1 = min(p0 + kTokens, tile.m_end);

@@ -17,8 +17,9 @@ struct Shape {
   using S = MxTile<XK, PAIR, FN, FM, WN, WM, WK, KS, NBUF, COLS>;
 
   // Estimated time; tokens are taken as spread evenly over the experts, each
-  // adding a partial tile of 0.6 (0.5, and unevenness: 4096 tokens x 4 of 128
-  // experts take tiles of 128 tokens with it, 262 us, not of 256, 300).
+  // adding a partial tile of 0.6 (0.5, and unevenness: 4096 MXFP4 tokens x 4 of
+  // 128 experts of 2880 x 2880 take tiles of 128 tokens with it, 277 us, not of
+  // 256, 317).
   static double cost(const MxArgs &a) {
     if (!Grid<S>(a).fits()) return kNever;
     const double active = a.offsets ? (a.n_expert < a.places ? a.n_expert : a.places) : 1;
@@ -42,8 +43,8 @@ struct Shape {
 // shape of its kind for 37 problems each (1 to 4096 tokens, dense, and of 8 to 147
 // experts; k = 64 to 12480), the chosen one took 1.01 times the best (geometric
 // mean; 1.3 to 1.4 in three calls of 9 to 17 us).  No one shape does: bf16 tokens, 5 x
-// 11008 outputs of k = 4096, 11 us in the smallest shape and 54 in the largest;
-// 2048 x 8192, 786 and 133.
+// 11008 outputs of k = 4096, 13 us in the smallest shape and 56 in the largest;
+// 2048 x 8192, 805 and 134.
 template <typename... Of>
 struct Cheapest {
   static constexpr int kShapes = sizeof...(Of);

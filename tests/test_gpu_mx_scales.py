@@ -123,4 +123,5 @@ def test_largest_scales_beside_others(dev, kind, tok):
     # 6 * 2^127 times the sum of 32 of x: only that decides, and token 0's infinity
     s = host(x)[:, 32:64].sum(1)
     sure = (np.abs(s) > 1.0) & (np.arange(tok) != 2)
-    assert sure.sum() >= 1 and np.array_equal(ys[1][sure][:, 3::16], np.repeat(np.sign(s[sure])[:, None] * np.inf, len(range(3, n, 16)), 1))
+    want = np.broadcast_to(np.sign(s[sure])[:, None] * np.inf, (sure.sum(), len(range(3, n, 16))))
+    assert sure.sum() >= 1 and np.array_equal(ys[1][sure][:, 3::16], want)

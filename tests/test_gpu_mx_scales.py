@@ -125,3 +125,29 @@ def test_largest_scales_beside_others(dev, kind, tok):
     sure = (np.abs(s) > 1.0) & (np.arange(tok) != 2)
     want = np.broadcast_to(np.sign(s[sure])[:, None] * np.inf, (sure.sum(), len(range(3, n, 16))))
     assert sure.sum() >= 1 and np.array_equal(ys[1][sure][:, 3::16], want)
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mxfp4"])
+@pytest.mark.parametrize("large_x", [False, True])
+@pytest.mark.parametrize("tok,n,k", [(3, 40, 160), (300, 523, 224)])
+def test_opposite_scales(dev, kind, pair, large_x, tok, n, k):
+    """The scales' ends against each other: weights of scales 0 to 4 (subnormal in fp32 among them) times x about 2^125,
+    and weights of scales 250 to 252 times x about 2^-125; every product is an ordinary number."""
+    rng = np.random.default_rng(tok + large_x)
+    ws = [mxref.random_blocks(rng, n, k, *((0, 5) if large_x else (250, 253))) for _ in range(1 + pair)]
+    if kind == "mxfp4":
+        b = mxref.random_blocks(rng, tok, k, *((249, 253) if large_x else (0, 5)))
+        x, xv = blocks(b, k, dev), mxref.values(b, k)
+    else:
+        x = rng.uniform(0.5, 1.0, (tok, k)) * rng.choice([-1, 1], (tok, k)) * 2.0 ** (125 if large_x else -125)
+        x, xv = as_given(x, kind, dev)
+    y = nan_buffer(tok, n, "f32", dev)
+    (q.qgemv_rows_mx_swiglu if pair else q.qgemv_rows_mx)(*[blocks(w, k, dev) for w in ws], 0, n, x, y)
+    r = [mxref.product(xv, mxref.values(w, k), kind) for w in ws]
+    ref, bound = mxref.swiglu(*r[0], *r[1]) if pair else r[0]
+    if kind == "f32" and not large_x:
+        # x about 2^-125 has bits down to 2^-149; those below 2^-133 are cut off, of each value less than 2^-133
+        cut = [2.0 ** -133 * np.abs(mxref.values(w, k)).sum(1)[None] for w in ws]
+        bound = bound + (1.1 * cut[0] * np.abs(r[1][0]) + np.abs(r[0][0]) * cut[1] + cut[0] * cut[1] if pair else cut[0])
+    near(host(y), ref, bound, "f32")

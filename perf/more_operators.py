@@ -391,7 +391,8 @@ def plain_resize(s, wanted):
     tables.masked_fill_(col >= have[:, None], -1)
     counted(s)
     refs = s["refs"].long()
-    grows = wanted > lens
+    wide = -(-wanted // page) > width
+    grows = (wanted > lens) & ~wide
     last = tables.long().gather(1, (have - 1).clamp(min=0)[:, None])[:, 0]
     partial = grows & (lens % page > 0)
     last = torch.where(partial, last, refs.numel())
@@ -403,7 +404,7 @@ def plain_resize(s, wanted):
     need = torch.where(grows, -(-wanted // page) - have, 0) + copies
     free = (refs == 0).nonzero().flatten()
     before = need.cumsum(0) - need
-    fits = (before + need <= free.numel()) & (-(-wanted // page) <= width)
+    fits = ((before + need <= free.numel()) | (need == 0)) & ~wide
     need = torch.where(fits, need, 0)
     owner = torch.repeat_interleave(seq, need)
     rank = torch.arange(owner.numel(), device=DEV) - (need.cumsum(0) - need)[owner]

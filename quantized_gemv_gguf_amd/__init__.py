@@ -21,6 +21,8 @@ MAX_WINDOWS = 64
 MAX_K = 49152
 CHAIN_MAX_K = 24576
 MAX_EXPERTS = 1024
+MAX_SEQS, MAX_HEADS, MAX_HEAD_DIM, MAX_POOL_PAGES = 4096, 1024, 256, 1 << 22
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 IN_X, IN_RMS, IN_GELU_RMS, IN_SILU_MUL = 0, 1, 2, 3
 OUT_Y, OUT_GELU = 0, 1
 
@@ -33,7 +35,7 @@ STATUS = {
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqgemv.so")
 
-_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_i32, _i64, _f64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p
 
 
 class QgemvError(RuntimeError):
@@ -74,6 +76,31 @@ class qg_chain_step(ctypes.Structure):
 class qg_tensor(ctypes.Structure):
     _fields_ = [("data", _vp), ("type", _i32), ("reserved", _i32), ("n_rows", _i64), ("n_cols", _i64),
                 ("stride", _i64)]
+
+
+class qg_heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("type", _i32), ("reserved", _i32), ("n_tok", _i64), ("n_head", _i32),
+                ("head_dim", _i32), ("tok_stride", _i64), ("head_stride", _i64)]
+
+
+class qg_rope(ctypes.Structure):
+    _fields_ = [("freqs", _vp), ("n_rot", _i32), ("interleaved", _i32), ("mscale", ctypes.c_double)]
+
+
+class qg_kv_cache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("type", _i32), ("page_size", _i32), ("n_layer", _i32), ("n_head", _i32),
+                ("head_dim", _i32), ("reserved", _i32), ("n_pages", _i64), ("layer_stride", _i64),
+                ("page_stride", _i64), ("head_stride", _i64), ("slot_stride", _i64)]
+
+
+class qg_kv_seqs(ctypes.Structure):
+    _fields_ = [("starts", _vp), ("lens", _vp), ("tables", _vp), ("n_seq", _i32), ("reserved", _i32),
+                ("max_pages", _i64)]
+
+
+class qg_kv_pool(ctypes.Structure):
+    _fields_ = [("tables", _vp), ("lens", _vp), ("refs", _vp), ("used", _vp), ("n_seq", _i32), ("page_size", _i32),
+                ("max_pages", _i64), ("n_pages", _i64), ("work", _vp), ("work_bytes", _i64)]
 
 
 _lib = None
@@ -145,6 +172,18 @@ def lib():
         "qgemv_expert_combine": ([P(qg_tensor), _vp, _vp, _i32, P(qg_tensor), _vp], ctypes.c_int),
         "qgemv_expert_combine_grad": ([P(qg_tensor), P(qg_tensor), _vp, _vp, _i32, P(qg_tensor), _vp, _vp],
                                       ctypes.c_int),
+        "qgemv_rope_freqs": ([_i32, _f64, _i32, _f64, _f64, _f64, _f64, P(_f64), P(_f64)], ctypes.c_int),
+        "qgemv_rope": ([P(qg_heads), _vp, P(qg_rope), P(qg_heads), _i32, _vp], ctypes.c_int),
+        "qgemv_kv_append": ([P(qg_heads), P(qg_heads), P(qg_kv_seqs), P(qg_kv_cache), _i32, P(qg_rope), _vp,
+                             P(qg_heads), P(qg_heads), _vp], ctypes.c_int),
+        "qgemv_kv_attend": ([P(qg_heads), P(qg_kv_seqs), P(qg_kv_cache), _i32, P(qg_heads), ctypes.c_float, _i32,
+                             _i32, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+        "qgemv_kv_attend_bytes": ([P(qg_heads), P(qg_kv_seqs), P(qg_kv_cache)], _i64),
+        "qgemv_kv_pool_bytes": ([_i64, _i64, _i64], _i64),
+        "qgemv_kv_resize": ([P(qg_kv_pool), P(qg_kv_cache), _vp, _vp], ctypes.c_int),
+        "qgemv_kv_fork": ([P(qg_kv_pool), _vp, _vp], ctypes.c_int),
+        "qgemv_kv_compact": ([P(qg_kv_pool), P(qg_kv_cache), _vp], ctypes.c_int),
+        "qgemv_kv_copy": ([P(qg_kv_cache), _vp, _vp, _i64, _vp], ctypes.c_int),
         "qgemv_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "qgemv_last_hip_error": ([], ctypes.c_char_p),
         "qgemv_version": ([], ctypes.c_char_p),
@@ -665,13 +704,13 @@ def qgemv_chain_create(fmt: int, steps: Sequence[ChainStep]) -> Chain:
 # A small call's time is the host's: names of torch are looked up once, and a
 # tensor's device is compared with the driver's current one without a
 # torch.cuda call each (a token's sort, gather and weighted sum 18.7 us, not 24.3).
-_kinds = _int32 = _float32 = _device = _raw_stream = None
+_kinds = _int32 = _float32 = _float64 = _device = _raw_stream = None
 
 
 def _torch_names() -> None:
-    global _kinds, _int32, _float32, _device, _raw_stream
+    global _kinds, _int32, _float32, _float64, _device, _raw_stream
     import torch
-    _int32, _float32 = torch.int32, torch.float32
+    _int32, _float32, _float64 = torch.int32, torch.float32, torch.float64
     _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _kinds = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
@@ -856,6 +895,212 @@ def qgemv_expert_combine_grad(dout, y, pos, w, dy, dw, stream=None) -> None:
                                            ctypes.byref(_rows(dy, "dy")), _per_choice(dw, pos, "dw"),
                                            _here_stream(stream)),
            "qgemv_expert_combine_grad")
+
+
+# --- a paged cache of keys and values (include/qgemv_kv.h) ---------------------------
+#
+# Activations are 3-D device tensors (tokens, heads, head_dim) of float32, float16
+# or bfloat16 with unit last stride: slices of a QKV product's rows as they are.
+# Every tensor of a call must lie on the current device.
+
+@dataclass
+class Rope:
+    """Rotary positions: ``freqs`` (device, float64; n_rot / 2 radians a position), pairs (i, i + n_rot / 2) or,
+    ``interleaved``, (2 i, 2 i + 1), turned values times ``mscale``."""
+    freqs: object
+    interleaved: bool = False
+    mscale: float = 1.0
+
+
+@dataclass
+class KvCache:
+    """Keys and values: device tensors (layers, pages, heads, page_size, head_dim), float16 or bfloat16, of the same
+    strides (any order of the axes but the last in memory)."""
+    k: object
+    v: object
+
+
+@dataclass
+class KvSeqs:
+    """Sequences of a call, int32 device tensors: ``starts`` (n_seq + 1) the first rows of their new tokens, ``lens``
+    (n_seq) their positions with the new ones, ``tables`` (n_seq, max_pages) their pages."""
+    starts: object
+    lens: object
+    tables: object
+
+
+@dataclass
+class KvPool:
+    """Who holds which page, int32 device tensors that the calls keep up to date: ``tables`` (n_seq, max_pages; -1
+    behind a sequence's length), ``lens`` (n_seq), ``refs`` (n_pages), ``used`` (a bit a page); ``work`` of
+    qgemv_kv_pool_bytes."""
+    tables: object
+    lens: object
+    refs: object
+    used: object
+    page_size: int
+    work: object
+
+
+def _heads(t, name: str) -> qg_heads:
+    if _kinds is None:
+        _torch_names()
+    kind = _kinds.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (tokens, heads, head_dim)")
+    n, heads, dim = t.shape
+    if not n:  # (no memory behind it)
+        return qg_heads(None, kind, 0, 0, _c32(heads), _c32(dim), 0, dim)
+    tok, head, unit = t.stride()
+    if unit != 1 and dim > 1:
+        raise ValueError(f"the heads of {name} must be contiguous")
+    # (the stride of a single token or head says nothing)
+    head = head if heads > 1 else dim
+    return qg_heads(_here(t, name), kind, 0, n, _c32(heads), _c32(dim), tok if n > 1 else heads * head, head)
+
+
+def _c32(n) -> int:
+    """A size for a C int: past 32 bits, where ctypes would cut it, the largest, which is refused."""
+    return max(min(int(n), 0x7fffffff), -0x80000000)
+
+
+def _rope(r: Rope) -> qg_rope:
+    if _kinds is None:
+        _torch_names()
+    f = r.freqs
+    if f.dtype is not _float64 or f.dim() != 1:
+        raise TypeError("freqs must be a float64 vector")
+    return qg_rope(_array(f, f.numel(), "freqs", _float64, "float64"), _c32(2 * f.numel()), int(bool(r.interleaved)),
+                   float(r.mscale))
+
+
+def _cache(c: KvCache) -> qg_kv_cache:
+    if _kinds is None:
+        _torch_names()
+    k, v = c.k, c.v
+    kind = _kinds.get(k.dtype)
+    if kind is None:
+        raise TypeError(f"the cache must be float16 or bfloat16, not {k.dtype}")
+    if k.dim() != 5:
+        raise ValueError("the cache must be (layers, pages, heads, page_size, head_dim)")
+    strides = k.stride()
+    if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != strides:
+        raise ValueError("k and v of the cache must have the same type, sizes and strides")
+    if strides[4] != 1:
+        raise ValueError("the heads of the cache must be contiguous")
+    layers, pages, heads, size, dim = k.shape
+    return qg_kv_cache(_here(k, "k"), _here(v, "v"), kind, _c32(size), _c32(layers), _c32(heads), _c32(dim), 0, pages,
+                       *strides[:4])
+
+
+def _seqs(s: KvSeqs) -> qg_kv_seqs:
+    n, pages = s.tables.shape
+    return qg_kv_seqs(_i32s(s.starts, n + 1, "starts"), _i32s(s.lens, n, "lens"),
+                      _i32s(s.tables, n * pages, "tables"), _c32(n), 0, pages)
+
+
+def _pool(p: KvPool) -> qg_kv_pool:
+    n, pages = p.tables.shape
+    n_pages = p.refs.numel()
+    return qg_kv_pool(_i32s(p.tables, n * pages, "tables"), _i32s(p.lens, n, "lens"), _i32s(p.refs, n_pages, "refs"),
+                      _i32s(p.used, (n_pages + 31) // 32, "used"), _c32(n), _c32(p.page_size), pages, n_pages,
+                      *_work(p.work))
+
+
+def _work(t):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("work must be contiguous")
+    return (_here(t, "work") if t.numel() else None), t.nbytes
+
+
+def qgemv_rope_freqs(n_rot: int, base: float = 10000.0, scaling: int = ROPE_NONE, factor: float = 1.0,
+                     trained: float = 4096.0, fast: float = 32.0, slow: float = 1.0):
+    """(frequencies as a list of n_rot / 2 floats, mscale) of rotary positions of ``base``, stretched by ``factor``."""
+    out, m = (_f64 * max(int(n_rot) // 2, 1))(), _f64()
+    _check(lib().qgemv_rope_freqs(_c32(n_rot), base, int(scaling), factor, trained, fast, slow, out, ctypes.byref(m)),
+           "qgemv_rope_freqs")
+    return list(out), m.value
+
+
+def qgemv_rope(x, pos, rope: Rope, y, inverse: bool = False, stream=None) -> None:
+    """y[t] = x[t] turned by its position ``pos[t]`` (int32), or ``inverse`` by -pos[t], the turn's gradient; ``y``
+    may be ``x``."""
+    _check(lib().qgemv_rope(ctypes.byref(_heads(x, "x")), _i32s(pos, x.shape[0], "pos"), ctypes.byref(_rope(rope)),
+                            ctypes.byref(_heads(y, "y")), int(bool(inverse)), _here_stream(stream)), "qgemv_rope")
+
+
+def qgemv_kv_append(k, v, seqs: KvSeqs, cache: KvCache, layer: int, rope: Rope = None, pos=None, q=None, q_out=None,
+                    stream=None) -> None:
+    """The new tokens' keys, turned by ``rope``, and values into ``layer`` of the cache, and ``q`` turned into
+    ``q_out``; by their positions in the sequence, or by ``pos`` (int32, one a row)."""
+    _check(lib().qgemv_kv_append(ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(v, "v")), ctypes.byref(_seqs(seqs)),
+                                 ctypes.byref(_cache(cache)), _c32(layer),
+                                 ctypes.byref(_rope(rope)) if rope is not None else None,
+                                 _i32s(pos, k.shape[0], "pos") if pos is not None else None,
+                                 ctypes.byref(_heads(q, "q")) if q is not None else None,
+                                 ctypes.byref(_heads(q_out, "q_out")) if q_out is not None else None,
+                                 _here_stream(stream)), "qgemv_kv_append")
+
+
+def qgemv_kv_attend_bytes(q, seqs: KvSeqs, cache: KvCache) -> int:
+    """Bytes of ``work`` for a qgemv_kv_attend of these sizes."""
+    n = lib().qgemv_kv_attend_bytes(ctypes.byref(_heads(q, "q")), ctypes.byref(_seqs(seqs)),
+                                    ctypes.byref(_cache(cache)))
+    if n < 0:
+        _check(n, "qgemv_kv_attend_bytes")
+    return n
+
+
+def qgemv_kv_attend(q, seqs: KvSeqs, cache: KvCache, layer: int, out, scale: float, causal: bool = True,
+                    window: int = 0, sinks=None, lse=None, work=None, stream=None) -> None:
+    """out = softmax(scale q k^T) v of the new tokens over their sequences' positions in ``layer``; ``sinks`` (float32,
+    one a q head), ``lse`` (float32, tokens x q heads) and ``work`` (qgemv_kv_attend_bytes) as the header has them."""
+    n, heads = q.shape[:2]
+    _check(lib().qgemv_kv_attend(ctypes.byref(_heads(q, "q")), ctypes.byref(_seqs(seqs)), ctypes.byref(_cache(cache)),
+                                 _c32(layer), ctypes.byref(_heads(out, "out")), scale, int(bool(causal)), _c32(window),
+                                 _weights(sinks, heads, "sinks") if sinks is not None else None,
+                                 _weights(lse, n * heads, "lse") if lse is not None else None, *_work(work),
+                                 _here_stream(stream)), "qgemv_kv_attend")
+
+
+def qgemv_kv_pool_bytes(n_seq: int, max_pages: int, n_pages: int) -> int:
+    """Bytes of a pool's ``work``."""
+    n = lib().qgemv_kv_pool_bytes(n_seq, max_pages, n_pages)
+    if n < 0:
+        _check(n, "qgemv_kv_pool_bytes")
+    return n
+
+
+def qgemv_kv_resize(pool: KvPool, cache: KvCache, lens, stream=None) -> None:
+    """Cuts and grows the sequences to ``lens`` (int32; negative: as it is), copying shared pages they grow into;
+    ``pool.lens`` tells which found room."""
+    _check(lib().qgemv_kv_resize(ctypes.byref(_pool(pool)), ctypes.byref(_cache(cache)),
+                                 _i32s(lens, pool.tables.shape[0], "lens"), _here_stream(stream)), "qgemv_kv_resize")
+
+
+def qgemv_kv_fork(pool: KvPool, parents, stream=None) -> None:
+    """All at once every sequence s becomes what ``parents[s]`` (int32) was, sharing its pages; -1 lets s go."""
+    _check(lib().qgemv_kv_fork(ctypes.byref(_pool(pool)), _i32s(parents, pool.tables.shape[0], "parents"),
+                               _here_stream(stream)), "qgemv_kv_fork")
+
+
+def qgemv_kv_compact(pool: KvPool, cache: KvCache, stream=None) -> None:
+    """Moves the pages in use to the lowest numbers."""
+    _check(lib().qgemv_kv_compact(ctypes.byref(_pool(pool)), ctypes.byref(_cache(cache)), _here_stream(stream)),
+           "qgemv_kv_compact")
+
+
+def qgemv_kv_copy(cache: KvCache, src, dst, stream=None) -> None:
+    """Page src[i] to page dst[i] (int32) in every layer."""
+    n = src.numel()
+    if dst.numel() != n:
+        raise ValueError("src and dst must be of the same length")
+    _check(lib().qgemv_kv_copy(ctypes.byref(_cache(cache)), _i32s(src, n, "src"), _i32s(dst, n, "dst"), n,
+                               _here_stream(stream)), "qgemv_kv_copy")
 
 
 def qgemv_version() -> str:

@@ -22,6 +22,10 @@ HEADERS = ["qgemv_impl.h"]
 # activation type each.
 MX_SOURCES = ["mx.hip", "mx_f32.hip", "mx_f16.hip", "mx_bf16.hip", "mx_fp4.hip"]
 MX_HEADERS = ["mx_gemm.h", "mx_launch.h"]
+# kv.hip, kv_pool.hip, kv_attend.hip: the C ABI of qgemv_kv.h (positions and writes
+# into the cache, its pages, attention); the attention kernels of one cache type each.
+KV_SOURCES = ["kv.hip", "kv_pool.hip", "kv_attend.hip", "kv_attend_f16.hip", "kv_attend_bf16.hip"]
+KV_HEADERS = ["kv_common.h", "kv_attend.h", "kv_attend_launch.h"]
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqgemv.so")
 ARCH = "gfx950"
@@ -57,12 +61,17 @@ def mx_source_paths():
     return [os.path.join(CSRC, f) for f in MX_SOURCES + MX_HEADERS]
 
 
+def kv_source_paths():
+    """Every file the paged cache's operators are built from (their profile names its hash)."""
+    return [os.path.join(CSRC, f) for f in KV_SOURCES + KV_HEADERS]
+
+
 def build(verbose: bool = False) -> str:
     """Compile csrc/*.hip (in parallel) and link libqgemv.so (always recompiles)."""
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     procs = []
-    for s in SOURCES + MX_SOURCES:
+    for s in SOURCES + MX_SOURCES + KV_SOURCES:
         obj = os.path.join(objdir, s.replace(".hip", ".o"))
         log = obj + ".log"
         cmd = [hipcc(), *HIPCC_FLAGS, f"-I{INC}", "-c", os.path.join(CSRC, s), "-o", obj]

@@ -1,0 +1,562 @@
+// kv_attend.h -- attention of new tokens over a paged cache.
+//
+// A row (t, h) of q with the keys it sees, m = max_j s_j, gives
+//     o = sum_j e^(s_j - m) v_j / l,   l = sum_j e^(s_j - m) + e^(sink - m).
+// Keys are walked once, in pieces: of a piece's maximum m', sum l' and products
+// o' (all fp32) the running ones become m'' = max(m, m'), l'' = l e^(m - m'') +
+// l' e^(m' - m''), and o'' likewise; so do those of parts of the keys that
+// different workgroups have walked.
+//
+// Matrix instructions take S^T = K Q^T with the keys as rows and the q rows as
+// columns.  A lane then holds several keys' scores of one q row, which is the
+// layout that O^T = V^T P^T takes P^T in: weights go from scores to products
+// within a lane's registers, a row's maximum and factor are one value a lane.
+// (The keys of a product may come in any order, if v's do too.)
+//
+// The q heads that share a head of the cache are rows of one tile: of sequence
+// s, row r is token r / group, head r % group.
+#pragma once
+
+#include "kv_common.h"
+
+namespace qgemv_kv {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct AttendArgs {
+  Heads q, out;
+  const uint16_t *k, *v;  // the layer's
+  int64_t page_stride, head_stride, slot_stride;
+  Seqs seqs;
+  const float *sinks;
+  float *lse;
+  float *part;  // of parts: rows of dim sums, then rows of (m, l)
+  int64_t part_rows;
+  int n_tok, group, kv_heads, n_pages;
+  float scale;  // log2(e) times the caller's
+  int causal, window;
+  int target;  // parts to cut the keys into, at most, beyond one a tile; 0: no cuts
+};
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_huge_valf();
+
+// ---------------------------------------------------------------------------
+// Which workgroup takes what.  Lengths are on the device, so each finds its
+// tile of rows and part of the keys itself: pieces of kPiece keys are counted
+// over all tiles, and a sequence's tiles are cut into parts of so many pieces
+// that about `target` parts come out in all.  A wave does this for itself, its
+// lanes over the sequences: no barrier (64 sequences: 0.6 us).
+// ---------------------------------------------------------------------------
+
+struct Item {
+  int s, tile, part, parts;  // parts: of this tile; 0: nothing to do
+  int first;                 // the tile's first part among all parts
+  int start, n, len;         // the sequence's rows and length
+};
+
+template <int ROWS, int PIECE> struct Plan {
+  const AttendArgs &a;
+  __device__ Plan(const AttendArgs &args) : a(args) {}
+
+  // Tiles of a sequence and the pieces of keys that its rows see.
+  __device__ void size_of(int s, int &tiles, int &pieces) const {
+    int start, n, len;
+    seq_rows(a.seqs, s, a.n_tok, start, n, len);
+    tiles = (int)(((int64_t)n * a.group + ROWS - 1) / ROWS);
+    const int lo = a.window ? max(len - n - a.window + 1, 0) : 0;
+    pieces = max(1, (len - min(lo, len) + PIECE - 1) / PIECE);
+  }
+  // The item of this number among parts (BY_TILE: among tiles).
+  template <bool BY_TILE> __device__ Item find(int number) const {
+    const int lane = threadIdx.x & 63, n_seq = a.seqs.n_seq;
+    int each = 0x7fffffff;  // pieces of a part
+    if (a.target > 0) {
+      int64_t all = 0;
+      for (int s0 = 0; s0 < n_seq; s0 += 64) {
+        int tiles = 0, pieces = 0;
+        if (s0 + lane < n_seq) size_of(s0 + lane, tiles, pieces);
+        all += (int64_t)tiles * pieces;
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d /= 2) all += __shfl_xor(all, d);
+      each = (int)((all + a.target - 1) / a.target);
+      each = max(each, 1);
+    }
+    Item it = {};
+    int items = 0, parts_before = 0;  // of the sequences before s0
+    for (int s0 = 0; s0 < n_seq; s0 += 64) {
+      int tiles = 0, pieces = 1;
+      if (s0 + lane < n_seq) size_of(s0 + lane, tiles, pieces);
+      const int parts = a.target > 0 ? (pieces - 1) / each + 1 : 1;
+      int sum = BY_TILE ? tiles : tiles * parts, sum_parts = tiles * parts;
+      const int mine = sum, mine_parts = sum_parts;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(sum, d), p = __shfl_up(sum_parts, d);
+        if (lane >= d) {
+          sum += o;
+          sum_parts += p;
+        }
+      }
+      const uint64_t here = __ballot(items + sum > number);
+      if (here) {
+        const int l = __builtin_ctzll(here);
+        const int in = number - items - __builtin_amdgcn_readlane(sum - mine, l);
+        const int p = __builtin_amdgcn_readlane(parts, l);
+        it.s = s0 + l;
+        it.parts = p;
+        it.tile = BY_TILE ? in : in / p;
+        it.part = BY_TILE ? 0 : in - it.tile * p;
+        it.first = parts_before + __builtin_amdgcn_readlane(sum_parts - mine_parts, l) + it.tile * p;
+        seq_rows(a.seqs, it.s, a.n_tok, it.start, it.n, it.len);
+        return it;
+      }
+      items += __builtin_amdgcn_readlane(sum, 63);
+      parts_before += __builtin_amdgcn_readlane(sum_parts, 63);
+    }
+    return it;
+  }
+};
+
+// The keys that a tile's rows see: from the first row's first to the last row's
+// last; and those that all of them see.
+struct Range {
+  int lo, hi, all_lo, all_hi;
+};
+template <int ROWS> __device__ __forceinline__ Range range_of(const AttendArgs &a, const Item &it) {
+  const int first = it.tile * ROWS / a.group;
+  const int last = (min(it.n * a.group, (it.tile + 1) * ROWS) - 1) / a.group;
+  const int old = it.len - it.n;  // (may be below 0: then the first rows see nothing)
+  Range r;
+  r.lo = a.window ? max(old + first - a.window + 1, 0) : 0;
+  r.hi = a.causal ? max(old + last + 1, 0) : it.len;
+  r.all_lo = a.window ? max(old + last - a.window + 1, 0) : 0;
+  r.all_hi = a.causal ? old + first + 1 : it.len;
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Element types of the cache, and the terms of an fp32 value in them.
+// ---------------------------------------------------------------------------
+
+template <int T> struct Kind;
+template <> struct Kind<QG_F16> {
+  typedef _Float16 H;
+  typedef _Float16 V8 __attribute__((ext_vector_type(8)));
+  static constexpr int kWide = 2;            // terms that hold an fp32 (22 bits and the sign of the second)
+  static constexpr uint32_t kExp = 0x7c00u;  // the exponent of infinities and NaN
+  static constexpr uint32_t kOne = 0x3c00u;
+  static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Kind<QG_BF16> {
+  typedef __bf16 H;
+  typedef __bf16 V8 __attribute__((ext_vector_type(8)));
+  static constexpr int kWide = 3;
+  static constexpr uint32_t kExp = 0x7f80u;
+  static constexpr uint32_t kOne = 0x3f80u;
+  static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+
+// x as a sum of NT values of the type: each the nearest to what the ones before leave.
+template <int T, int NT> __device__ __forceinline__ void terms_of(const float (&x)[8], typename Kind<T>::V8 (&t)[NT]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float left = x[i];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      t[k][i] = (typename Kind<T>::H)left;
+      if (k + 1 < NT) left -= (float)t[k][i];
+    }
+  }
+}
+
+// 2^e with the exponent of the largest of a row's values (0 for a row of zeros,
+// infinities and NaN): an fp32 row divided by it has terms in fp16.
+__device__ __forceinline__ int row_exponent(float most) {
+  const int e = (int)((__float_as_uint(most) >> 23) & 255);
+  return e == 0 || e == 255 ? 0 : e - 127;
+}
+
+// Lanes that are 16 and 32 apart hold the same q row: the largest, the sum.
+__device__ __forceinline__ float max_of_row16(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float sum_of_row16(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// The words of 8 values of the type: all of them finite?
+template <int T> __device__ __forceinline__ bool finite8(const u32x4 &w) {
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ok = ok && (w[i] & Kind<T>::kExp) != Kind<T>::kExp && (w[i] >> 16 & Kind<T>::kExp) != Kind<T>::kExp;
+  return ok;
+}
+// Finite values kept (WHAT 0), or ones where the value is NaN (1), +inf (2), -inf (3), else zeros.
+template <int T, int WHAT> __device__ __forceinline__ uint32_t sift16(uint32_t x) {
+  const uint32_t e = Kind<T>::kExp;
+  if (WHAT == 0) return (x & e) == e ? 0 : x;
+  if (WHAT == 1) return (x & 0x7fff) > e ? Kind<T>::kOne : 0;
+  return x == (WHAT == 2 ? e : e | 0x8000u) ? Kind<T>::kOne : 0;
+}
+template <int T, int WHAT> __device__ __forceinline__ u32x4 sift8(const u32x4 &w) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = sift16<T, WHAT>(w[i] & 0xffff) | sift16<T, WHAT>(w[i] >> 16) << 16;
+  return r;
+}
+// What visible values of no finite size add to a sum: how many NaN, +inf and -inf a row sees.
+__device__ __forceinline__ float without_size(float nan, float up, float down) {
+  const float x = up > 0.0f ? kInf : 0.0f;
+  return nan > 0.0f || (up > 0.0f && down > 0.0f) ? __builtin_nanf("") : down > 0.0f ? -kInf : x;
+}
+
+// A finished row's factor, and the logarithm of its denominator (base e).
+__device__ __forceinline__ void finish_row(const AttendArgs &a, int head, float m, float l, float &f, float &lse) {
+  if (a.sinks) {
+    const float z = a.sinks[head] * kLog2e, top = fmaxf(m, z);
+    const float w = top == -kInf ? 0.0f : exp2_of(z - top);
+    const float keep = m == -kInf ? 0.0f : exp2_of(m - top);
+    l = l * keep + w;
+    f = l == 0.0f ? 0.0f : keep / l;
+    m = top;
+  } else {
+    f = l == 0.0f ? 0.0f : 1.0f / l;
+  }
+  lse = l == 0.0f ? -kInf : (m + log2_of(l)) * kLn2;
+}
+
+template <int N> __device__ __forceinline__ void store_row(const Heads &h, int64_t t, int head, int at,
+                                                           const float (&v)[N]) {
+  store_as(h.type, h.p, t * h.tok_stride + head * h.head_stride + at, v);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: tiles of 16.  Bound by memory, so nothing is staged: each of four
+// waves takes every fourth 32 keys straight from the pages into the layout of
+// the matrix instructions (16 x 16 x 32), the next ones under way while it
+// computes.  A lane's 8 keys of v are rows of dim / 16 values; of value e of
+// each, the lane's column c makes column (c, e) of v, so the transposition that
+// V^T needs is 8 permutations of words a lane, and the order of v's columns
+// comes back when the sums are stored.
+// ---------------------------------------------------------------------------
+
+constexpr int kFewRows = 16, kFewPiece = 128, kFewWaves = 4;
+
+template <int T, int D, int NT> struct Few {
+  using K = Kind<T>;
+  using V8 = typename K::V8;
+  static constexpr int E = D / 16;  // values of a lane's part of a row of v
+  static constexpr int ST = D / 32; // steps of a product over a row of k
+  static constexpr int kAlign = E % 8 == 0 ? 16 : E % 4 == 0 ? 8 : 4;  // of that part
+  struct Keys {
+    u32x4 k[2][ST];     // keys base + 16 u + c, values 32 t + 8 g + ..
+    uint32_t v[8][E / 2];  // keys base + 16 (j / 4) + 4 g + j % 4, values E c + ..
+    uint32_t there;        // bit j: v's key j is
+  };
+};
+
+// Byte offset of a key's row in the cache's head, and whether its page is there.
+struct KeyAt {
+  int64_t at;
+  bool there;
+};
+__device__ __forceinline__ KeyAt key_at(const AttendArgs &a, int key, int page) {
+  const bool there = (unsigned)page < (unsigned)a.n_pages;
+  return {((there ? page : 0) * a.page_stride + (key & ((1 << a.seqs.page_shift) - 1)) * a.slot_stride) * 2, there};
+}
+
+template <int T, int D, int NT>
+__global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t group0) {
+  using F = Few<T, D, NT>;
+  using K = typename F::K;
+  using V8 = typename F::V8;
+  constexpr int E = F::E, ST = F::ST;
+  constexpr int kStride = D + 4;  // of a row's sums in LDS: rows in other banks
+  __shared__ float sums[kFewWaves][kFewRows][kStride];
+  __shared__ float2 stats[kFewWaves][kFewRows];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  const int number = (int)((group0 + blockIdx.x) / a.kv_heads), head = (int)(group0 + blockIdx.x - (int64_t)number * a.kv_heads);
+  const Item it = Plan<kFewRows, kFewPiece>(a).template find<false>(number);
+  if (it.parts == 0) return;
+  const Range range = range_of<kFewRows>(a, it);
+  // this part's keys: whole pieces from a multiple of 32 on
+  const int lo = range.lo & ~31, pieces = max(0, (range.hi - lo + kFewPiece - 1) / kFewPiece);
+  const int share = (pieces + it.parts - 1) / it.parts;
+  const int begin = lo + min(pieces, it.part * share) * kFewPiece;
+  const int end = min(range.hi, lo + min(pieces, (it.part + 1) * share) * kFewPiece);
+
+  // the lane's q row
+  const int row = it.tile * kFewRows + c, tok = row / a.group, q_head = head * a.group + row % a.group;
+  const bool real = row < it.n * a.group;
+  const int pos = it.len - it.n + tok;
+  const int see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  const int see_hi = real ? (a.causal ? pos + 1 : it.len) : 0;
+  V8 q[ST][NT];
+  float scale = a.scale;
+  {
+    float x[ST][8];
+    float most = 0.0f;
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[t][i] = 0.0f;
+      if (real)
+        load_as(a.q.type, a.q.p, (it.start + tok) * a.q.tok_stride + q_head * a.q.head_stride + 32 * t + 8 * g, x[t]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[t][i]));
+    }
+    if (T == QG_F16 && NT > 1) {
+      const int e = row_exponent(max_of_row16(most));
+      scale = ldexpf(scale, e);
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[t][i] = ldexpf(x[t][i], -e);
+    }
+#pragma unroll
+    for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
+  }
+
+  const uint8_t *ck = (const uint8_t *)(a.k + head * a.head_stride), *cv = (const uint8_t *)(a.v + head * a.head_stride);
+  const int32_t *table = a.seqs.tables + it.s * a.seqs.max_pages;
+  // Pages of a round's keys: two of k's and, where pages hold fours of keys, two of v's.
+  const bool fours = a.seqs.page_shift >= 2;
+  const int last_key = max(end - 1, 0);
+  struct Pages {
+    int k[2], v[8];
+  };
+  const auto page_of = [&](int key) { return table[min(key, last_key) >> a.seqs.page_shift]; };
+  const auto load_pages = [&](int base, Pages &p) {
+    if (base >= end) return;
+    p.k[0] = page_of(base + c);
+    p.k[1] = page_of(base + 16 + c);
+    p.v[0] = page_of(base + 4 * g);
+    p.v[4] = page_of(base + 16 + 4 * g);
+    if (!fours) {
+#pragma unroll
+      for (int j = 1; j < 4; ++j) {
+        p.v[j] = page_of(base + 4 * g + j);
+        p.v[4 + j] = page_of(base + 16 + 4 * g + j);
+      }
+    }
+  };
+  const auto load_keys = [&](int base, const Pages &p, typename F::Keys &x) {
+    if (base >= end) return;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const KeyAt at = key_at(a, min(base + 16 * u + c, last_key), p.k[u]);
+#pragma unroll
+      for (int t = 0; t < ST; ++t) x.k[u][t] = *(const u32x4 *)(ck + at.at + 64 * t + 16 * g);
+    }
+    x.there = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int key = base + 16 * (j / 4) + 4 * g + (j & 3);
+      const KeyAt at = key_at(a, min(key, last_key), fours ? p.v[j & 4] : p.v[j]);
+      __builtin_memcpy(x.v[j], __builtin_assume_aligned(cv + at.at + 2 * E * c, F::kAlign), 2 * E);
+      x.there |= (uint32_t)(at.there && key < end) << j;
+    }
+  };
+
+  f32x4 o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
+  float m = -kInf, l = 0.0f;
+
+  const auto compute = [&](int base, typename F::Keys &x) {
+    f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int k = 0; k < NT; ++k) s[u] = K::mfma16(__builtin_bit_cast(V8, x.k[u][t]), q[t][k], s[u]);
+    float p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = s[j / 4][j & 3];
+    const bool whole = base >= range.all_lo && base + 32 <= min(range.all_hi, end) && __all(x.there == 0xff);
+    uint32_t seen = 0xff;
+    bool odd = false;  // values of v without a size where some rows may not see them
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = base + 16 * (j / 4) + 4 * g + (j & 3);
+        const bool there = x.there >> j & 1;
+        if (!(there && key >= see_lo && key < see_hi)) {
+          p[j] = -kInf;
+          seen &= ~(1u << j);
+        }
+        bool fine = true;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          if (!there) x.v[j][i] = 0;
+          const uint32_t w = x.v[j][i];
+          fine = fine && (w & K::kExp) != K::kExp && (w >> 16 & K::kExp) != K::kExp;
+        }
+        odd = odd || !fine;
+      }
+      odd = __any(odd);
+    }
+    float top = p[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) top = fmaxf(top, p[j]);
+    top = fmaxf(m, max_of_row16(top) * scale);
+    if (__any(top > m)) {
+      const float f = top > m ? exp2_of(m - top) : 1.0f;  // (of m = -inf, 0)
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      m = top;
+    }
+    const float off = m == -kInf ? 0.0f : m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = exp2_of(fmaf(p[j], scale, -off));
+      l += p[j];
+    }
+    V8 w[NT];
+    terms_of<T, NT>(p, w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      u32x4 col;  // value e of the lane's 8 rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        col[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][e / 2], x.v[2 * i][e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+      if (!odd) {
+#pragma unroll
+        for (int k = 0; k < NT; ++k) o[e] = K::mfma16(__builtin_bit_cast(V8, col), w[k], o[e]);
+      } else {
+        const u32x4 finite = sift8<T, 0>(col);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) o[e] = K::mfma16(__builtin_bit_cast(V8, finite), w[k], o[e]);
+        V8 sees;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sees[j] = (typename K::H)(seen >> j & 1 ? 1.0f : 0.0f);
+        const f32x4 zero = {0, 0, 0, 0};
+        const f32x4 nan = K::mfma16(__builtin_bit_cast(V8, (sift8<T, 1>(col))), sees, zero);
+        const f32x4 up = K::mfma16(__builtin_bit_cast(V8, (sift8<T, 2>(col))), sees, zero);
+        const f32x4 down = K::mfma16(__builtin_bit_cast(V8, (sift8<T, 3>(col))), sees, zero);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[e][i] += without_size(nan[i], up[i], down[i]);
+      }
+    }
+  };
+
+  {
+    constexpr int kStep = 32 * kFewWaves;
+    int base = begin + 32 * wave;
+    Pages pages = {};
+    typename F::Keys now = {}, next = {};
+    load_pages(base, pages);
+    load_keys(base, pages, now);
+    load_pages(base + kStep, pages);
+    for (; base < end; base += kStep) {
+      load_keys(base + kStep, pages, next);
+      load_pages(base + 2 * kStep, pages);
+      compute(base, now);
+      now = next;
+    }
+  }
+
+  // the four waves' sums joined; lane (row, part of the values) of 256
+  l = sum_of_row16(l);
+  if (g == 0) stats[wave][c] = make_float2(m, l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[wave][c][(4 * g + i) * E + e] = o[e][i];
+  __syncthreads();
+  const int r = threadIdx.x >> 4, at = (threadIdx.x & 15) * E;
+  float top = -kInf;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) top = fmaxf(top, stats[w][r].x);
+  float total = 0.0f, v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) {
+    const float f = stats[w][r].x == -kInf ? 0.0f : exp2_of(stats[w][r].x - top);
+    total += stats[w][r].y * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += sums[w][r][at + e] * f;
+  }
+  const int out_row = it.tile * kFewRows + r;
+  if (out_row >= it.n * a.group) return;
+  if (it.parts == 1) {
+    const int64_t t = it.start + out_row / a.group;
+    const int h = head * a.group + out_row % a.group;
+    float f, lse;
+    finish_row(a, h, top, total, f, lse);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= f;
+    store_row(a.out, t, h, at, v);
+    if (a.lse && (threadIdx.x & 15) == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
+  } else {
+    const int64_t pr = ((int64_t)(it.first + it.part) * a.kv_heads + head) * kFewRows + r;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.part[pr * D + at + e] = v[e];
+    if ((threadIdx.x & 15) == 0) ((float2 *)(a.part + a.part_rows * D))[pr] = make_float2(top, total);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The parts of a tile joined, where there are several: 16 lanes a row.
+// ---------------------------------------------------------------------------
+
+template <int D, int ROWS, int PIECE> __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int64_t group0) {
+  constexpr int E = D / 16, kGroups = ROWS / 16;  // workgroups of a tile
+  const int64_t group = group0 + blockIdx.x;
+  const int sub = (int)(group / a.kv_heads), head = (int)(group - (int64_t)sub * a.kv_heads);
+  const Item it = Plan<ROWS, PIECE>(a).template find<true>(sub / kGroups);
+  if (it.parts < 2) return;
+  const int r = (sub % kGroups) * 16 + (threadIdx.x >> 4), at = (threadIdx.x & 15) * E;
+  const int row = it.tile * ROWS + r;
+  if (row >= it.n * a.group) return;
+  const float2 *stats = (const float2 *)(a.part + a.part_rows * D);
+  const int64_t first = ((int64_t)it.first * a.kv_heads + head) * ROWS + r, step = (int64_t)a.kv_heads * ROWS;
+  float m = -kInf;
+  for (int p = 0; p < it.parts; ++p) m = fmaxf(m, stats[first + p * step].x);
+  float l = 0.0f, v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < it.parts; ++p) {
+    const float2 s = stats[first + p * step];
+    const float f = s.x == -kInf ? 0.0f : exp2_of(s.x - m);
+    l += s.y * f;
+    const float *x = a.part + (first + p * step) * D + at;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += x[e] * f;
+  }
+  const int64_t t = it.start + row / a.group;
+  const int h = head * a.group + row % a.group;
+  float f, lse;
+  finish_row(a, h, m, l, f, lse);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] *= f;
+  store_row(a.out, t, h, at, v);
+  if (a.lse && (threadIdx.x & 15) == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
+}
+
+// A call's shape: the rows of a tile, the most tiles and parts its sequences can have.
+struct AttendShape {
+  int64_t tiles, parts, rows;
+  int target;
+};
+
+template <int T> hipError_t launch_attend(const AttendArgs &a, const AttendShape &s, int dim, bool wide,
+                                          hipStream_t stream);
+
+}  // namespace qgemv_kv

@@ -1,0 +1,100 @@
+// kv_attend.hip -- the C ABI of qgemv_kv_attend: checks, the workspace, the shape of a call.
+#include "kv_attend.h"
+
+#include <algorithm>
+#include <cmath>
+
+using namespace qgemv_kv;
+
+namespace {
+
+// Parts of keys in flight: four workgroups a compute unit.
+constexpr int64_t kParts = 1024;
+
+AttendShape shape_of(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache) {
+  AttendShape s = {};
+  const int64_t group = q->n_head / cache->n_head, n_seq = seqs->n_seq;
+  s.rows = kFewRows;
+  // every sequence may end in a partial tile, of one row at least
+  s.tiles = std::min(q->n_tok * group, q->n_tok * group / s.rows + n_seq);
+  // enough tiles, or keys for one piece: nothing is cut
+  const int64_t least = (q->n_tok * group + s.rows - 1) / s.rows * cache->n_head;
+  const int64_t most_keys = seqs->max_pages * cache->page_size;
+  s.target = least >= kParts || most_keys <= kFewPiece ? 0 : (int)((kParts + cache->n_head - 1) / cache->n_head);
+  s.parts = s.tiles + s.target;
+  return s;
+}
+
+int64_t part_rows_of(const AttendShape &s, const qg_kv_cache *cache) {
+  return s.target > 0 ? s.parts * cache->n_head * s.rows : 0;
+}
+
+int check_attend(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache, bool sizes_only) {
+  if (!q || !seqs || !cache) return QG_E_NULL;
+  qg_heads h = *q;
+  qg_kv_seqs s = *seqs;
+  qg_kv_cache c = *cache;
+  if (sizes_only) {  // any addresses
+    static char some[16] __attribute__((aligned(16)));
+    h.data = c.k = c.v = some;
+    s.starts = s.lens = s.tables = (const int32_t *)some;
+  }
+  int rc;
+  if ((rc = check_cache(&c)) || (rc = check_seqs(&s, &c)) || (rc = check_heads(&h, false, QG_MAX_HEAD_DIM))) return rc;
+  if (h.head_dim != c.head_dim || h.n_head % c.n_head != 0 || h.n_tok * h.n_head > kMaxCount) return QG_E_SHAPE;
+  return QG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t qgemv_kv_attend_bytes(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache) {
+  const int rc = check_attend(q, seqs, cache, true);
+  if (rc) return rc;
+  const AttendShape s = shape_of(q, seqs, cache);
+  return part_rows_of(s, cache) * (cache->head_dim + 2) * 4;
+}
+
+int qgemv_kv_attend(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache, int32_t layer,
+                    const qg_heads *out, float scale, int32_t causal, int32_t window, const float *sinks, float *lse,
+                    void *work, int64_t work_bytes, qg_stream_t stream) {
+  int rc;
+  if ((rc = check_attend(q, seqs, cache, false)) || (rc = check_heads(out, true, QG_MAX_HEAD_DIM))) return rc;
+  if (out->n_tok != q->n_tok || out->n_head != q->n_head || out->head_dim != q->head_dim) return QG_E_SHAPE;
+  if (layer < 0 || layer >= cache->n_layer) return QG_E_RANGE;
+  if (!std::isfinite(scale) || scale <= 0.0f || window < 0) return QG_E_ARG;
+  const AttendShape s = shape_of(q, seqs, cache);
+  const int64_t part_rows = part_rows_of(s, cache), bytes = part_rows * (cache->head_dim + 2) * 4;
+  if (work_bytes < bytes) return QG_E_SIZE;
+  if (q->n_tok == 0 || seqs->n_seq == 0) return QG_OK;
+  if (bytes > 0 && !work) return QG_E_NULL;
+  if ((uintptr_t)work & 15) return QG_E_ARG;
+  AttendArgs a = {};
+  a.q = heads_of(q);
+  a.out = heads_of(out);
+  a.k = (const uint16_t *)cache->k + layer * cache->layer_stride;
+  a.v = (const uint16_t *)cache->v + layer * cache->layer_stride;
+  a.page_stride = cache->page_stride;
+  a.head_stride = cache->head_stride;
+  a.slot_stride = cache->slot_stride;
+  a.seqs = seqs_of(seqs, cache);
+  a.sinks = sinks;
+  a.lse = lse;
+  a.part = (float *)work;
+  a.part_rows = part_rows;
+  a.n_tok = (int)q->n_tok;
+  a.group = q->n_head / cache->n_head;
+  a.kv_heads = cache->n_head;
+  a.n_pages = (int)cache->n_pages;
+  a.scale = scale * kLog2e;
+  a.causal = causal != 0;
+  a.window = window;
+  a.target = s.target;
+  const bool wide = q->type != cache->type || out->type != cache->type;
+  const auto run = cache->type == QG_F16 ? launch_attend<QG_F16> : launch_attend<QG_BF16>;
+  KV_HIP(run(a, s, cache->head_dim, wide, stream));
+  return QG_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,311 @@
+"""include/qgemv_kv.h on the host (no GPU): every entry point is exported, bad arguments are refused with the documented
+status before any HIP call, frequencies are the formulas', and the tests' plain forms hold."""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import re
+import subprocess
+
+import pytest
+
+import quantized_gemv_gguf_amd as q
+from quantized_gemv_gguf_amd import qg_heads, qg_kv_cache, qg_kv_pool, qg_kv_seqs, qg_rope
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "qgemv_kv.h")
+E_NULL, E_FMT, E_SHAPE, E_RANGE, E_SIZE, E_ARG = -1, -2, -3, -4, -5, -6
+FAKE = 0x1000  # a non-NULL address; never dereferenced by a call that is refused
+INF, NAN = math.inf, math.nan
+
+
+def test_every_declared_symbol_is_exported():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(qgemv_\w+)\s*\(", text)))
+    assert len(names) == 10, names
+    out = subprocess.run(["nm", "-D", "--defined-only", q.LIB_PATH], capture_output=True, text=True).stdout
+    exported = set(re.findall(r"\sT\s(\w+)$", out, flags=re.M))
+    assert not [n for n in names if n not in exported]
+    for n in names:
+        assert hasattr(q.lib(), n) and hasattr(q, n)
+
+
+def test_header_compiles_as_c_and_matches_the_binding():
+    sizes = " && ".join("sizeof(%s) == %d" % (c.__name__, ctypes.sizeof(c))
+                        for c in (qg_heads, qg_rope, qg_kv_cache, qg_kv_seqs, qg_kv_pool))
+    src = ('#include "qgemv_kv.h"\nint main(void){return %s && QG_MAX_SEQS == %d && QG_MAX_HEADS == %d &&'
+           ' QG_MAX_HEAD_DIM == %d && QG_MAX_POOL_PAGES == %d && QG_ROPE_YARN == %d ? 0 : 1;}\n'
+           % (sizes, q.MAX_SEQS, q.MAX_HEADS, q.MAX_HEAD_DIM, q.MAX_POOL_PAGES, q.ROPE_YARN))
+    exe = "/tmp/qgemv_kv_header_%d" % os.getpid()
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", f"-I{os.path.dirname(HEADER)}", "-x", "c", "-",
+                        "-o", exe], input=src, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    try:
+        assert subprocess.run([exe]).returncode == 0
+    finally:
+        os.remove(exe)
+
+
+def heads(n=4, h=2, d=64, kind=q.F32, tok=None, head=None, data=FAKE, reserved=0):
+    head = d if head is None else head
+    return ctypes.byref(qg_heads(data, kind, reserved, n, h, d, h * head if tok is None else tok, head))
+
+
+def rope(rot=64, inter=0, m=1.0, freqs=FAKE):
+    return ctypes.byref(qg_rope(freqs, rot, inter, m))
+
+
+def cache(kind=q.F16, size=16, layers=2, h=2, d=64, pages=8, k=FAKE, v=FAKE, reserved=0, strides=None):
+    page = h * size * d
+    return ctypes.byref(qg_kv_cache(k, v, kind, size, layers, h, d, reserved, pages,
+                                    *(strides or (pages * page, page, size * d, d))))
+
+
+def seqs(n=3, pages=4, starts=FAKE, lens=FAKE, tables=FAKE, reserved=0):
+    return ctypes.byref(qg_kv_seqs(starts, lens, tables, n, reserved, pages))
+
+
+def pool(n=3, size=16, max_pages=4, pages=8, work=FAKE, work_bytes=1 << 20, **p):
+    p = {**dict(tables=FAKE, lens=FAKE, refs=FAKE, used=FAKE), **p}
+    return ctypes.byref(qg_kv_pool(p["tables"], p["lens"], p["refs"], p["used"], n, size, max_pages, pages, work,
+                                   work_bytes))
+
+
+BAD_HEADS = [(None, E_NULL), (heads(kind=0), E_FMT), (heads(kind=q.MXFP4), E_FMT), (heads(n=-1), E_SHAPE),
+             (heads(n=1 << 31), E_SHAPE), (heads(h=0), E_SHAPE), (heads(h=1025), E_SHAPE), (heads(d=0), E_SHAPE),
+             (heads(reserved=1), E_ARG), (heads(tok=-1), E_ARG), (heads(head=-64), E_ARG),
+             (heads(tok=1 << 50), E_ARG), (heads(n=1 << 20, tok=1 << 40), E_ARG), (heads(data=None), E_NULL),
+             (heads(data=FAKE + 2), E_ARG)]
+OVERLAPPING = [heads(tok=64), heads(head=32), heads(tok=0), heads(head=0, tok=64)]
+
+
+@pytest.mark.parametrize("i", range(len(BAD_HEADS)))
+def test_heads_are_refused(i):
+    h, rc = BAD_HEADS[i]
+    L = q.lib()
+    assert L.qgemv_rope(h, FAKE, rope(), heads(), 0, None) == rc
+    assert L.qgemv_rope(heads(), FAKE, rope(), h, 0, None) == rc
+    assert L.qgemv_kv_append(h, heads(), seqs(), cache(), 0, None, None, None, None, None) == rc
+    assert L.qgemv_kv_append(heads(), h, seqs(), cache(), 0, None, None, None, None, None) == rc
+    assert L.qgemv_kv_attend(h, seqs(), cache(), 0, heads(), 1.0, 1, 0, None, None, FAKE, 1 << 30, None) == rc
+    assert L.qgemv_kv_attend(heads(), seqs(), cache(), 0, h, 1.0, 1, 0, None, None, FAKE, 1 << 30, None) == rc
+    if h is not None:
+        assert L.qgemv_kv_append(heads(), heads(), seqs(), cache(), 0, rope(), None, h, heads(), None) == rc
+        assert L.qgemv_kv_append(heads(), heads(), seqs(), cache(), 0, rope(), None, heads(), h, None) == rc
+
+
+@pytest.mark.parametrize("i", range(len(OVERLAPPING)))
+def test_outputs_whose_heads_meet_are_refused(i):
+    L, h = q.lib(), OVERLAPPING[i]
+    assert L.qgemv_rope(heads(), FAKE, rope(), h, 0, None) == E_ARG
+    assert L.qgemv_kv_append(heads(), heads(), seqs(), cache(), 0, rope(), None, heads(), h, None) == E_ARG
+    assert L.qgemv_kv_attend(heads(), seqs(), cache(), 0, h, 1.0, 1, 0, None, None, FAKE, 1 << 30, None) == E_ARG
+
+
+@pytest.mark.parametrize("r,rc", [(None, E_NULL), (rope(rot=0), E_SHAPE), (rope(rot=3), E_SHAPE), (rope(rot=66), E_SHAPE),
+                                  (rope(inter=2), E_ARG), (rope(m=INF), E_ARG), (rope(m=NAN), E_ARG),
+                                  (rope(freqs=None), E_NULL), (rope(freqs=FAKE + 4), E_ARG)])
+def test_rope_refusals(r, rc):
+    L = q.lib()
+    assert L.qgemv_rope(heads(), FAKE, r, heads(), 0, None) == rc
+    if r is not None:
+        assert L.qgemv_kv_append(heads(), heads(), seqs(), cache(), 0, r, None, None, None, None) == rc
+
+
+def test_rope_sizes():
+    L = q.lib()
+    assert L.qgemv_rope(heads(), None, rope(), heads(), 0, None) == E_NULL
+    for bad in (heads(n=5), heads(h=3), heads(d=96)):
+        assert L.qgemv_rope(heads(), FAKE, rope(), bad, 0, None) == E_SHAPE
+    # in place only as it is
+    assert L.qgemv_rope(heads(), FAKE, rope(), heads(kind=q.F16), 0, None) == E_ARG
+    assert L.qgemv_rope(heads(), FAKE, rope(), heads(tok=192), 0, None) == E_ARG
+    assert L.qgemv_rope(heads(d=65537), FAKE, rope(), heads(d=65537), 0, None) == E_SHAPE
+    assert L.qgemv_rope(heads(n=0), FAKE, rope(), heads(n=0), 0, None) == 0
+
+
+BAD_CACHES = [(None, E_NULL), (cache(kind=q.F32), E_FMT), (cache(kind=q.Q8_0), E_FMT), (cache(size=0), E_SHAPE),
+              (cache(size=24), E_SHAPE), (cache(size=1 << 17), E_SHAPE), (cache(layers=0), E_SHAPE),
+              (cache(h=0), E_SHAPE), (cache(h=1025), E_SHAPE), (cache(d=48), E_SHAPE), (cache(d=0), E_SHAPE),
+              (cache(d=288), E_SHAPE), (cache(pages=0), E_SHAPE), (cache(pages=1 << 31), E_SHAPE),
+              (cache(reserved=1), E_ARG), (cache(k=None), E_NULL), (cache(v=None), E_NULL), (cache(k=FAKE + 8), E_ARG),
+              (cache(strides=(16384, 2048, 1024, 0)), E_ARG), (cache(strides=(16384, 2048, 1024, -64)), E_ARG),
+              (cache(strides=(16384, 2048, 1024, 68)), E_ARG), (cache(strides=(16384, 2048, 1016, 64)), E_ARG),
+              (cache(strides=(16384, 2040, 1024, 64)), E_ARG), (cache(strides=(16376, 2048, 1024, 64)), E_ARG),
+              (cache(strides=(16384, 2048, 64, 64)), E_ARG), (cache(strides=(1 << 49, 2048, 1024, 64)), E_ARG)]
+
+
+@pytest.mark.parametrize("i", range(len(BAD_CACHES)))
+def test_caches_are_refused(i):
+    c, rc = BAD_CACHES[i]
+    L = q.lib()
+    assert L.qgemv_kv_append(heads(), heads(), seqs(), c, 0, None, None, None, None, None) == rc
+    assert L.qgemv_kv_attend(heads(), seqs(), c, 0, heads(), 1.0, 1, 0, None, None, FAKE, 1 << 30, None) == rc
+    assert L.qgemv_kv_copy(c, FAKE, FAKE, 1, None) == rc
+    assert L.qgemv_kv_resize(pool(), c, FAKE, None) == rc
+    assert L.qgemv_kv_compact(pool(), c, None) == rc
+
+
+def test_any_order_of_the_axes():
+    L = q.lib()
+    for strides in [(16384, 2048, 1024, 64), (16384, 2048, 64, 128), (2048, 4096, 1024, 64), (64, 4096, 2048, 128),
+                    (1 << 20, 1 << 16, 2048, 128)]:
+        assert L.qgemv_kv_copy(cache(strides=strides), FAKE, FAKE, 0, None) == 0
+    # one page, one layer: their strides only have to be whole
+    assert L.qgemv_kv_copy(cache(pages=1, layers=1, strides=(8, 8, 1024, 64)), FAKE, FAKE, 0, None) == 0
+
+
+@pytest.mark.parametrize("s,rc", [(None, E_NULL), (seqs(n=-1), E_SHAPE), (seqs(n=4097), E_SHAPE),
+                                  (seqs(pages=-1), E_SHAPE), (seqs(pages=1 << 27), E_SHAPE), (seqs(reserved=1), E_ARG),
+                                  (seqs(starts=None), E_NULL), (seqs(lens=None), E_NULL), (seqs(tables=None), E_NULL)])
+def test_sequences_are_refused(s, rc):
+    L = q.lib()
+    assert L.qgemv_kv_append(heads(), heads(), s, cache(), 0, None, None, None, None, None) == rc
+    assert L.qgemv_kv_attend(heads(), s, cache(), 0, heads(), 1.0, 1, 0, None, None, FAKE, 1 << 30, None) == rc
+
+
+def test_append_refusals():
+    L = q.lib()
+
+    def call(k=heads(), v=heads(), c=cache(), layer=0, r=rope(), x=None, y=None):
+        return L.qgemv_kv_append(k, v, seqs(), c, layer, r, None, x, y, None)
+
+    assert call(layer=-1) == E_RANGE and call(layer=2) == E_RANGE
+    assert call(k=heads(kind=q.F16)) == E_FMT and call(x=heads(kind=q.F16), y=heads()) == E_FMT
+    assert call(k=heads(h=3)) == E_SHAPE and call(v=heads(h=1)) == E_SHAPE and call(v=heads(d=96)) == E_SHAPE
+    assert call(v=heads(n=5)) == E_SHAPE
+    assert call(x=heads(n=5), y=heads(n=5)) == E_SHAPE and call(x=heads(), y=heads(h=3)) == E_SHAPE
+    assert call(x=heads(d=96), y=heads(d=96)) == E_SHAPE
+    assert call(x=heads()) == E_NULL and call(y=heads()) == E_ARG
+    assert call(r=None, x=heads(), y=heads()) == E_ARG
+    assert call(x=heads(), y=heads(kind=q.F16)) == E_ARG  # in place, another type
+    assert call(k=heads(n=0), v=heads(n=0)) == 0
+    assert L.qgemv_kv_append(heads(), heads(), seqs(n=0), cache(), 0, None, None, None, None, None) == 0
+
+
+def test_attend_refusals():
+    L = q.lib()
+
+    def call(x=heads(), s=seqs(), c=cache(), layer=0, y=heads(), scale=1.0, window=0, work=FAKE, n=1 << 30):
+        return L.qgemv_kv_attend(x, s, c, layer, y, scale, 1, window, None, None, work, n, None)
+
+    assert call(layer=-1) == E_RANGE and call(layer=2) == E_RANGE
+    assert call(x=heads(h=3), y=heads(h=3)) == E_SHAPE and call(x=heads(d=96), y=heads(d=96)) == E_SHAPE
+    assert call(y=heads(n=5)) == E_SHAPE and call(y=heads(h=4)) == E_SHAPE and call(y=heads(d=32)) == E_SHAPE
+    for scale in (0.0, -1.0, INF, NAN):
+        assert call(scale=scale) == E_ARG
+    assert call(window=-1) == E_ARG
+    need = L.qgemv_kv_attend_bytes(heads(), seqs(pages=64), cache())
+    assert need > 0 and need % 4 == 0
+    assert call(s=seqs(pages=64), n=need - 1) == E_SIZE
+    assert call(s=seqs(pages=64), work=None) == E_NULL and call(s=seqs(pages=64), work=FAKE + 8) == E_ARG
+    many = heads(n=(1 << 31) - (1 << 16), h=2, tok=128)
+    assert call(x=many, y=many) == E_SHAPE
+    assert call(x=heads(n=0), y=heads(n=0)) == 0 and call(s=seqs(n=0)) == 0
+    assert L.qgemv_kv_attend_bytes(heads(h=3), seqs(), cache()) == E_SHAPE
+    assert L.qgemv_kv_attend_bytes(None, seqs(), cache()) == E_NULL
+    assert L.qgemv_kv_attend_bytes(heads(data=None), seqs(tables=None), cache(k=None)) >= 0
+
+
+def test_pool_refusals():
+    L = q.lib()
+    need = L.qgemv_kv_pool_bytes(3, 4, 8)
+    assert need > 0 and need % 16 == 0
+    bad = [(None, E_NULL), (pool(n=0), E_SHAPE), (pool(n=4097), E_SHAPE), (pool(size=0), E_SHAPE), (pool(size=12), E_SHAPE),
+           (pool(max_pages=0), E_SHAPE), (pool(max_pages=1 << 27), E_SHAPE), (pool(pages=0), E_SHAPE),
+           (pool(pages=q.MAX_POOL_PAGES + 1), E_SHAPE), (pool(n=4096, size=1, max_pages=1 << 20), E_SHAPE),
+           (pool(work=None), E_NULL), (pool(work=FAKE + 8), E_ARG), (pool(work_bytes=need - 1), E_SIZE)]
+    bad += [(pool(**{name: None}), E_NULL) for name in ("tables", "lens", "refs", "used")]
+    for p, rc in bad:
+        assert L.qgemv_kv_fork(p, FAKE, None) == rc
+        assert L.qgemv_kv_resize(p, cache(), FAKE, None) == rc
+        assert L.qgemv_kv_compact(p, cache(), None) == rc
+    assert L.qgemv_kv_fork(pool(), None, None) == E_NULL and L.qgemv_kv_resize(pool(), cache(), None, None) == E_NULL
+    for c in (cache(size=32), cache(pages=9)):
+        assert L.qgemv_kv_resize(pool(), c, FAKE, None) == E_SHAPE and L.qgemv_kv_compact(pool(), c, None) == E_SHAPE
+    for args in ((0, 4, 8), (3, 0, 8), (3, 4, 0), (4097, 4, 8), (3, 1 << 31, 8), (3, 4, q.MAX_POOL_PAGES + 1)):
+        assert L.qgemv_kv_pool_bytes(*args) == E_SHAPE
+    assert L.qgemv_kv_copy(cache(), FAKE, FAKE, -1, None) == E_ARG
+    assert L.qgemv_kv_copy(cache(), None, FAKE, 1, None) == E_NULL and L.qgemv_kv_copy(cache(), FAKE, None, 1, None) == E_NULL
+
+
+# --- frequencies ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("rot", [2, 24, 64, 128, 1024])
+def test_frequencies(rot):
+    half = rot // 2
+    plain = [10000.0 ** (-2 * i / rot) for i in range(half)]
+    close = lambda a, b: a == pytest.approx(b, rel=1e-13)  # noqa: E731
+    f, m = q.qgemv_rope_freqs(rot)
+    assert close(f, plain) and m == 1.0
+    f, m = q.qgemv_rope_freqs(rot, 10000.0, q.ROPE_LINEAR, 4.0)
+    assert close(f, [x / 4 for x in plain]) and m == 1.0
+    f, m = q.qgemv_rope_freqs(rot, 10000.0, q.ROPE_NTK, 4.0)
+    assert f[0] == 1.0 and m == 1.0
+    if half > 1:
+        assert close(f[-1], plain[-1] / 4)
+    f, m = q.qgemv_rope_freqs(rot, 10000.0, q.ROPE_YARN, 8.0, 4096.0)
+    assert m == pytest.approx(0.1 * math.log(8.0) + 1.0, rel=1e-15)
+    for x, y in zip(f, plain):
+        turns = 4096.0 * y / (2 * math.pi)
+        assert y / 8 * (1 - 1e-12) <= x <= y * (1 + 1e-12)
+        # well inside either end (the border indices are rounded outwards by less than one)
+        if turns > 32 * 10000.0 ** (2 / rot):
+            assert close(x, y)
+        if turns < 10000.0 ** (-2 / rot):
+            assert close(x, y / 8)
+
+
+def test_frequencies_refused():
+    out = (ctypes.c_double * 64)()
+
+    def call(rot=64, base=10000.0, kind=0, factor=2.0, trained=4096.0, fast=32.0, slow=1.0, to=out):
+        return q.lib().qgemv_rope_freqs(rot, base, kind, factor, trained, fast, slow, to, None)
+
+    assert call() == 0 and call(factor=0.0) == 0
+    for rot in (0, -2, 3, 1026):
+        assert call(rot=rot) == E_SHAPE
+    assert call(kind=-1) == E_FMT and call(kind=4) == E_FMT and call(to=None) == E_NULL
+    for base in (1.0, 0.0, -5.0, INF, NAN):
+        assert call(base=base) == E_ARG
+    for kind in (1, 2, 3):
+        for factor in (0.5, INF, NAN):
+            assert call(kind=kind, factor=factor) == E_ARG
+    assert call(kind=3, trained=0.0) == E_ARG and call(kind=3, slow=0.0) == E_ARG and call(kind=3, fast=0.5) == E_ARG
+    assert call(kind=3, fast=NAN) == E_ARG
+
+
+# --- the plain forms --------------------------------------------------------------------
+
+def test_plain_attention_is_the_softmax():
+    torch = pytest.importorskip("torch")
+    import kvref
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(1, 3, 1, 4, 8, generator=g).half() for _ in range(2))
+    x = torch.randn(3, 2, 8, generator=g)
+    tables = torch.tensor([[2, 0, 1]])
+    r = kvref.attended(x, [0, 3], [7], tables, k, v, 0, 0.5)
+    at = torch.cat([k[0, 2, 0], k[0, 0, 0]])[:7].double(), torch.cat([v[0, 2, 0], v[0, 0, 0]])[:7].double()
+    for i in range(3):
+        for h in range(2):
+            a = at[0][:5 + i] @ x[i, h].double() * 0.5
+            assert torch.allclose(r["out"][i, h], torch.softmax(a, 0) @ at[1][:5 + i])
+            assert torch.allclose(r["lse"][i, h], torch.logsumexp(a, 0))
+
+
+def test_plain_pool_shares_and_copies():
+    import kvref
+    p = kvref.Pool(4, 8, 16, 4)
+    p.resize([6, 0, 0, 0])
+    assert p.pages[0] == [0, 1]
+    p.fork([0, 0, 0, -1])
+    assert p.refs()[:2] == [3, 3]
+    p.resize([7, 7, -1, -1])  # two of three grow: both copy
+    assert p.pages[:3] == [[0, 2], [0, 3], [0, 1]] and p.data[2] == p.data[3] == 1
+    p.fork([2, 2, 2, 1])
+    p.resize([9, 9, 9, -1])  # all three grow: the first keeps page 1
+    assert p.pages == [[0, 1, 2], [0, 4, 5], [0, 6, 7], [0, 3]]
+    p.resize([0, -1, -1, 0])
+    p.compact()
+    assert p.pages == [[], [0, 4, 1], [0, 2, 3], []]

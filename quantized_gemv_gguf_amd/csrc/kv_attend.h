@@ -22,6 +22,8 @@
 namespace qgemv_kv {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 struct AttendArgs {
   Heads q, out;
@@ -152,6 +154,9 @@ template <> struct Kind<QG_F16> {
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
+  static __device__ __forceinline__ f32x16 mfma32(V8 a, V8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
 };
 template <> struct Kind<QG_BF16> {
   typedef __bf16 H;
@@ -161,6 +166,9 @@ template <> struct Kind<QG_BF16> {
   static constexpr uint32_t kOne = 0x3f80u;
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(V8 a, V8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
 };
 
@@ -194,31 +202,33 @@ __device__ __forceinline__ float sum_of_row16(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// The words of 8 values of the type: all of them finite?
-template <int T> __device__ __forceinline__ bool finite8(const u32x4 &w) {
-  bool ok = true;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    ok = ok && (w[i] & Kind<T>::kExp) != Kind<T>::kExp && (w[i] >> 16 & Kind<T>::kExp) != Kind<T>::kExp;
-  return ok;
+// Two values of the type in a word: are both finite?  Those that are, zeros for the others.
+template <int T> __device__ __forceinline__ bool finite2(uint32_t w) {
+  constexpr uint32_t e = Kind<T>::kExp;
+  return (w & e) != e && (w >> 16 & e) != e;
 }
-// Finite values kept (WHAT 0), or ones where the value is NaN (1), +inf (2), -inf (3), else zeros.
-template <int T, int WHAT> __device__ __forceinline__ uint32_t sift16(uint32_t x) {
-  const uint32_t e = Kind<T>::kExp;
-  if (WHAT == 0) return (x & e) == e ? 0 : x;
-  if (WHAT == 1) return (x & 0x7fff) > e ? Kind<T>::kOne : 0;
-  return x == (WHAT == 2 ? e : e | 0x8000u) ? Kind<T>::kOne : 0;
+template <int T> __device__ __forceinline__ uint32_t only_finite2(uint32_t w) {
+  constexpr uint32_t e = Kind<T>::kExp;
+  return ((w & e) == e ? 0 : w & 0xffff) | ((w >> 16 & e) == e ? 0 : w & 0xffff0000u);
 }
-template <int T, int WHAT> __device__ __forceinline__ u32x4 sift8(const u32x4 &w) {
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = sift16<T, WHAT>(w[i] & 0xffff) | sift16<T, WHAT>(w[i] >> 16) << 16;
-  return r;
+
+// The bits from number n on, of 32.
+__device__ __forceinline__ uint32_t bits_from(int n) { return n >= 32 ? 0u : ~0u << max(n, 0); }
+
+// Values of v without a size (infinities, NaN) must not reach the rows that may
+// not see them: a product with a weight of 0 would be NaN.  Where a tile's rows
+// differ in what they see, such values are taken out of the products, and after
+// all keys they are counted, kind by kind, with ones in place of the weights of
+// the keys a row sees; a count adds the kind itself, which no factor changes.
+// (The values are read again from the cache.)
+enum Kinds { kNan = 0, kUp = 1, kDown = 2 };
+template <int T> __device__ __forceinline__ uint32_t is_kind(uint32_t x, int kind) {
+  constexpr uint32_t e = Kind<T>::kExp;
+  const bool yes = kind == kNan ? (x & 0x7fff) > e : x == (kind == kUp ? e : e | 0x8000u);
+  return yes ? Kind<T>::kOne : 0;
 }
-// What visible values of no finite size add to a sum: how many NaN, +inf and -inf a row sees.
-__device__ __forceinline__ float without_size(float nan, float up, float down) {
-  const float x = up > 0.0f ? kInf : 0.0f;
-  return nan > 0.0f || (up > 0.0f && down > 0.0f) ? __builtin_nanf("") : down > 0.0f ? -kInf : x;
+__device__ __forceinline__ float of_kind(float count, int kind) {
+  return count > 0.0f ? kind == kNan ? __builtin_nanf("") : kind == kUp ? kInf : -kInf : 0.0f;
 }
 
 // A finished row's factor, and the logarithm of its denominator (base e).
@@ -276,8 +286,10 @@ __device__ __forceinline__ KeyAt key_at(const AttendArgs &a, int key, int page) 
   return {((there ? page : 0) * a.page_stride + (key & ((1 << a.seqs.page_shift) - 1)) * a.slot_stride) * 2, there};
 }
 
+constexpr int few_waves(int dim, int terms) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
+
 template <int T, int D, int NT>
-__global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t group0) {
+__global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(AttendArgs a, int64_t group0) {
   using F = Few<T, D, NT>;
   using K = typename F::K;
   using V8 = typename F::V8;
@@ -375,6 +387,16 @@ __global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t g
   for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
   float m = -kInf, l = 0.0f;
 
+  const auto key_of = [&](int j) { return 16 * (j / 4) + 4 * g + (j & 3); };
+  // bit j: the lane's row sees its key j of those from base on
+  const auto seen_of = [&](int base, uint32_t there) {
+    const uint32_t in = (bits_from(see_lo - base) & ~bits_from(see_hi - base)) >> (4 * g);
+    return there & ((in & 15) | (in >> 12 & 0xf0));
+  };
+  const auto all_see = [&](int base, uint32_t there) {
+    return base >= range.all_lo && base + 32 <= range.all_hi && __all(there == 0xff);
+  };
+  bool odd_values = false;
   const auto compute = [&](int base, typename F::Keys &x) {
     f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
@@ -386,28 +408,29 @@ __global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t g
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = s[j / 4][j & 3];
-    const bool whole = base >= range.all_lo && base + 32 <= min(range.all_hi, end) && __all(x.there == 0xff);
-    uint32_t seen = 0xff;
-    bool odd = false;  // values of v without a size where some rows may not see them
+    const bool whole = all_see(base, x.there);
     if (!whole) {
+      bool odd = false;
+      const uint32_t seen = seen_of(base, x.there);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int key = base + 16 * (j / 4) + 4 * g + (j & 3);
         const bool there = x.there >> j & 1;
-        if (!(there && key >= see_lo && key < see_hi)) {
-          p[j] = -kInf;
-          seen &= ~(1u << j);
-        }
-        bool fine = true;
+        const float score = p[j];
+        p[j] = seen >> j & 1 ? score : -kInf;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
           if (!there) x.v[j][i] = 0;
-          const uint32_t w = x.v[j][i];
-          fine = fine && (w & K::kExp) != K::kExp && (w >> 16 & K::kExp) != K::kExp;
+          odd = odd || !finite2<T>(x.v[j][i]);
         }
-        odd = odd || !fine;
       }
       odd = __any(odd);
+      if (odd) {
+        odd_values = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) x.v[j][i] = only_finite2<T>(x.v[j][i]);
+      }
     }
     float top = p[0];
 #pragma unroll
@@ -434,23 +457,8 @@ __global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t g
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         col[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][e / 2], x.v[2 * i][e / 2], e & 1 ? 0x07060302u : 0x05040100u);
-      if (!odd) {
 #pragma unroll
-        for (int k = 0; k < NT; ++k) o[e] = K::mfma16(__builtin_bit_cast(V8, col), w[k], o[e]);
-      } else {
-        const u32x4 finite = sift8<T, 0>(col);
-#pragma unroll
-        for (int k = 0; k < NT; ++k) o[e] = K::mfma16(__builtin_bit_cast(V8, finite), w[k], o[e]);
-        V8 sees;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sees[j] = (typename K::H)(seen >> j & 1 ? 1.0f : 0.0f);
-        const f32x4 zero = {0, 0, 0, 0};
-        const f32x4 nan = K::mfma16(__builtin_bit_cast(V8, (sift8<T, 1>(col))), sees, zero);
-        const f32x4 up = K::mfma16(__builtin_bit_cast(V8, (sift8<T, 2>(col))), sees, zero);
-        const f32x4 down = K::mfma16(__builtin_bit_cast(V8, (sift8<T, 3>(col))), sees, zero);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[e][i] += without_size(nan[i], up[i], down[i]);
-      }
+      for (int k = 0; k < NT; ++k) o[e] = K::mfma16(__builtin_bit_cast(V8, col), w[k], o[e]);
     }
   };
 
@@ -467,6 +475,36 @@ __global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t g
       load_pages(base + 2 * kStep, pages);
       compute(base, now);
       now = next;
+    }
+  }
+  if (odd_values) {
+    for (int base = begin + 32 * wave; base < end; base += 32 * kFewWaves) {
+      int64_t at[8];
+      uint32_t there = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = min(base + key_of(j), last_key);
+        const KeyAt k = key_at(a, key, page_of(key));
+        at[j] = k.at;
+        there |= (uint32_t)(k.there && base + key_of(j) < end) << j;
+      }
+      if (all_see(base, there)) continue;
+      const uint32_t seen = seen_of(base, there);
+      u32x4 ones = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ones[j / 2] |= (seen >> j & 1 ? K::kOne : 0) << (16 * (j & 1));
+      for (int kind = kNan; kind <= kDown; ++kind) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          u32x4 is = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            is[j / 2] |= is_kind<T>(*(const uint16_t *)(cv + at[j] + 2 * (E * c + e)), kind) << (16 * (j & 1));
+          const f32x4 n = K::mfma16(__builtin_bit_cast(V8, is), __builtin_bit_cast(V8, ones), f32x4{0, 0, 0, 0});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[e][i] += of_kind(n[i], kind);
+        }
+      }
     }
   }
 
@@ -512,6 +550,322 @@ __global__ void __launch_bounds__(256) attend_few_kernel(AttendArgs a, int64_t g
 }
 
 // ---------------------------------------------------------------------------
+// Many rows: tiles of 128, 32 to a wave.  Bound by the matrix cores and by the
+// softmax beside them.  Keys and values come in tiles of KT through LDS, the
+// next tile's copies (HBM or L2 -> LDS, asynchronous, 16 bytes a lane) under way
+// while one is computed.  32 x 32 x 16 instructions: a wave's q rows are their 32
+// columns; K^T comes by 16-byte reads, V^T by the transposing 8-byte ones, whose
+// four keys a lane are those of the scores' layout.
+// A row of 2 D bytes begins at the same bank as another one, so its 16-byte
+// pieces lie at places exchanged by the key's low bits, differently for K and V:
+// as the reads that go together fall on different banks.
+// The running maximum follows only when a row's grows by more than 8 (in powers
+// of 2): until then weights up to 256 are as exact, and the sums need no factor.
+// ---------------------------------------------------------------------------
+
+constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves, kManyPiece = 64;
+constexpr float kSlack = 8.0f;
+
+template <int D> struct ManyTile {
+  static constexpr int KT = D <= 128 ? 64 : 32;  // keys
+  static constexpr int CH = D / 8;               // pieces of a row
+  static constexpr int kBytes = KT * D * 2;
+  static constexpr int kBanks = D / 2 % 64;      // where the next row begins
+  static __host__ __device__ constexpr int k_turn(int key) {
+    return kBanks == 0 ? key & 7 : kBanks == 32 ? (key >> 1) & 3 : (key >> 2) & 3;
+  }
+  static __host__ __device__ constexpr int v_turn(int key) {
+    return kBanks == 0 ? (key & 3) << 2 : kBanks == 32 ? ((key >> 1) & 1) << 2 : 0;
+  }
+};
+
+// One asynchronous copy of 16 bytes a lane to LDS at lds + 16 lane.  The
+// compiler's own waits would drain it before any read of LDS; here the kernel
+// waits, a tile later.
+__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// The largest, the sum of a value and the one 32 lanes away.
+__device__ __forceinline__ float max_of_row32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_of_row32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Waves a SIMD: as many as their sums and rows leave registers for.
+constexpr int many_waves(int dim, int terms) { return dim <= 64 && terms == 1 ? 3 : dim * (1 + terms) <= 256 ? 2 : 1; }
+
+template <int T, int D, int NT>
+__global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_many_kernel(AttendArgs a, int64_t group0) {
+  using K = Kind<T>;
+  using V8 = typename K::V8;
+  using M = ManyTile<D>;
+  constexpr int KT = M::KT, CH = M::CH, U = KT / 32, ST = D / 16, DT = D / 32;
+  constexpr int kCopies = (KT * CH + 255) / 256;  // of a wave, for K, for V
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][M::kBytes];  // of a tile: K, V
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, h = lane >> 5;
+  const int number = (int)((group0 + blockIdx.x) / a.kv_heads);
+  const int head = (int)(group0 + blockIdx.x - (int64_t)number * a.kv_heads);
+  const Item it = Plan<kManyRows, kManyPiece>(a).template find<false>(number);
+  if (it.parts == 0) return;
+  const Range range = range_of<kManyRows>(a, it);
+  const int lo = range.lo & ~31, pieces = max(0, (range.hi - lo + kManyPiece - 1) / kManyPiece);
+  const int share = (pieces + it.parts - 1) / it.parts;
+  const int begin = lo + min(pieces, it.part * share) * kManyPiece;
+  const int end = min(range.hi, lo + min(pieces, (it.part + 1) * share) * kManyPiece);
+
+  // the lane's q row, and what the wave's rows see
+  const int row0 = it.tile * kManyRows + 32 * wave, rows = it.n * a.group;
+  const int row = row0 + c, tok = row / a.group, q_head = head * a.group + row % a.group;
+  const bool real = row < rows;
+  const int old = it.len - it.n, pos = old + tok;
+  const int see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  const int see_hi = real ? (a.causal ? pos + 1 : it.len) : 0;
+  const int first_tok = row0 / a.group, last_tok = (min(row0 + 32, rows) - 1) / a.group;
+  const int wave_lo = a.window ? max(old + first_tok - a.window + 1, 0) : 0;
+  const int wave_hi = row0 < rows ? (a.causal ? old + last_tok + 1 : it.len) : 0;
+  const int whole_lo = a.window ? max(old + last_tok - a.window + 1, 0) : 0;
+  const int whole_hi = a.causal ? old + first_tok + 1 : it.len;
+  V8 q[ST][NT];
+  float scale = a.scale;
+  {
+    float x[ST][8];
+    float most = 0.0f;
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[t][i] = 0.0f;
+      if (real)
+        load_as(a.q.type, a.q.p, (it.start + tok) * a.q.tok_stride + q_head * a.q.head_stride + 16 * t + 8 * h, x[t]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[t][i]));
+    }
+    if (T == QG_F16 && NT > 1) {
+      const int e = row_exponent(max_of_row32(most));
+      scale = ldexpf(scale, e);
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[t][i] = ldexpf(x[t][i], -e);
+    }
+#pragma unroll
+    for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
+  }
+
+  const uint8_t *ck = (const uint8_t *)(a.k + head * a.head_stride), *cv = (const uint8_t *)(a.v + head * a.head_stride);
+  const int32_t *table = a.seqs.tables + it.s * a.seqs.max_pages;
+  const int last_key = max(end - 1, 0);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0][0][0];
+
+  // Lane i holds the page of a tile's key i.
+  const auto page_of = [&](int base) {
+    return base < end ? table[min(base + (lane & (KT - 1)), last_key) >> a.seqs.page_shift] : -1;
+  };
+  // Keys of the tile that are there, a bit each.
+  const auto there_of = [&](int base, int page) {
+    return __ballot((unsigned)page < (unsigned)a.n_pages && base + (lane & (KT - 1)) < end);
+  };
+  const auto copy_tile = [&](int base, int page, int buf) {
+    if (base >= end) return;
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) {
+      const int first = (j * kManyWaves + wave) * 64;
+      if (kCopies * 256 != KT * CH && first >= KT * CH) break;
+      const int p = first + lane, key = p / CH, piece = p - key * CH;
+      const int64_t at = key_at(a, min(base + key, last_key), __shfl(page, key)).at;
+      const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + buf * 2 * M::kBytes + first * 16);
+      copy_to_lds(ck + at + 16 * (piece ^ M::k_turn(key)), to);
+      copy_to_lds(cv + at + 16 * (piece ^ M::v_turn(key)), to + M::kBytes);
+    }
+  };
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  float m = -kInf, l = 0.0f;
+
+  constexpr uint64_t kAll = KT == 64 ? ~0ull : (1ull << KT) - 1;
+  const auto all_see = [&](int base, uint64_t now) {
+    return base >= range.all_lo && base + KT <= range.all_hi && (now & kAll) == kAll;
+  };
+  // Bit 8 (i / 4) + i % 4: the lane's row sees key i of its own of the 32 from base + 32 u on.
+  const auto seen = [&](int base, uint64_t now, int u) {
+    return ((uint32_t)(now >> (32 * u)) & bits_from(see_lo - base - 32 * u) & ~bits_from(see_hi - base - 32 * u)) >>
+           (4 * h);
+  };
+  bool odd_values = false;
+  int page = page_of(begin);
+  uint64_t there = there_of(begin, page);
+  copy_tile(begin, page, 0);
+  page = page_of(begin + KT);
+  int buf = 0;
+  for (int base = begin; base < end; base += KT, buf ^= 1) {
+    wait_copies();
+    __syncthreads();
+    uint8_t *tk = lds[buf][0], *tv = lds[buf][1];
+    const uint64_t now = there;
+    if (!all_see(base, now)) {
+      bool odd = false;
+      // what is not there weighs nothing, and may hold anything
+      for (int i = threadIdx.x; i < KT * CH; i += 256) {
+        u32x4 *const at = (u32x4 *)(tv + 16 * i);
+        if (!(now >> (i / CH) & 1)) *at = u32x4{0, 0, 0, 0};
+        const u32x4 w = *at;
+        odd = odd || !(finite2<T>(w[0]) && finite2<T>(w[1]) && finite2<T>(w[2]) && finite2<T>(w[3]));
+      }
+      odd = __syncthreads_or(odd);
+      if (odd) {
+        odd_values = true;
+        for (int i = threadIdx.x; i < KT * CH; i += 256) {
+          u32x4 *const at = (u32x4 *)(tv + 16 * i);
+          const u32x4 w = *at;
+          *at = u32x4{only_finite2<T>(w[0]), only_finite2<T>(w[1]), only_finite2<T>(w[2]), only_finite2<T>(w[3])};
+        }
+        __syncthreads();
+      }
+    }
+    there = there_of(base + KT, page);
+    copy_tile(base + KT, page, buf ^ 1);
+    page = page_of(base + 2 * KT);
+    if (base >= wave_hi || base + KT <= wave_lo) continue;
+
+    f32x16 s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        const V8 key = *(const V8 *)(tk + (32 * u + c) * 2 * D + 16 * ((2 * t + h) ^ M::k_turn(c)));
+#pragma unroll
+        for (int k = 0; k < NT; ++k) s[u] = K::mfma32(key, q[t][k], s[u]);
+      }
+    }
+    const bool whole = base >= whole_lo && base + KT <= whole_hi && (now & kAll) == kAll;
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t mine = seen(base, now, u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = s[u][i];
+          s[u][i] = mine & 1u << (8 * (i / 4) + (i & 3)) ? x : -kInf;
+        }
+      }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+    top = max_of_row32(top) * scale;
+    if (__any(top > m + kSlack)) {
+      const float f = top > m ? exp2_of(m - top) : 1.0f;  // (of m = -inf, 0)
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= f;
+      m = fmaxf(m, top);
+    }
+    const float off = m == -kInf ? 0.0f : m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[u][i] = exp2_of(fmaf(s[u][i], scale, -off));
+        sum += s[u][i];
+      }
+      l += sum;
+    }
+#pragma unroll
+    for (int t = 0; t < KT / 16; ++t) {
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = s[t / 2][8 * (t & 1) + i];
+      V8 w[NT];
+      terms_of<T, NT>(p, w);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        // values 32 d + c of keys 16 t + 4 h + .. and 8 more
+        const int a16 = lane & 15, key = 16 * t + 4 * h + (a16 >> 2);
+        const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((a16 >> 1) & 1);
+        const uint8_t *at = tv + key * 2 * D + 16 * (piece ^ M::v_turn(a16 >> 2)) + 8 * (a16 & 1);
+        typedef __attribute__((address_space(3))) s16x4 *Lds;
+        struct {
+          s16x4 x[2];
+        } col = {{__builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4 *)at),
+                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4 *)(at + 16 * D))}};
+#pragma unroll
+        for (int k = 0; k < NT; ++k) o[d] = K::mfma32(__builtin_bit_cast(V8, col), w[k], o[d]);
+      }
+    }
+  }
+
+  if (odd_values) {
+    for (int base = begin; base < end; base += KT) {
+      const uint64_t now = there_of(base, page_of(base));
+      if (all_see(base, now) || base >= wave_hi || base + KT <= wave_lo) continue;
+      for (int kind = kNan; kind <= kDown; ++kind) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          f32x16 n;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) n[i] = 0.0f;
+          for (int t = 0; t < KT / 16; ++t) {
+            u32x4 is = {0, 0, 0, 0}, ones = {0, 0, 0, 0};
+            const uint32_t mine = seen(base, now, t / 2) >> (16 * (t & 1));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int key = min(base + 16 * t + 8 * (j / 4) + 4 * h + (j & 3), last_key);
+              const uint32_t v = *(const uint16_t *)(
+                  cv + key_at(a, key, table[key >> a.seqs.page_shift]).at + 2 * (32 * d + c));
+              is[j / 2] |= is_kind<T>(v, kind) << (16 * (j & 1));
+              ones[j / 2] |= (mine & 1u << (8 * (j / 4) + (j & 3)) ? K::kOne : 0) << (16 * (j & 1));
+            }
+            n = K::mfma32(__builtin_bit_cast(V8, is), __builtin_bit_cast(V8, ones), n);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] += of_kind(n[i], kind);
+        }
+      }
+    }
+  }
+
+  l = sum_of_row32(l);
+  if (!real) return;
+  if (it.parts == 1) {
+    const int64_t t = it.start + tok;
+    float f, lse;
+    finish_row(a, q_head, m, l, f, lse);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v[4] = {o[d][4 * i] * f, o[d][4 * i + 1] * f, o[d][4 * i + 2] * f, o[d][4 * i + 3] * f};
+        store_row(a.out, t, q_head, 32 * d + 8 * i + 4 * h, v);
+      }
+    if (a.lse && h == 0) a.lse[t * a.group * a.kv_heads + q_head] = lse;
+  } else {
+    const int64_t pr = ((int64_t)(it.first + it.part) * a.kv_heads + head) * kManyRows + 32 * wave + c;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(f32x4 *)(a.part + pr * D + 32 * d + 8 * i + 4 * h) =
+            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    if (h == 0) ((float2 *)(a.part + a.part_rows * D))[pr] = make_float2(m, l);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // The parts of a tile joined, where there are several: 16 lanes a row.
 // ---------------------------------------------------------------------------
 
@@ -552,8 +906,8 @@ template <int D, int ROWS, int PIECE> __global__ void __launch_bounds__(256) att
 
 // A call's shape: the rows of a tile, the most tiles and parts its sequences can have.
 struct AttendShape {
-  int64_t tiles, parts, rows;
-  int target;
+  int64_t tiles, parts;
+  int rows, target;
 };
 
 template <int T> hipError_t launch_attend(const AttendArgs &a, const AttendShape &s, int dim, bool wide,

@@ -14,13 +14,13 @@ constexpr int64_t kParts = 1024;
 AttendShape shape_of(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache) {
   AttendShape s = {};
   const int64_t group = q->n_head / cache->n_head, n_seq = seqs->n_seq;
-  s.rows = kFewRows;
+  s.rows = q->n_tok * group > 32 * n_seq ? kManyRows : kFewRows;
   // every sequence may end in a partial tile, of one row at least
   s.tiles = std::min(q->n_tok * group, q->n_tok * group / s.rows + n_seq);
   // enough tiles, or keys for one piece: nothing is cut
   const int64_t least = (q->n_tok * group + s.rows - 1) / s.rows * cache->n_head;
   const int64_t most_keys = seqs->max_pages * cache->page_size;
-  s.target = least >= kParts || most_keys <= kFewPiece ? 0 : (int)((kParts + cache->n_head - 1) / cache->n_head);
+  s.target = least >= kParts || most_keys <= kManyPiece ? 0 : (int)((kParts + cache->n_head - 1) / cache->n_head);
   s.parts = s.tiles + s.target;
   return s;
 }

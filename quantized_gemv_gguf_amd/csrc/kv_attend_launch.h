@@ -11,19 +11,22 @@ template <typename F> void in_grids(int64_t groups, F f) {
     f(first, dim3((unsigned)(groups - first < kMaxGrid ? groups - first : kMaxGrid)));
 }
 
-template <int T, int D, int NT> void launch_few(const AttendArgs &a, const AttendShape &s, hipStream_t stream) {
+template <int T, int D, int NT> void launch_rows(const AttendArgs &a, const AttendShape &s, hipStream_t stream) {
+  const bool few = s.rows == kFewRows;
   in_grids(s.parts * a.kv_heads, [&](int64_t first, dim3 grid) {
-    hipLaunchKernelGGL((attend_few_kernel<T, D, NT>), grid, dim3(256), 0, stream, a, first);
+    if (few) hipLaunchKernelGGL((attend_few_kernel<T, D, NT>), grid, dim3(256), 0, stream, a, first);
+    else hipLaunchKernelGGL((attend_many_kernel<T, D, NT>), grid, dim3(64 * kManyWaves), 0, stream, a, first);
   });
-  if (a.target > 0)
-    in_grids(s.tiles * a.kv_heads, [&](int64_t first, dim3 grid) {
-      hipLaunchKernelGGL((attend_join_kernel<D, kFewRows, kFewPiece>), grid, dim3(256), 0, stream, a, first);
-    });
+  if (a.target == 0) return;
+  in_grids(s.tiles * (s.rows / 16) * a.kv_heads, [&](int64_t first, dim3 grid) {
+    if (few) hipLaunchKernelGGL((attend_join_kernel<D, kFewRows, kFewPiece>), grid, dim3(256), 0, stream, a, first);
+    else hipLaunchKernelGGL((attend_join_kernel<D, kManyRows, kManyPiece>), grid, dim3(256), 0, stream, a, first);
+  });
 }
 
 template <int T, int D> void launch_dim(const AttendArgs &a, const AttendShape &s, bool wide, hipStream_t stream) {
-  if (wide) launch_few<T, D, Kind<T>::kWide>(a, s, stream);
-  else launch_few<T, D, 1>(a, s, stream);
+  if (wide) launch_rows<T, D, Kind<T>::kWide>(a, s, stream);
+  else launch_rows<T, D, 1>(a, s, stream);
 }
 
 template <int T>

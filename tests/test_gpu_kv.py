@@ -198,6 +198,15 @@ def test_attend_heads_and_types(dev, dim, x, c, y):
     check_attend(b, queries(b, 6, dim, x), y)
 
 
+@pytest.mark.parametrize("x,c,y", KINDS)
+@pytest.mark.parametrize("dim", DIMS)
+def test_attend_prompts_heads_and_types(dev, dim, x, c, y):
+    """Chunks of prompts, partial tiles of rows and keys among them."""
+    b = Batch(dev, [150, 61, 200], [75, 61, 1], 1, dim, c, seed=dim)
+    check_attend(b, queries(b, 2, dim, x), y)
+    check_attend(b, queries(b, 2, dim, x), y, window=50)
+
+
 LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 511, 513]
 
 

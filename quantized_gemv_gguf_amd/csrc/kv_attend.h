@@ -41,7 +41,7 @@ struct AttendArgs {
 };
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
+__device__ __forceinline__ float log2f_of(float x) { return __builtin_amdgcn_logf(x); }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -52,6 +52,8 @@ constexpr float kInf = __builtin_huge_valf();
 // that about `target` parts come out in all.  A wave does this for itself, its
 // lanes over the sequences: no barrier (64 sequences: 0.6 us).
 // ---------------------------------------------------------------------------
+
+constexpr int kFewRows = 16, kFewPiece = 128;
 
 struct Item {
   int s, tile, part, parts;  // parts: of this tile; 0: nothing to do
@@ -71,9 +73,29 @@ template <int ROWS, int PIECE> struct Plan {
     const int lo = a.window ? max(len - n - a.window + 1, 0) : 0;
     pieces = max(1, (len - min(lo, len) + PIECE - 1) / PIECE);
   }
+  // Pieces of a part.  One of many rows costs its sums' way through memory, as
+  // much as some pieces' products: it gets eight at least (100 new tokens of each
+  // of 4 sequences up to 4000, 32 heads over 8 of 128: 30 us, with sixteen 36).
+  __device__ int pieces_each(int64_t all) const {
+    return max((int)((all + a.target - 1) / a.target), ROWS == kFewRows ? 1 : 8);
+  }
   // The item of this number among parts (BY_TILE: among tiles).
   template <bool BY_TILE> __device__ Item find(int number) const {
     const int lane = threadIdx.x & 63, n_seq = a.seqs.n_seq;
+    if (n_seq == 1) {  // (the same without a scan: 1.2 us less of a launch's start)
+      int tiles, pieces;
+      size_of(0, tiles, pieces);
+      const int parts = a.target > 0 ? (pieces - 1) / pieces_each((int64_t)tiles * pieces) + 1 : 1;
+      const int tile = BY_TILE ? number : number / parts;
+      Item it = {};
+      if (tile >= tiles) return it;
+      it.parts = parts;
+      it.part = BY_TILE ? 0 : number - tile * parts;
+      it.first = tile * parts;
+      it.tile = tiles - 1 - tile;
+      seq_rows(a.seqs, 0, a.n_tok, it.start, it.n, it.len);
+      return it;
+    }
     int each = 0x7fffffff;  // pieces of a part
     if (a.target > 0) {
       int64_t all = 0;
@@ -84,8 +106,7 @@ template <int ROWS, int PIECE> struct Plan {
       }
 #pragma unroll
       for (int d = 32; d > 0; d /= 2) all += __shfl_xor(all, d);
-      each = (int)((all + a.target - 1) / a.target);
-      each = max(each, 1);
+      each = pieces_each(all);
     }
     Item it = {};
     int items = 0, parts_before = 0;  // of the sequences before s0
@@ -108,11 +129,13 @@ template <int ROWS, int PIECE> struct Plan {
         const int l = __builtin_ctzll(here);
         const int in = number - items - __builtin_amdgcn_readlane(sum - mine, l);
         const int p = __builtin_amdgcn_readlane(parts, l);
+        const int tile = BY_TILE ? in : in / p;
         it.s = s0 + l;
         it.parts = p;
-        it.tile = BY_TILE ? in : in / p;
-        it.part = BY_TILE ? 0 : in - it.tile * p;
-        it.first = parts_before + __builtin_amdgcn_readlane(sum_parts - mine_parts, l) + it.tile * p;
+        it.part = BY_TILE ? 0 : in - tile * p;
+        it.first = parts_before + __builtin_amdgcn_readlane(sum_parts - mine_parts, l) + tile * p;
+        // (the last rows, which see the most, first)
+        it.tile = __builtin_amdgcn_readlane(tiles, l) - 1 - tile;
         seq_rows(a.seqs, it.s, a.n_tok, it.start, it.n, it.len);
         return it;
       }
@@ -243,38 +266,13 @@ __device__ __forceinline__ void finish_row(const AttendArgs &a, int head, float 
   } else {
     f = l == 0.0f ? 0.0f : 1.0f / l;
   }
-  lse = l == 0.0f ? -kInf : (m + log2_of(l)) * kLn2;
+  lse = l == 0.0f ? -kInf : (m + log2f_of(l)) * kLn2;
 }
 
 template <int N> __device__ __forceinline__ void store_row(const Heads &h, int64_t t, int head, int at,
                                                            const float (&v)[N]) {
   store_as(h.type, h.p, t * h.tok_stride + head * h.head_stride + at, v);
 }
-
-// ---------------------------------------------------------------------------
-// Few rows: tiles of 16.  Bound by memory, so nothing is staged: each of four
-// waves takes every fourth 32 keys straight from the pages into the layout of
-// the matrix instructions (16 x 16 x 32), the next ones under way while it
-// computes.  A lane's 8 keys of v are rows of dim / 16 values; of value e of
-// each, the lane's column c makes column (c, e) of v, so the transposition that
-// V^T needs is 8 permutations of words a lane, and the order of v's columns
-// comes back when the sums are stored.
-// ---------------------------------------------------------------------------
-
-constexpr int kFewRows = 16, kFewPiece = 128, kFewWaves = 4;
-
-template <int T, int D, int NT> struct Few {
-  using K = Kind<T>;
-  using V8 = typename K::V8;
-  static constexpr int E = D / 16;  // values of a lane's part of a row of v
-  static constexpr int ST = D / 32; // steps of a product over a row of k
-  static constexpr int kAlign = E % 8 == 0 ? 16 : E % 4 == 0 ? 8 : 4;  // of that part
-  struct Keys {
-    u32x4 k[2][ST];     // keys base + 16 u + c, values 32 t + 8 g + ..
-    uint32_t v[8][E / 2];  // keys base + 16 (j / 4) + 4 g + j % 4, values E c + ..
-    uint32_t there;        // bit j: v's key j is
-  };
-};
 
 // Byte offset of a key's row in the cache's head, and whether its page is there.
 struct KeyAt {
@@ -286,20 +284,62 @@ __device__ __forceinline__ KeyAt key_at(const AttendArgs &a, int key, int page) 
   return {((there ? page : 0) * a.page_stride + (key & ((1 << a.seqs.page_shift) - 1)) * a.slot_stride) * 2, there};
 }
 
-constexpr int few_waves(int dim, int terms) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
+// One asynchronous copy of 16 bytes a lane to LDS at lds + 16 lane.  The
+// compiler's own waits would drain it before any read of LDS; here the kernels
+// wait themselves, a tile or more later.
+__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+}
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// Few rows: tiles of 16.  Bound by memory: each wave walks every kFewWaves-th 32
+// keys through a ring of its own in LDS, filled by asynchronous copies some
+// tiles ahead (no barrier, no registers for what is under way; lanes that are
+// next to each other copy what lies next to each other, which loads in the
+// layout of the matrix instructions would not: 64 requests an instruction
+// instead of 16, 160 us for the 64 sequences below).  16 x 16 x 32 instructions;
+// K^T comes by 16-byte reads, V^T by the transposing 8-byte ones.
+// A row of 2 D bytes begins at the same bank as another one, so its 16-byte
+// pieces lie at places exchanged by the key's low bits, differently for K and V:
+// as the reads that go together fall on different banks.
+// ---------------------------------------------------------------------------
+
+template <int D> struct FewTile {
+  static constexpr int CH = D / 8;                 // pieces of a row
+  static constexpr int kBytes = 32 * D * 2;        // of a tile's k or v
+  static constexpr int kWaves = D <= 128 ? 4 : 2;  // of a workgroup
+  static constexpr int kDepth = 2;                 // tiles of a ring
+  static constexpr int kBanks = D / 2 % 64;        // where the next row begins
+  static __host__ __device__ constexpr int k_turn(int key) {
+    return kBanks == 0 ? key & 15 : kBanks == 32 ? (key >> 1) & 7 : (key >> 2) & 3;
+  }
+  static __host__ __device__ constexpr int v_turn(int key) {
+    return kBanks == 0 ? (key & 7) << 1 : kBanks == 32 ? ((key >> 1) & 3) << 1 : ((key >> 2) & 1) << 1;
+  }
+};
 
 template <int T, int D, int NT>
-__global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(AttendArgs a, int64_t group0) {
-  using F = Few<T, D, NT>;
-  using K = typename F::K;
-  using V8 = typename F::V8;
-  constexpr int E = F::E, ST = F::ST;
-  constexpr int kStride = D + 4;  // of a row's sums in LDS: rows in other banks
-  __shared__ float sums[kFewWaves][kFewRows][kStride];
-  __shared__ float2 stats[kFewWaves][kFewRows];
+__global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(AttendArgs a, int64_t group0) {
+  using K = Kind<T>;
+  using V8 = typename K::V8;
+  using M = FewTile<D>;
+  constexpr int E = D / 16, ST = D / 32, CH = M::CH, W = M::kWaves, S = M::kDepth;
+  constexpr int kCopies = CH / 4;   // of 16 keys' k, or v
+  constexpr int kTileCopies = CH;   // of a tile
+  constexpr int kStride = D + 4;    // of a row's sums in LDS: rows in other banks
+  constexpr int kRing = W * S * 2 * M::kBytes, kSums = W * kFewRows * kStride * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing > kSums ? kRing : kSums];
+  __shared__ float2 stats[W][kFewRows];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const int number = (int)((group0 + blockIdx.x) / a.kv_heads), head = (int)(group0 + blockIdx.x - (int64_t)number * a.kv_heads);
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int number = (int)((group0 + blockIdx.x) / a.kv_heads);
+  const int head = (int)(group0 + blockIdx.x - (int64_t)number * a.kv_heads);
   const Item it = Plan<kFewRows, kFewPiece>(a).template find<false>(number);
   if (it.parts == 0) return;
   const Range range = range_of<kFewRows>(a, it);
@@ -308,6 +348,71 @@ __global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(Atten
   const int share = (pieces + it.parts - 1) / it.parts;
   const int begin = lo + min(pieces, it.part * share) * kFewPiece;
   const int end = min(range.hi, lo + min(pieces, (it.part + 1) * share) * kFewPiece);
+
+  const uint8_t *ck = (const uint8_t *)(a.k + head * a.head_stride), *cv = (const uint8_t *)(a.v + head * a.head_stride);
+  const int32_t *table = a.seqs.tables + it.s * a.seqs.max_pages;
+  const int last_key = max(end - 1, 0);
+  constexpr int kStep = 32 * W;
+  uint8_t *const ring = lds + wave * S * 2 * M::kBytes;
+  const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
+  const auto page_of = [&](int key) { return table[min(key, last_key) >> a.seqs.page_shift]; };
+  // (the same for a uniform key, through the scalar cache: waiting for a vector
+  // load would wait for the copies too)
+  const auto page_at = [&](int key) {
+    typedef const __attribute__((address_space(4))) int32_t *Constant;
+    return ((Constant)table)[min(key, last_key) >> a.seqs.page_shift];
+  };
+
+  // Where the lane's pieces of 16 keys lie, from the first key on: pages of 16
+  // slots and more hold all of them in a row, and then one address does.
+  const bool in_row = a.seqs.page_shift >= 4 && a.slot_stride < (1 << 24);
+  uint32_t k_off[kCopies], v_off[kCopies];
+#pragma unroll
+  for (int j = 0; j < kCopies; ++j) {
+    const int p = 64 * j + lane, key = p / CH, piece = p % CH;
+    k_off[j] = (uint32_t)(key * (int)a.slot_stride * 2 + 16 * (piece ^ M::k_turn(key)));
+    v_off[j] = (uint32_t)(key * (int)a.slot_stride * 2 + 16 * (piece ^ M::v_turn(key)));
+  }
+  const auto copy_tile = [&](int base, int slot) {
+    if (base >= end) return;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(ring_at + slot * 2 * M::kBytes);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key0 = base + 16 * h;
+      if (in_row) {
+        const int64_t at = key_at(a, min(key0, last_key), page_at(key0)).at;
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+          copy_to_lds(ck + at, k_off[j], to + 1024 * (h * kCopies + j));
+          copy_to_lds(cv + at, v_off[j], to + M::kBytes + 1024 * (h * kCopies + j));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+          const int p = 64 * j + lane, key = p / CH, piece = p % CH;
+          const int64_t at = key_at(a, min(key0 + key, last_key), page_of(key0 + key)).at;
+          copy_to_lds(ck + at + 16 * (piece ^ M::k_turn(key)), to + 1024 * (h * kCopies + j));
+          copy_to_lds(cv + at + 16 * (piece ^ M::v_turn(key)), to + M::kBytes + 1024 * (h * kCopies + j));
+        }
+      }
+    }
+  };
+  // Keys of the tile that are there, a bit each.
+  const auto there_of = [&](int base) -> uint32_t {
+    if (in_row) {
+      uint32_t there = ~bits_from(end - base);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if ((unsigned)page_at(base + 16 * h) >= (unsigned)a.n_pages) there &= ~(0xffffu << (16 * h));
+      return __builtin_amdgcn_readfirstlane(there);
+    }
+    const int key = base + (lane & 31);
+    return (uint32_t)__ballot((unsigned)page_of(key) < (unsigned)a.n_pages && key < end);
+  };
+
+  const int first = begin + 32 * wave;
+#pragma unroll
+  for (int i = 0; i < S; ++i) copy_tile(first + i * kStep, i);
 
   // the lane's q row
   const int row = it.tile * kFewRows + c, tok = row / a.group, q_head = head * a.group + row % a.group;
@@ -341,96 +446,53 @@ __global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(Atten
     for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
   }
 
-  const uint8_t *ck = (const uint8_t *)(a.k + head * a.head_stride), *cv = (const uint8_t *)(a.v + head * a.head_stride);
-  const int32_t *table = a.seqs.tables + it.s * a.seqs.max_pages;
-  // Pages of a round's keys: two of k's and, where pages hold fours of keys, two of v's.
-  const bool fours = a.seqs.page_shift >= 2;
-  const int last_key = max(end - 1, 0);
-  struct Pages {
-    int k[2], v[8];
-  };
-  const auto page_of = [&](int key) { return table[min(key, last_key) >> a.seqs.page_shift]; };
-  const auto load_pages = [&](int base, Pages &p) {
-    if (base >= end) return;
-    p.k[0] = page_of(base + c);
-    p.k[1] = page_of(base + 16 + c);
-    p.v[0] = page_of(base + 4 * g);
-    p.v[4] = page_of(base + 16 + 4 * g);
-    if (!fours) {
-#pragma unroll
-      for (int j = 1; j < 4; ++j) {
-        p.v[j] = page_of(base + 4 * g + j);
-        p.v[4 + j] = page_of(base + 16 + 4 * g + j);
-      }
-    }
-  };
-  const auto load_keys = [&](int base, const Pages &p, typename F::Keys &x) {
-    if (base >= end) return;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const KeyAt at = key_at(a, min(base + 16 * u + c, last_key), p.k[u]);
-#pragma unroll
-      for (int t = 0; t < ST; ++t) x.k[u][t] = *(const u32x4 *)(ck + at.at + 64 * t + 16 * g);
-    }
-    x.there = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int key = base + 16 * (j / 4) + 4 * g + (j & 3);
-      const KeyAt at = key_at(a, min(key, last_key), fours ? p.v[j & 4] : p.v[j]);
-      __builtin_memcpy(x.v[j], __builtin_assume_aligned(cv + at.at + 2 * E * c, F::kAlign), 2 * E);
-      x.there |= (uint32_t)(at.there && key < end) << j;
-    }
-  };
-
   f32x4 o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
   float m = -kInf, l = 0.0f;
-
-  const auto key_of = [&](int j) { return 16 * (j / 4) + 4 * g + (j & 3); };
-  // bit j: the lane's row sees its key j of those from base on
-  const auto seen_of = [&](int base, uint32_t there) {
-    const uint32_t in = (bits_from(see_lo - base) & ~bits_from(see_hi - base)) >> (4 * g);
-    return there & ((in & 15) | (in >> 12 & 0xf0));
-  };
-  const auto all_see = [&](int base, uint32_t there) {
-    return base >= range.all_lo && base + 32 <= range.all_hi && __all(there == 0xff);
-  };
   bool odd_values = false;
-  const auto compute = [&](int base, typename F::Keys &x) {
+
+  const auto all_see = [&](int base, uint32_t there) {
+    return base >= range.all_lo && base + 32 <= range.all_hi && there == ~0u;
+  };
+  // Bit j: the lane's row sees key 4 g + j of those from base on, or 12 + 4 g + j from bit 4 on.
+  const auto seen_of = [&](int base, uint32_t there) {
+    const uint32_t in = (there & bits_from(see_lo - base) & ~bits_from(see_hi - base)) >> (4 * g);
+    return (in & 15) | (in >> 12 & 0xf0);
+  };
+  const auto compute = [&](int base, uint8_t *tk) {
+    uint8_t *const tv = tk + M::kBytes;
     f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int t = 0; t < ST; ++t)
 #pragma unroll
-      for (int t = 0; t < ST; ++t)
+      for (int u = 0; u < 2; ++u) {
+        const V8 key = *(const V8 *)(tk + (16 * u + c) * 2 * D + 16 * ((4 * t + g) ^ M::k_turn(c)));
 #pragma unroll
-        for (int k = 0; k < NT; ++k) s[u] = K::mfma16(__builtin_bit_cast(V8, x.k[u][t]), q[t][k], s[u]);
+        for (int k = 0; k < NT; ++k) s[u] = K::mfma16(key, q[t][k], s[u]);
+      }
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = s[j / 4][j & 3];
-    const bool whole = all_see(base, x.there);
-    if (!whole) {
-      bool odd = false;
-      const uint32_t seen = seen_of(base, x.there);
+    const uint32_t there = there_of(base);
+    if (!all_see(base, there)) {
+      const uint32_t seen = seen_of(base, there);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool there = x.there >> j & 1;
         const float score = p[j];
         p[j] = seen >> j & 1 ? score : -kInf;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          if (!there) x.v[j][i] = 0;
-          odd = odd || !finite2<T>(x.v[j][i]);
-        }
       }
-      odd = __any(odd);
-      if (odd) {
-        odd_values = true;
+      // what is not there weighs nothing, and may hold anything
+      bool odd = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) x.v[j][i] = only_finite2<T>(x.v[j][i]);
+      for (int j = 0; j < CH / 2; ++j) {
+        u32x4 *const at = (u32x4 *)(tv + 16 * (64 * j + lane));
+        u32x4 w = *at;
+        if (!(there >> ((64 * j + lane) / CH) & 1)) w = u32x4{0, 0, 0, 0};
+        odd = odd || !(finite2<T>(w[0]) && finite2<T>(w[1]) && finite2<T>(w[2]) && finite2<T>(w[3]));
+        *at = u32x4{only_finite2<T>(w[0]), only_finite2<T>(w[1]), only_finite2<T>(w[2]), only_finite2<T>(w[3])};
       }
+      odd_values = odd_values || __any(odd);
     }
     float top = p[0];
 #pragma unroll
@@ -453,53 +515,48 @@ __global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(Atten
     terms_of<T, NT>(p, w);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      u32x4 col;  // value e of the lane's 8 rows
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        col[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][e / 2], x.v[2 * i][e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+      // value 16 e + c of keys 4 g + .. and 16 more
+      const int key = 4 * g + (c >> 2), piece = 2 * e + ((c >> 1) & 1);
+      const uint8_t *at = tv + key * 2 * D + 16 * (piece ^ M::v_turn(key)) + 8 * (c & 1);
+      typedef __attribute__((address_space(3))) s16x4 *Lds;
+      struct {
+        s16x4 x[2];
+      } col = {{__builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4 *)at),
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4 *)(at + 32 * D))}};
 #pragma unroll
       for (int k = 0; k < NT; ++k) o[e] = K::mfma16(__builtin_bit_cast(V8, col), w[k], o[e]);
     }
   };
 
-  {
-    constexpr int kStep = 32 * kFewWaves;
-    int base = begin + 32 * wave;
-    Pages pages = {};
-    typename F::Keys now = {}, next = {};
-    load_pages(base, pages);
-    load_keys(base, pages, now);
-    load_pages(base + kStep, pages);
-    for (; base < end; base += kStep) {
-      load_keys(base + kStep, pages, next);
-      load_pages(base + 2 * kStep, pages);
-      compute(base, now);
-      now = next;
-    }
+  int slot = 0;
+  for (int base = first; base < end; base += kStep) {
+    if (base + (S - 1) * kStep < end) wait_copies<(S - 1) * kTileCopies>();
+    else wait_copies<0>();
+    compute(base, ring + slot * 2 * M::kBytes);
+    wait_reads();
+    copy_tile(base + S * kStep, slot);
+    slot = slot + 1 < S ? slot + 1 : 0;
   }
   if (odd_values) {
-    for (int base = begin + 32 * wave; base < end; base += 32 * kFewWaves) {
-      int64_t at[8];
-      uint32_t there = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = min(base + key_of(j), last_key);
-        const KeyAt k = key_at(a, key, page_of(key));
-        at[j] = k.at;
-        there |= (uint32_t)(k.there && base + key_of(j) < end) << j;
-      }
+    for (int base = first; base < end; base += kStep) {
+      const uint32_t there = there_of(base);
       if (all_see(base, there)) continue;
       const uint32_t seen = seen_of(base, there);
+      int64_t at[8];
       u32x4 ones = {0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ones[j / 2] |= (seen >> j & 1 ? K::kOne : 0) << (16 * (j & 1));
+      for (int j = 0; j < 8; ++j) {
+        const int key = min(base + 16 * (j / 4) + 4 * g + (j & 3), last_key);
+        at[j] = key_at(a, key, page_of(key)).at;
+        ones[j / 2] |= (seen >> j & 1 ? K::kOne : 0) << (16 * (j & 1));
+      }
       for (int kind = kNan; kind <= kDown; ++kind) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           u32x4 is = {0, 0, 0, 0};
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            is[j / 2] |= is_kind<T>(*(const uint16_t *)(cv + at[j] + 2 * (E * c + e)), kind) << (16 * (j & 1));
+            is[j / 2] |= is_kind<T>(*(const uint16_t *)(cv + at[j] + 2 * (16 * e + c)), kind) << (16 * (j & 1));
           const f32x4 n = K::mfma16(__builtin_bit_cast(V8, is), __builtin_bit_cast(V8, ones), f32x4{0, 0, 0, 0});
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[e][i] += of_kind(n[i], kind);
@@ -508,44 +565,47 @@ __global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(Atten
     }
   }
 
-  // the four waves' sums joined; lane (row, part of the values) of 256
+  // the waves' sums joined, 16 lanes a row
   l = sum_of_row16(l);
   if (g == 0) stats[wave][c] = make_float2(m, l);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < E; ++e) sums[wave][c][(4 * g + i) * E + e] = o[e][i];
   __syncthreads();
-  const int r = threadIdx.x >> 4, at = (threadIdx.x & 15) * E;
-  float top = -kInf;
+  float *const sums = (float *)lds;
 #pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) top = fmaxf(top, stats[w][r].x);
-  float total = 0.0f, v[E];
+  for (int e = 0; e < E; ++e) *(f32x4 *)(sums + (wave * kFewRows + c) * kStride + 16 * e + 4 * g) = o[e];
+  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  for (int r0 = 0; r0 < kFewRows; r0 += 4 * W) {
+    const int r = r0 + (threadIdx.x >> 4), at = (threadIdx.x & 15) * E;
+    const int out_row = it.tile * kFewRows + r;
+    if (out_row >= it.n * a.group) return;
+    float top = -kInf;
 #pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) {
-    const float f = stats[w][r].x == -kInf ? 0.0f : exp2_of(stats[w][r].x - top);
-    total += stats[w][r].y * f;
+    for (int w = 0; w < W; ++w) top = fmaxf(top, stats[w][r].x);
+    float total = 0.0f, v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += sums[w][r][at + e] * f;
-  }
-  const int out_row = it.tile * kFewRows + r;
-  if (out_row >= it.n * a.group) return;
-  if (it.parts == 1) {
-    const int64_t t = it.start + out_row / a.group;
-    const int h = head * a.group + out_row % a.group;
-    float f, lse;
-    finish_row(a, h, top, total, f, lse);
+    for (int e = 0; e < E; ++e) v[e] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= f;
-    store_row(a.out, t, h, at, v);
-    if (a.lse && (threadIdx.x & 15) == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
-  } else {
-    const int64_t pr = ((int64_t)(it.first + it.part) * a.kv_heads + head) * kFewRows + r;
+    for (int w = 0; w < W; ++w) {
+      const float f = stats[w][r].x == -kInf ? 0.0f : exp2_of(stats[w][r].x - top);
+      total += stats[w][r].y * f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.part[pr * D + at + e] = v[e];
-    if ((threadIdx.x & 15) == 0) ((float2 *)(a.part + a.part_rows * D))[pr] = make_float2(top, total);
+      for (int e = 0; e < E; ++e) v[e] += sums[(w * kFewRows + r) * kStride + at + e] * f;
+    }
+    if (it.parts == 1) {
+      const int64_t t = it.start + out_row / a.group;
+      const int h = head * a.group + out_row % a.group;
+      float f, lse;
+      finish_row(a, h, top, total, f, lse);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= f;
+      store_row(a.out, t, h, at, v);
+      if (a.lse && (threadIdx.x & 15) == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
+    } else {
+      const int64_t pr = ((int64_t)(it.first + it.part) * a.kv_heads + head) * kFewRows + r;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a.part[pr * D + at + e] = v[e];
+      if ((threadIdx.x & 15) == 0) ((float2 *)(a.part + a.part_rows * D))[pr] = make_float2(top, total);
+    }
   }
 }
 
@@ -556,15 +616,19 @@ __global__ void __launch_bounds__(256, few_waves(D, NT)) attend_few_kernel(Atten
 // while one is computed.  32 x 32 x 16 instructions: a wave's q rows are their 32
 // columns; K^T comes by 16-byte reads, V^T by the transposing 8-byte ones, whose
 // four keys a lane are those of the scores' layout.
-// A row of 2 D bytes begins at the same bank as another one, so its 16-byte
-// pieces lie at places exchanged by the key's low bits, differently for K and V:
-// as the reads that go together fall on different banks.
+// Places of a row's pieces are exchanged as above.
 // The running maximum follows only when a row's grows by more than 8 (in powers
 // of 2): until then weights up to 256 are as exact, and the sums need no factor.
 // ---------------------------------------------------------------------------
 
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves, kManyPiece = 64;
 constexpr float kSlack = 8.0f;
+#ifndef PRE
+#define PRE 8
+#endif
+
+// Instructions that __builtin_amdgcn_sched_group_barrier puts in order.
+constexpr int kVector = 0x2, kMatrix = 0x8, kDsRead = 0x100, kTranscendental = 0x400;
 
 template <int D> struct ManyTile {
   static constexpr int KT = D <= 128 ? 64 : 32;  // keys
@@ -572,20 +636,12 @@ template <int D> struct ManyTile {
   static constexpr int kBytes = KT * D * 2;
   static constexpr int kBanks = D / 2 % 64;      // where the next row begins
   static __host__ __device__ constexpr int k_turn(int key) {
-    return kBanks == 0 ? key & 7 : kBanks == 32 ? (key >> 1) & 3 : (key >> 2) & 3;
+    return kBanks == 0 ? key & 15 : kBanks == 32 ? (key >> 1) & 7 : (key >> 2) & 3;
   }
   static __host__ __device__ constexpr int v_turn(int key) {
     return kBanks == 0 ? (key & 3) << 2 : kBanks == 32 ? ((key >> 1) & 1) << 2 : 0;
   }
 };
-
-// One asynchronous copy of 16 bytes a lane to LDS at lds + 16 lane.  The
-// compiler's own waits would drain it before any read of LDS; here the kernel
-// waits, a tile later.
-__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The largest, the sum of a value and the one 32 lanes away.
 __device__ __forceinline__ float max_of_row32(float x) {
@@ -606,7 +662,8 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   using V8 = typename K::V8;
   using M = ManyTile<D>;
   constexpr int KT = M::KT, CH = M::CH, U = KT / 32, ST = D / 16, DT = D / 32;
-  constexpr int kCopies = (KT * CH + 255) / 256;  // of a wave, for K, for V
+  // a wave copies a quarter of a tile's keys
+  constexpr int kKeys = KT / kManyWaves, kCopies = (kKeys * CH + 63) / 64;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][M::kBytes];  // of a tile: K, V
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, h = lane >> 5;
@@ -671,17 +728,37 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   const auto there_of = [&](int base, int page) {
     return __ballot((unsigned)page < (unsigned)a.n_pages && base + (lane & (KT - 1)) < end);
   };
+  // Where the lane's pieces of the wave's keys lie, from the first key on: pages
+  // of kKeys slots and more hold all of them in a row, and then one address does.
+  const bool in_row = a.seqs.page_shift >= log2_of(kKeys) && a.slot_stride < (1 << 24);
+  uint32_t k_off[kCopies], v_off[kCopies];
+#pragma unroll
+  for (int j = 0; j < kCopies; ++j) {
+    const int p = 64 * j + lane, key = min(p / CH, kKeys - 1), piece = p % CH;
+    k_off[j] = (uint32_t)(key * (int)a.slot_stride * 2 + 16 * (piece ^ M::k_turn(kKeys * wave + key)));
+    v_off[j] = (uint32_t)(key * (int)a.slot_stride * 2 + 16 * (piece ^ M::v_turn(kKeys * wave + key)));
+  }
+  const int first_key = __builtin_amdgcn_readfirstlane(kKeys * wave);
   const auto copy_tile = [&](int base, int page, int buf) {
     if (base >= end) return;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + buf * 2 * M::kBytes + first_key * CH * 16);
+    if (in_row) {
+      const int64_t at = key_at(a, min(base + first_key, last_key), __builtin_amdgcn_readlane(page, first_key)).at;
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) {
-      const int first = (j * kManyWaves + wave) * 64;
-      if (kCopies * 256 != KT * CH && first >= KT * CH) break;
-      const int p = first + lane, key = p / CH, piece = p - key * CH;
-      const int64_t at = key_at(a, min(base + key, last_key), __shfl(page, key)).at;
-      const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + buf * 2 * M::kBytes + first * 16);
-      copy_to_lds(ck + at + 16 * (piece ^ M::k_turn(key)), to);
-      copy_to_lds(cv + at + 16 * (piece ^ M::v_turn(key)), to + M::kBytes);
+      for (int j = 0; j < kCopies; ++j) {
+        if (kCopies * 64 > kKeys * CH && 64 * j + lane >= kKeys * CH) break;
+        copy_to_lds(ck + at, k_off[j], to + 1024 * j);
+        copy_to_lds(cv + at, v_off[j], to + M::kBytes + 1024 * j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) {
+        const int p = 64 * j + lane, key = min(p / CH, kKeys - 1) + first_key, piece = p % CH;
+        const int64_t at = key_at(a, min(base + key, last_key), __shfl(page, key)).at;
+        if (kCopies * 64 > kKeys * CH && p >= kKeys * CH) break;
+        copy_to_lds(ck + at + 16 * (piece ^ M::k_turn(key)), to + 1024 * j);
+        copy_to_lds(cv + at + 16 * (piece ^ M::v_turn(key)), to + M::kBytes + 1024 * j);
+      }
     }
   };
 
@@ -708,14 +785,14 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   page = page_of(begin + KT);
   int buf = 0;
   for (int base = begin; base < end; base += KT, buf ^= 1) {
-    wait_copies();
+    wait_copies<0>();
     __syncthreads();
     uint8_t *tk = lds[buf][0], *tv = lds[buf][1];
     const uint64_t now = there;
     if (!all_see(base, now)) {
       bool odd = false;
       // what is not there weighs nothing, and may hold anything
-      for (int i = threadIdx.x; i < KT * CH; i += 256) {
+      for (int i = threadIdx.x; i < KT * CH; i += 64 * kManyWaves) {
         u32x4 *const at = (u32x4 *)(tv + 16 * i);
         if (!(now >> (i / CH) & 1)) *at = u32x4{0, 0, 0, 0};
         const u32x4 w = *at;
@@ -724,7 +801,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
       odd = __syncthreads_or(odd);
       if (odd) {
         odd_values = true;
-        for (int i = threadIdx.x; i < KT * CH; i += 256) {
+        for (int i = threadIdx.x; i < KT * CH; i += 64 * kManyWaves) {
           u32x4 *const at = (u32x4 *)(tv + 16 * i);
           const u32x4 w = *at;
           *at = u32x4{only_finite2<T>(w[0]), only_finite2<T>(w[1]), only_finite2<T>(w[2]), only_finite2<T>(w[3])};
@@ -739,15 +816,24 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 
     f32x16 s[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < ST; ++t) {
+    for (int t = 0; t < ST; ++t)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
         const V8 key = *(const V8 *)(tk + (32 * u + c) * 2 * D + 16 * ((2 * t + h) ^ M::k_turn(c)));
 #pragma unroll
         for (int k = 0; k < NT; ++k) s[u] = K::mfma32(key, q[t][k], s[u]);
       }
+    // reads of LDS kPre products ahead
+    constexpr int kPre = U * ST < PRE ? U * ST : PRE;
+    __builtin_amdgcn_sched_group_barrier(kDsRead, kPre, 0);
+#pragma unroll
+    for (int i = 0; i < U * ST; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kMatrix, NT, 0);
+      if (i + kPre < U * ST) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
     }
     const bool whole = base >= whole_lo && base + KT <= whole_hi && (now & kAll) == kAll;
     if (!whole) {
@@ -866,42 +952,73 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 }
 
 // ---------------------------------------------------------------------------
-// The parts of a tile joined, where there are several: 16 lanes a row.
+// The parts of a tile joined, where there are several.  A workgroup takes
+// `rows` of the tile's rows (all 16 of few, or one where there are few tiles and
+// so may be hundreds of parts; 16 of many): groups of its lanes take a row's
+// every so many parts, 4 values a lane.
 // ---------------------------------------------------------------------------
 
-template <int D, int ROWS, int PIECE> __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int64_t group0) {
-  constexpr int E = D / 16, kGroups = ROWS / 16;  // workgroups of a tile
+template <int D, int ROWS, int PIECE>
+__global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int rows, int64_t group0) {
+  constexpr int kLanes = D / 4 <= 8 ? 8 : D / 4 <= 16 ? 16 : D / 4 <= 32 ? 32 : 64, kGroups = 256 / kLanes;
+  __shared__ f32x4 sums[kGroups][kLanes];
+  __shared__ float2 stats_of[kGroups];
   const int64_t group = group0 + blockIdx.x;
+  const int per = ROWS / rows;  // workgroups of a tile
   const int sub = (int)(group / a.kv_heads), head = (int)(group - (int64_t)sub * a.kv_heads);
-  const Item it = Plan<ROWS, PIECE>(a).template find<true>(sub / kGroups);
+  const Item it = Plan<ROWS, PIECE>(a).template find<true>(sub / per);
   if (it.parts < 2) return;
-  const int r = (sub % kGroups) * 16 + (threadIdx.x >> 4), at = (threadIdx.x & 15) * E;
-  const int row = it.tile * ROWS + r;
-  if (row >= it.n * a.group) return;
+  const int row0 = it.tile * ROWS + sub % per * rows, real = min(rows, it.n * a.group - row0);
+  if (real <= 0) return;
+  int each = kGroups;  // groups of a row
+  while (each > 1 && (each * real > kGroups || each >= 2 * it.parts)) each /= 2;
+  const int i = threadIdx.x / kLanes, at = 4 * (threadIdx.x % kLanes);
   const float2 *stats = (const float2 *)(a.part + a.part_rows * D);
-  const int64_t first = ((int64_t)it.first * a.kv_heads + head) * ROWS + r, step = (int64_t)a.kv_heads * ROWS;
-  float m = -kInf;
-  for (int p = 0; p < it.parts; ++p) m = fmaxf(m, stats[first + p * step].x);
-  float l = 0.0f, v[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  const int64_t step = (int64_t)a.kv_heads * ROWS;
+  for (int r0 = 0; r0 < real; r0 += kGroups / each) {
+    const int r = r0 + i / each, j = i % each, row = row0 + r;
+    const int64_t first = ((int64_t)it.first * a.kv_heads + head) * ROWS + row - it.tile * ROWS;
+    float m = -kInf, l = 0.0f;
+    f32x4 v = {0, 0, 0, 0};
+    if (r < real) {
+      for (int p = j; p < it.parts; p += each) m = fmaxf(m, stats[first + p * step].x);
 #pragma unroll 4
-  for (int p = 0; p < it.parts; ++p) {
-    const float2 s = stats[first + p * step];
-    const float f = s.x == -kInf ? 0.0f : exp2_of(s.x - m);
-    l += s.y * f;
-    const float *x = a.part + (first + p * step) * D + at;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += x[e] * f;
+      for (int p = j; p < it.parts; p += each) {
+        const float2 s = stats[first + p * step];
+        const float f = s.x == -kInf ? 0.0f : exp2_of(s.x - m);
+        l += s.y * f;
+        if (at < D) v += *(const f32x4 *)(a.part + (first + p * step) * D + at) * f;
+      }
+    }
+    if (each > 1) {
+      sums[i][at / 4] = v;
+      if (at == 0) stats_of[i] = make_float2(m, l);
+      __syncthreads();
+      if (j == 0) {
+        float top = m;
+        for (int k = 1; k < each; ++k) top = fmaxf(top, stats_of[i + k].x);
+        const float f = m == -kInf ? 0.0f : exp2_of(m - top);
+        l *= f;
+        v *= f;
+        for (int k = 1; k < each; ++k) {
+          const float2 s = stats_of[i + k];
+          const float fk = s.x == -kInf ? 0.0f : exp2_of(s.x - top);
+          l += s.y * fk;
+          v += sums[i + k][at / 4] * fk;
+        }
+        m = top;
+      }
+      __syncthreads();
+    }
+    if (r >= real || j > 0 || at >= D) continue;
+    const int64_t t = it.start + row / a.group;
+    const int h = head * a.group + row % a.group;
+    float f, lse;
+    finish_row(a, h, m, l, f, lse);
+    const float out[4] = {v[0] * f, v[1] * f, v[2] * f, v[3] * f};
+    store_row(a.out, t, h, at, out);
+    if (a.lse && at == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
   }
-  const int64_t t = it.start + row / a.group;
-  const int h = head * a.group + row % a.group;
-  float f, lse;
-  finish_row(a, h, m, l, f, lse);
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] *= f;
-  store_row(a.out, t, h, at, v);
-  if (a.lse && (threadIdx.x & 15) == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
 }
 
 // A call's shape: the rows of a tile, the most tiles and parts its sequences can have.

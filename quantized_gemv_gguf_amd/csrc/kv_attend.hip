@@ -8,19 +8,30 @@ using namespace qgemv_kv;
 
 namespace {
 
-// Parts of keys in flight: four workgroups a compute unit.
-constexpr int64_t kParts = 1024;
+// Workgroups of few rows that the compute units hold at once, by their LDS.
+int64_t few_at_once(int dim) {
+  const int64_t waves = dim <= 128 ? 4 : 2, lds = waves * 2 * 2 * 32 * dim * 2 + 1024;
+  return 256 * std::min<int64_t>(163840 / lds, 4);
+}
 
 AttendShape shape_of(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache) {
   AttendShape s = {};
   const int64_t group = q->n_head / cache->n_head, n_seq = seqs->n_seq;
   s.rows = q->n_tok * group > 32 * n_seq ? kManyRows : kFewRows;
+  const bool few = s.rows == kFewRows;
   // every sequence may end in a partial tile, of one row at least
   s.tiles = std::min(q->n_tok * group, q->n_tok * group / s.rows + n_seq);
-  // enough tiles, or keys for one piece: nothing is cut
+  // Parts to cut the keys into: of one sequence as many as run at once, of
+  // several, whose parts are not alike, half as many again.
+  int64_t parts = few ? few_at_once(cache->head_dim) * (n_seq > 1 ? 3 : 2) / 2 : 512;
+  // Enough tiles, or keys for one part: nothing is cut.  (256 tiles of many rows
+  // leave room for as many again, which pays for long keys only: 2000 new tokens
+  // of 2000, 32 heads over 8 of 128, 53 us, cut 63; 4000 of 4000, 8 heads, 83 and 70.)
   const int64_t least = (q->n_tok * group + s.rows - 1) / s.rows * cache->n_head;
   const int64_t most_keys = seqs->max_pages * cache->page_size;
-  s.target = least >= kParts || most_keys <= kManyPiece ? 0 : (int)((kParts + cache->n_head - 1) / cache->n_head);
+  const bool whole = few ? least >= parts || most_keys <= kFewPiece
+                         : least >= parts || most_keys <= 8 * kManyPiece || (least >= parts / 2 && most_keys <= 2048);
+  s.target = whole ? 0 : (int)((parts + cache->n_head - 1) / cache->n_head);
   s.parts = s.tiles + s.target;
   return s;
 }

@@ -14,13 +14,17 @@ template <typename F> void in_grids(int64_t groups, F f) {
 template <int T, int D, int NT> void launch_rows(const AttendArgs &a, const AttendShape &s, hipStream_t stream) {
   const bool few = s.rows == kFewRows;
   in_grids(s.parts * a.kv_heads, [&](int64_t first, dim3 grid) {
-    if (few) hipLaunchKernelGGL((attend_few_kernel<T, D, NT>), grid, dim3(256), 0, stream, a, first);
+    if (few) hipLaunchKernelGGL((attend_few_kernel<T, D, NT>), grid, dim3(64 * FewTile<D>::kWaves), 0, stream, a, first);
     else hipLaunchKernelGGL((attend_many_kernel<T, D, NT>), grid, dim3(64 * kManyWaves), 0, stream, a, first);
   });
   if (a.target == 0) return;
-  in_grids(s.tiles * (s.rows / 16) * a.kv_heads, [&](int64_t first, dim3 grid) {
-    if (few) hipLaunchKernelGGL((attend_join_kernel<D, kFewRows, kFewPiece>), grid, dim3(256), 0, stream, a, first);
-    else hipLaunchKernelGGL((attend_join_kernel<D, kManyRows, kManyPiece>), grid, dim3(256), 0, stream, a, first);
+  // few tiles are joined by many workgroups
+  const int rows = few ? s.tiles * a.kv_heads <= 128 ? 1 : 16 : s.tiles * a.kv_heads <= 128 ? 16 : kManyRows;
+  in_grids(s.tiles * (s.rows / rows) * a.kv_heads, [&](int64_t first, dim3 grid) {
+    if (few)
+      hipLaunchKernelGGL((attend_join_kernel<D, kFewRows, kFewPiece>), grid, dim3(256), 0, stream, a, rows, first);
+    else
+      hipLaunchKernelGGL((attend_join_kernel<D, kManyRows, kManyPiece>), grid, dim3(256), 0, stream, a, rows, first);
   });
 }
 

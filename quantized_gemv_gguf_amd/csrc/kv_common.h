@@ -89,7 +89,7 @@ int check_heads(const qg_heads *h, bool out, int64_t most_dim);
 int check_cache(const qg_kv_cache *c);
 int check_seqs(const qg_kv_seqs *q, const qg_kv_cache *c);
 
-inline int log2_of(int64_t v) {
+__host__ __device__ constexpr int log2_of(int64_t v) {
   int n = 0;
   while ((1ll << n) < v) ++n;
   return n;

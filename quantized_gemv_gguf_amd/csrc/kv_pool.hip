@@ -31,10 +31,28 @@ __device__ __forceinline__ int fresh(const int32_t *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// One holder fewer; the last one's page is free.
-__device__ __forceinline__ void let_go(const Pool &p, int page) {
-  if ((unsigned)page < (unsigned)p.n_pages && atomicSub(&p.refs[page], 1) == 1)
-    atomicAnd(&p.used[page >> 5], (int)~(1u << (page & 31)));
+// One holder fewer of a page (-1: none): was it the last?
+__device__ __forceinline__ bool let_go(const Pool &p, int page) {
+  return (unsigned)page < (unsigned)p.n_pages && atomicSub(&p.refs[page], 1) == 1;
+}
+
+// Clears the bits of free pages, of the lanes of a wave at once: a sequence's
+// pages often lie in a row, and 32 lanes' atomics on a word would wait for each
+// other (4500 pages of 24 sequences let go: 52 us, so 17).
+__device__ void mark_free(const Pool &p, int page, bool free) {
+  const int lane = threadIdx.x & 63, word = page >> 5;
+  uint64_t todo = __ballot(free);
+  for (int k = 0; k < 4 && todo; ++k) {
+    const int leader = __builtin_ctzll(todo), w = __builtin_amdgcn_readlane(word, leader);
+    const bool mine = free && word == w;
+    uint32_t bits = mine ? 1u << (page & 31) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) bits |= __shfl_xor(bits, d);
+    if (lane == leader) atomicAnd(&p.used[w], (int)~bits);
+    todo &= ~__ballot(mine);
+    free = free && !mine;
+  }
+  if (free) atomicAnd(&p.used[word], (int)~(1u << (page & 31)));
 }
 
 // The bits of the pages in word w of `used` that are in use; those past the last page are not looked at.
@@ -103,12 +121,25 @@ __device__ __forceinline__ int owner_of(const int *before, int n, int k) {
 }
 
 // ---------------------------------------------------------------------------
-// Growing and cutting.  One workgroup: a step's bookkeeping is a few hundred
-// sequences of which few need a page, so its time is that of a handful of
-// dependent passes over the lengths, and one over the bits of the pages in use
-// where any is needed (64 sequences over 200 000 pages: 25 KB).  Page lists
-// are walked by all threads alike, whosever pages they are.
+// Cutting, by as many workgroups as sequences and more: of 224 forks let go,
+// 42 000 entries, one takes 85 us.  Then growing, by one: a step's few hundred
+// sequences of which few need a page take it a handful of dependent passes over
+// the lengths, and one over the bits of the pages in use where any is needed
+// (200 000 pages: 25 KB).  Free pages are walked by all threads alike, whosever
+// they become.
 // ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(256) cut_kernel(Pool p, const int32_t *lens) {
+  const int s = blockIdx.x, len = length_of(p, s), want = lens[s];
+  if (want < 0 || want >= len) return;
+  const int end = pages_of(len, p.shift);
+  int32_t *mine = p.tables + s * p.max_pages;
+  for (int e0 = pages_of(want, p.shift) + blockIdx.y * 256; e0 < end; e0 += gridDim.y * 256) {
+    const int e = e0 + threadIdx.x, page = e < end ? mine[e] : -1;
+    mark_free(p, page, let_go(p, page));
+    if (e < end) mine[e] = -1;
+  }
+}
 
 __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t *lens) {
   __shared__ int pre[QG_MAX_SEQS], last[QG_MAX_SEQS];
@@ -116,21 +147,6 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
   const int n = p.n_seq, tid = threadIdx.x;
   int32_t *src = p.work + kHead, *dst = src + n, *list = dst + n;
   if (tid == 0) copies = 0;
-
-  // let go what is behind the new lengths
-  for (int s = tid; s < n; s += kThreads) {
-    const int len = length_of(p, s), want = lens[s] < 0 ? len : lens[s];
-    pre[s] = want < len ? pages_of(len, p.shift) - pages_of(want, p.shift) : 0;
-  }
-  __syncthreads();
-  const int gone = scan_array(pre, n);
-  for (int k = tid; k < gone; k += kThreads) {
-    const int s = owner_of(pre, n, k);
-    int32_t *e = p.tables + s * p.max_pages + pages_of(lens[s], p.shift) + (k - pre[s]);
-    let_go(p, *e);
-    *e = -1;
-  }
-  __syncthreads();
 
   // last pages that sequences want to grow into
   for (int s = tid; s < n; s += kThreads) {
@@ -183,10 +199,13 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
         free_bits = ~word_of(p, w0 + tid, &valid);
         free_bits &= valid;
       }
-      uint32_t found;
+      uint32_t found, taken = 0;
       int at = free_pages + (int)scan_threads(__popc(free_bits), &found);
-      for (; free_bits && at < total; free_bits &= free_bits - 1, ++at)
+      for (; free_bits && at < total; free_bits &= free_bits - 1, ++at) {
         list[at] = 32 * (w0 + tid) + __builtin_ctz(free_bits);
+        taken |= free_bits & -free_bits;
+      }
+      if (taken) atomicOr(&p.used[w0 + tid], (int)taken);
       free_pages += (int)found;
     }
     __syncthreads();
@@ -194,12 +213,14 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
   const int given = min(total, free_pages);
   for (int k = tid; k < given; k += kThreads) {
     const int s = owner_of(pre, n, k), share = (s + 1 < n ? pre[s + 1] : total) - pre[s];
-    if (pre[s] + share > free_pages) continue;
     const int page = list[k], r = k - pre[s], copied_page = last[s];
+    if (pre[s] + share > free_pages) {  // (given to one that does not find all of its own)
+      atomicAnd(&p.used[page >> 5], (int)~(1u << (page & 31)));
+      continue;
+    }
     const int at = pages_of(length_of(p, s), p.shift) - (copied_page >= 0) + r;
     p.tables[s * p.max_pages + at] = page;
     p.refs[page] = 1;
-    atomicOr(&p.used[page >> 5], (int)(1u << (page & 31)));
     if (copied_page >= 0 && r == 0) {
       atomicSub(&p.refs[copied_page], 1);  // (never the last: another holds it)
       const int i = atomicAdd(&copies, 1);
@@ -249,9 +270,10 @@ __global__ void __launch_bounds__(256) fork_give_kernel(Pool p, const int32_t *f
   const int len = p.work[kHead + p.n_seq * p.max_pages + s], n = pages_of(len, p.shift);
   // the old entries end where they do: -1 behind the length
   int32_t *mine = p.tables + s * p.max_pages;
-  for (int64_t e = blockIdx.y * 256 + threadIdx.x; e < p.max_pages; e += gridDim.y * 256) {
-    const int old = mine[e], now = e < n ? rows[e] : -1;
-    if (old >= 0) let_go(p, old);
+  for (int64_t e0 = blockIdx.y * 256; e0 < p.max_pages; e0 += gridDim.y * 256) {
+    const int64_t e = e0 + threadIdx.x;
+    const int old = e < p.max_pages ? mine[e] : -1, now = e < n ? rows[e] : -1;
+    mark_free(p, old, let_go(p, old));
     if (old != now) mine[e] = now;
   }
   if (blockIdx.y == 0 && threadIdx.x == 0) p.lens[s] = len;
@@ -420,7 +442,7 @@ Copy copy_of(const qg_kv_cache *cache) {
 
 // Copies the pairs of a pool's workspace, or n given ones.
 void launch_copy(const Copy &c, hipStream_t stream) {
-  constexpr int64_t kGroups = 4096;
+  constexpr int64_t kGroups = 2048;
   const int per = 256 / c.lanes;
   const int64_t all = c.n * c.layers * 2 * c.jobs;
   const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(kGroups, (all + per - 1) / per));
@@ -482,6 +504,7 @@ int qgemv_kv_resize(const qg_kv_pool *pool, const qg_kv_cache *cache, const int3
   if ((rc = check_pool_cache(pool, cache))) return rc;
   if (!lens) return QG_E_NULL;
   const Pool p = pool_of(pool);
+  hipLaunchKernelGGL(cut_kernel, rows_grid(pool), dim3(256), 0, stream, p, lens);
   hipLaunchKernelGGL(resize_kernel, dim3(1), dim3(kThreads), 0, stream, p, lens);
   Copy c = copy_of(cache);
   c.src = p.work + kHead;

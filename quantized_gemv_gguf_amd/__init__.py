@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Sequence
 
@@ -173,17 +174,17 @@ def lib():
         "qgemv_expert_combine_grad": ([P(qg_tensor), P(qg_tensor), _vp, _vp, _i32, P(qg_tensor), _vp, _vp],
                                       ctypes.c_int),
         "qgemv_rope_freqs": ([_i32, _f64, _i32, _f64, _f64, _f64, _f64, P(_f64), P(_f64)], ctypes.c_int),
-        "qgemv_rope": ([P(qg_heads), _vp, P(qg_rope), P(qg_heads), _i32, _vp], ctypes.c_int),
-        "qgemv_kv_append": ([P(qg_heads), P(qg_heads), P(qg_kv_seqs), P(qg_kv_cache), _i32, P(qg_rope), _vp,
-                             P(qg_heads), P(qg_heads), _vp], ctypes.c_int),
-        "qgemv_kv_attend": ([P(qg_heads), P(qg_kv_seqs), P(qg_kv_cache), _i32, P(qg_heads), ctypes.c_float, _i32,
+        "qgemv_rope": ([_vp, _vp, _vp, _vp, _i32, _vp], ctypes.c_int),
+        "qgemv_kv_append": ([_vp, _vp, _vp, _vp, _i32, _vp, _vp,
+                             _vp, _vp, _vp], ctypes.c_int),
+        "qgemv_kv_attend": ([_vp, _vp, _vp, _i32, _vp, ctypes.c_float, _i32,
                              _i32, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
-        "qgemv_kv_attend_bytes": ([P(qg_heads), P(qg_kv_seqs), P(qg_kv_cache)], _i64),
+        "qgemv_kv_attend_bytes": ([_vp, _vp, _vp], _i64),
         "qgemv_kv_pool_bytes": ([_i64, _i64, _i64], _i64),
-        "qgemv_kv_resize": ([P(qg_kv_pool), P(qg_kv_cache), _vp, _vp], ctypes.c_int),
-        "qgemv_kv_fork": ([P(qg_kv_pool), _vp, _vp], ctypes.c_int),
-        "qgemv_kv_compact": ([P(qg_kv_pool), P(qg_kv_cache), _vp], ctypes.c_int),
-        "qgemv_kv_copy": ([P(qg_kv_cache), _vp, _vp, _i64, _vp], ctypes.c_int),
+        "qgemv_kv_resize": ([_vp, _vp, _vp, _vp], ctypes.c_int),
+        "qgemv_kv_fork": ([_vp, _vp, _vp], ctypes.c_int),
+        "qgemv_kv_compact": ([_vp, _vp, _vp], ctypes.c_int),
+        "qgemv_kv_copy": ([_vp, _vp, _vp, _i64, _vp], ctypes.c_int),
         "qgemv_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "qgemv_last_hip_error": ([], ctypes.c_char_p),
         "qgemv_version": ([], ctypes.c_char_p),
@@ -942,79 +943,108 @@ class KvPool:
     work: object
 
 
-def _heads(t, name: str) -> qg_heads:
+# (packed as the header's structs: a ctypes.Structure takes several times as long to make; a decoded token's append
+# 15.4 -> 10.6 us a call)
+_HEADS, _ROPE, _CACHE = struct.Struct("Piiqiiqq"), struct.Struct("Piid"), struct.Struct("PPiiiiiiqqqqq")
+_SEQS, _POOL = struct.Struct("PPPiiq"), struct.Struct("PPPPiiqqPq")
+
+
+def _on(t, dev: int, name: str) -> int:
+    """The tensor's address, checked to be on the device that is current."""
+    if t.get_device() != dev:
+        _here(t, name)
+    return t.data_ptr()
+
+
+def _current() -> int:
     if _kinds is None:
         _torch_names()
+    return _device()
+
+
+def _heads(t, dev: int, name: str) -> bytes:
     kind = _kinds.get(t.dtype)
     if kind is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be (tokens, heads, head_dim)")
-    n, heads, dim = t.shape
-    if not n:  # (no memory behind it)
-        return qg_heads(None, kind, 0, 0, _c32(heads), _c32(dim), 0, dim)
     tok, head, unit = t.stride()
-    if unit != 1 and dim > 1:
+    if unit != 1 and shape[2] > 1:
         raise ValueError(f"the heads of {name} must be contiguous")
-    # (the stride of a single token or head says nothing)
-    head = head if heads > 1 else dim
-    return qg_heads(_here(t, name), kind, 0, n, _c32(heads), _c32(dim), tok if n > 1 else heads * head, head)
+    return _HEADS.pack(_on(t, dev, name), kind, 0, *shape, tok, head)
+
+
+def _ints(t, n: int, dev: int, name: str) -> int:
+    if t.dtype is not _int32:
+        raise TypeError(f"{name} must be int32")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} values, needs {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _on(t, dev, name)
 
 
 def _c32(n) -> int:
-    """A size for a C int: past 32 bits, where ctypes would cut it, the largest, which is refused."""
+    """A number for a C int: past 32 bits, where it would be cut, the largest, which is refused."""
     return max(min(int(n), 0x7fffffff), -0x80000000)
 
 
-def _rope(r: Rope) -> qg_rope:
-    if _kinds is None:
-        _torch_names()
+def _rope(r: Rope, dev: int) -> bytes:
     f = r.freqs
-    if f.dtype is not _float64 or f.dim() != 1:
-        raise TypeError("freqs must be a float64 vector")
-    return qg_rope(_array(f, f.numel(), "freqs", _float64, "float64"), _c32(2 * f.numel()), int(bool(r.interleaved)),
-                   float(r.mscale))
+    if f.dtype is not _float64 or f.dim() != 1 or not f.is_contiguous():
+        raise TypeError("freqs must be a contiguous float64 vector")
+    return _ROPE.pack(_on(f, dev, "freqs"), 2 * f.numel(), bool(r.interleaved), r.mscale)
 
 
-def _cache(c: KvCache) -> qg_kv_cache:
-    if _kinds is None:
-        _torch_names()
+def _cache(c: KvCache, dev: int) -> bytes:
     k, v = c.k, c.v
     kind = _kinds.get(k.dtype)
     if kind is None:
         raise TypeError(f"the cache must be float16 or bfloat16, not {k.dtype}")
-    if k.dim() != 5:
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 5:
         raise ValueError("the cache must be (layers, pages, heads, page_size, head_dim)")
-    strides = k.stride()
-    if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != strides:
+    if v.dtype is not k.dtype or v.shape != shape or v.stride() != strides:
         raise ValueError("k and v of the cache must have the same type, sizes and strides")
-    if strides[4] != 1:
+    layer, page, head, slot, unit = strides
+    if unit != 1:
         raise ValueError("the heads of the cache must be contiguous")
-    layers, pages, heads, size, dim = k.shape
-    return qg_kv_cache(_here(k, "k"), _here(v, "v"), kind, _c32(size), _c32(layers), _c32(heads), _c32(dim), 0, pages,
-                       *strides[:4])
+    layers, pages, heads, size, dim = shape
+    return _CACHE.pack(_on(k, dev, "k"), _on(v, dev, "v"), kind, size, layers, heads, dim, 0, pages, layer, page, head,
+                       slot)
 
 
-def _seqs(s: KvSeqs) -> qg_kv_seqs:
+def _seqs(s: KvSeqs, dev: int) -> bytes:
     n, pages = s.tables.shape
-    return qg_kv_seqs(_i32s(s.starts, n + 1, "starts"), _i32s(s.lens, n, "lens"),
-                      _i32s(s.tables, n * pages, "tables"), _c32(n), 0, pages)
+    return _SEQS.pack(_ints(s.starts, n + 1, dev, "starts"), _ints(s.lens, n, dev, "lens"),
+                      _ints(s.tables, n * pages, dev, "tables"), n, 0, pages)
 
 
-def _pool(p: KvPool) -> qg_kv_pool:
+def _pool(p: KvPool, dev: int) -> bytes:
     n, pages = p.tables.shape
     n_pages = p.refs.numel()
-    return qg_kv_pool(_i32s(p.tables, n * pages, "tables"), _i32s(p.lens, n, "lens"), _i32s(p.refs, n_pages, "refs"),
-                      _i32s(p.used, (n_pages + 31) // 32, "used"), _c32(n), _c32(p.page_size), pages, n_pages,
-                      *_work(p.work))
+    return _POOL.pack(_ints(p.tables, n * pages, dev, "tables"), _ints(p.lens, n, dev, "lens"),
+                      _ints(p.refs, n_pages, dev, "refs"), _ints(p.used, (n_pages + 31) // 32, dev, "used"), n,
+                      _c32(p.page_size), pages, n_pages, *_work(p.work, dev))
 
 
-def _work(t):
+def _work(t, dev: int):
     if t is None:
-        return None, 0
+        return 0, 0
     if not t.is_contiguous():
         raise ValueError("work must be contiguous")
-    return (_here(t, "work") if t.numel() else None), t.nbytes
+    return _on(t, dev, "work"), t.nbytes
+
+
+def _floats(t, n: int, dev: int, name: str) -> int:
+    if t.dtype is not _float32:
+        raise TypeError(f"{name} must be float32")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} values, needs {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _on(t, dev, name)
 
 
 def qgemv_rope_freqs(n_rot: int, base: float = 10000.0, scaling: int = ROPE_NONE, factor: float = 1.0,
@@ -1029,27 +1059,28 @@ def qgemv_rope_freqs(n_rot: int, base: float = 10000.0, scaling: int = ROPE_NONE
 def qgemv_rope(x, pos, rope: Rope, y, inverse: bool = False, stream=None) -> None:
     """y[t] = x[t] turned by its position ``pos[t]`` (int32), or ``inverse`` by -pos[t], the turn's gradient; ``y``
     may be ``x``."""
-    _check(lib().qgemv_rope(ctypes.byref(_heads(x, "x")), _i32s(pos, x.shape[0], "pos"), ctypes.byref(_rope(rope)),
-                            ctypes.byref(_heads(y, "y")), int(bool(inverse)), _here_stream(stream)), "qgemv_rope")
+    dev = _current()
+    _check(lib().qgemv_rope(_heads(x, dev, "x"), _ints(pos, x.shape[0], dev, "pos"), _rope(rope, dev),
+                            _heads(y, dev, "y"), bool(inverse), _here_stream(stream)), "qgemv_rope")
 
 
 def qgemv_kv_append(k, v, seqs: KvSeqs, cache: KvCache, layer: int, rope: Rope = None, pos=None, q=None, q_out=None,
                     stream=None) -> None:
     """The new tokens' keys, turned by ``rope``, and values into ``layer`` of the cache, and ``q`` turned into
     ``q_out``; by their positions in the sequence, or by ``pos`` (int32, one a row)."""
-    _check(lib().qgemv_kv_append(ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(v, "v")), ctypes.byref(_seqs(seqs)),
-                                 ctypes.byref(_cache(cache)), _c32(layer),
-                                 ctypes.byref(_rope(rope)) if rope is not None else None,
-                                 _i32s(pos, k.shape[0], "pos") if pos is not None else None,
-                                 ctypes.byref(_heads(q, "q")) if q is not None else None,
-                                 ctypes.byref(_heads(q_out, "q_out")) if q_out is not None else None,
-                                 _here_stream(stream)), "qgemv_kv_append")
+    dev = _current()
+    _check(lib().qgemv_kv_append(_heads(k, dev, "k"), _heads(v, dev, "v"), _seqs(seqs, dev), _cache(cache, dev),
+                                 _c32(layer), _rope(rope, dev) if rope is not None else None,
+                                 _ints(pos, k.shape[0], dev, "pos") if pos is not None else None,
+                                 _heads(q, dev, "q") if q is not None else None,
+                                 _heads(q_out, dev, "q_out") if q_out is not None else None, _here_stream(stream)),
+           "qgemv_kv_append")
 
 
 def qgemv_kv_attend_bytes(q, seqs: KvSeqs, cache: KvCache) -> int:
     """Bytes of ``work`` for a qgemv_kv_attend of these sizes."""
-    n = lib().qgemv_kv_attend_bytes(ctypes.byref(_heads(q, "q")), ctypes.byref(_seqs(seqs)),
-                                    ctypes.byref(_cache(cache)))
+    dev = _current()
+    n = lib().qgemv_kv_attend_bytes(_heads(q, dev, "q"), _seqs(seqs, dev), _cache(cache, dev))
     if n < 0:
         _check(n, "qgemv_kv_attend_bytes")
     return n
@@ -1059,11 +1090,12 @@ def qgemv_kv_attend(q, seqs: KvSeqs, cache: KvCache, layer: int, out, scale: flo
                     window: int = 0, sinks=None, lse=None, work=None, stream=None) -> None:
     """out = softmax(scale q k^T) v of the new tokens over their sequences' positions in ``layer``; ``sinks`` (float32,
     one a q head), ``lse`` (float32, tokens x q heads) and ``work`` (qgemv_kv_attend_bytes) as the header has them."""
-    n, heads = q.shape[:2]
-    _check(lib().qgemv_kv_attend(ctypes.byref(_heads(q, "q")), ctypes.byref(_seqs(seqs)), ctypes.byref(_cache(cache)),
-                                 _c32(layer), ctypes.byref(_heads(out, "out")), scale, int(bool(causal)), _c32(window),
-                                 _weights(sinks, heads, "sinks") if sinks is not None else None,
-                                 _weights(lse, n * heads, "lse") if lse is not None else None, *_work(work),
+    dev = _current()
+    n, heads, _ = q.shape
+    _check(lib().qgemv_kv_attend(_heads(q, dev, "q"), _seqs(seqs, dev), _cache(cache, dev), _c32(layer),
+                                 _heads(out, dev, "out"), scale, bool(causal), _c32(window),
+                                 _floats(sinks, heads, dev, "sinks") if sinks is not None else None,
+                                 _floats(lse, n * heads, dev, "lse") if lse is not None else None, *_work(work, dev),
                                  _here_stream(stream)), "qgemv_kv_attend")
 
 
@@ -1078,28 +1110,31 @@ def qgemv_kv_pool_bytes(n_seq: int, max_pages: int, n_pages: int) -> int:
 def qgemv_kv_resize(pool: KvPool, cache: KvCache, lens, stream=None) -> None:
     """Cuts and grows the sequences to ``lens`` (int32; negative: as it is), copying shared pages they grow into;
     ``pool.lens`` tells which found room."""
-    _check(lib().qgemv_kv_resize(ctypes.byref(_pool(pool)), ctypes.byref(_cache(cache)),
-                                 _i32s(lens, pool.tables.shape[0], "lens"), _here_stream(stream)), "qgemv_kv_resize")
+    dev = _current()
+    _check(lib().qgemv_kv_resize(_pool(pool, dev), _cache(cache, dev), _ints(lens, pool.tables.shape[0], dev, "lens"),
+                                 _here_stream(stream)), "qgemv_kv_resize")
 
 
 def qgemv_kv_fork(pool: KvPool, parents, stream=None) -> None:
     """All at once every sequence s becomes what ``parents[s]`` (int32) was, sharing its pages; -1 lets s go."""
-    _check(lib().qgemv_kv_fork(ctypes.byref(_pool(pool)), _i32s(parents, pool.tables.shape[0], "parents"),
+    dev = _current()
+    _check(lib().qgemv_kv_fork(_pool(pool, dev), _ints(parents, pool.tables.shape[0], dev, "parents"),
                                _here_stream(stream)), "qgemv_kv_fork")
 
 
 def qgemv_kv_compact(pool: KvPool, cache: KvCache, stream=None) -> None:
     """Moves the pages in use to the lowest numbers."""
-    _check(lib().qgemv_kv_compact(ctypes.byref(_pool(pool)), ctypes.byref(_cache(cache)), _here_stream(stream)),
-           "qgemv_kv_compact")
+    dev = _current()
+    _check(lib().qgemv_kv_compact(_pool(pool, dev), _cache(cache, dev), _here_stream(stream)), "qgemv_kv_compact")
 
 
 def qgemv_kv_copy(cache: KvCache, src, dst, stream=None) -> None:
     """Page src[i] to page dst[i] (int32) in every layer."""
+    dev = _current()
     n = src.numel()
     if dst.numel() != n:
         raise ValueError("src and dst must be of the same length")
-    _check(lib().qgemv_kv_copy(ctypes.byref(_cache(cache)), _i32s(src, n, "src"), _i32s(dst, n, "dst"), n,
+    _check(lib().qgemv_kv_copy(_cache(cache, dev), _ints(src, n, dev, "src"), _ints(dst, n, dev, "dst"), n,
                                _here_stream(stream)), "qgemv_kv_copy")
 
 

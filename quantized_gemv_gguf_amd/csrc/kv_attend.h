@@ -623,13 +623,6 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
 
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves, kManyPiece = 64;
 constexpr float kSlack = 8.0f;
-#ifndef PRE
-#define PRE 8
-#endif
-
-// Instructions that __builtin_amdgcn_sched_group_barrier puts in order.
-constexpr int kVector = 0x2, kMatrix = 0x8, kDsRead = 0x100, kTranscendental = 0x400;
-
 template <int D> struct ManyTile {
   static constexpr int KT = D <= 128 ? 64 : 32;  // keys
   static constexpr int CH = D / 8;               // pieces of a row
@@ -654,7 +647,7 @@ __device__ __forceinline__ float sum_of_row32(float x) {
 }
 
 // Waves a SIMD: as many as their sums and rows leave registers for.
-constexpr int many_waves(int dim, int terms) { return dim <= 64 && terms == 1 ? 3 : dim * (1 + terms) <= 256 ? 2 : 1; }
+constexpr int many_waves(int dim, int terms) { return dim <= 96 && terms == 1 ? 3 : dim * (1 + terms) <= 256 ? 2 : 1; }
 
 template <int T, int D, int NT>
 __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_many_kernel(AttendArgs a, int64_t group0) {
@@ -689,32 +682,6 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   const int wave_hi = row0 < rows ? (a.causal ? old + last_tok + 1 : it.len) : 0;
   const int whole_lo = a.window ? max(old + last_tok - a.window + 1, 0) : 0;
   const int whole_hi = a.causal ? old + first_tok + 1 : it.len;
-  V8 q[ST][NT];
-  float scale = a.scale;
-  {
-    float x[ST][8];
-    float most = 0.0f;
-#pragma unroll
-    for (int t = 0; t < ST; ++t) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[t][i] = 0.0f;
-      if (real)
-        load_as(a.q.type, a.q.p, (it.start + tok) * a.q.tok_stride + q_head * a.q.head_stride + 16 * t + 8 * h, x[t]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[t][i]));
-    }
-    if (T == QG_F16 && NT > 1) {
-      const int e = row_exponent(max_of_row32(most));
-      scale = ldexpf(scale, e);
-#pragma unroll
-      for (int t = 0; t < ST; ++t)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[t][i] = ldexpf(x[t][i], -e);
-    }
-#pragma unroll
-    for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
-  }
-
   const uint8_t *ck = (const uint8_t *)(a.k + head * a.head_stride), *cv = (const uint8_t *)(a.v + head * a.head_stride);
   const int32_t *table = a.seqs.tables + it.s * a.seqs.max_pages;
   const int last_key = max(end - 1, 0);
@@ -783,6 +750,32 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   uint64_t there = there_of(begin, page);
   copy_tile(begin, page, 0);
   page = page_of(begin + KT);
+
+  V8 q[ST][NT];
+  float scale = a.scale;
+  {
+    float x[ST][8];
+    float most = 0.0f;
+#pragma unroll
+    for (int t = 0; t < ST; ++t) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[t][i] = 0.0f;
+      if (real)
+        load_as(a.q.type, a.q.p, (it.start + tok) * a.q.tok_stride + q_head * a.q.head_stride + 16 * t + 8 * h, x[t]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[t][i]));
+    }
+    if (T == QG_F16 && NT > 1) {
+      const int e = row_exponent(max_of_row32(most));
+      scale = ldexpf(scale, e);
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[t][i] = ldexpf(x[t][i], -e);
+    }
+#pragma unroll
+    for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
+  }
   int buf = 0;
   for (int base = begin; base < end; base += KT, buf ^= 1) {
     wait_copies<0>();
@@ -827,14 +820,6 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 #pragma unroll
         for (int k = 0; k < NT; ++k) s[u] = K::mfma32(key, q[t][k], s[u]);
       }
-    // reads of LDS kPre products ahead
-    constexpr int kPre = U * ST < PRE ? U * ST : PRE;
-    __builtin_amdgcn_sched_group_barrier(kDsRead, kPre, 0);
-#pragma unroll
-    for (int i = 0; i < U * ST; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kMatrix, NT, 0);
-      if (i + kPre < U * ST) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
-    }
     const bool whole = base >= whole_lo && base + KT <= whole_hi && (now & kAll) == kAll;
     if (!whole) {
 #pragma unroll

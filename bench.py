@@ -26,7 +26,9 @@ Other workloads (--workload): q4_0_4096, moe_mxfp4, ffn_streamed, q8_0_256, and
 q4_k_m_dense20b (the same pass with Q4_K QKV/out/up and a Q6_K down
 projection, 12.9 GB), dense20b_batch (--batch tokens per step through
 qgemv_rows_batch), moe_streamed (the MoE experts streamed from pinned host
-memory: ring, plan and zero copy).  ffn_streamed takes --leg to run one of
+memory: ring, plan and zero copy), dense20b_context (the pass with the
+attention of its token over --context cached positions in place of the V
+third).  ffn_streamed takes --leg to run one of
 its ring, plan or zero-copy legs alone.
 """
 from __future__ import annotations
@@ -1233,6 +1235,94 @@ def dense_batch_workload(args, dev):
                        "pass": bool(worst <= TOL)}}
 
 
+def dense_context_workload(args, dev):
+    """The dense 20B-class pass with attention over a paged fp16 cache: 64 heads
+    of 96, a quarter of each turned by its position, --context positions of
+    synthetic keys and values.  The prompt's sequence is forked, and the fork
+    decodes: a token makes room in the pool (the first copies the shared last
+    page), and between a layer's QKV and output products come qgemv_kv_append
+    and qgemv_kv_attend.  A token is one HIP graph (--eager: issued from the
+    host).  The rate counts weight bytes only, as the pass without attention
+    does; the cache's are reported beside it."""
+    import torch
+    import quantized_gemv_gguf_amd as q
+    c = synth.CONFIGS[5]
+    layers = args.layers or c["layers"]
+    H, heads, rot, size = c["hidden"], 64, 24, 16
+    dim, n0 = H // heads, args.context
+    if n0 < 1:
+        raise SystemExit("bench.py: --context must be at least 1")
+    model = DensePass(layers, H, c["ffn"], dev)
+    total = n0 + args.warmup + args.steps + 2  # (and what is run before a capture)
+    wide = -(-total // size)
+    pages = 2 * wide
+    i32 = dict(dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(synth.seed_of(5, 500))
+    cache = q.KvCache(*(torch.randn(layers, pages, heads, size, dim, generator=g, dtype=torch.float16, device=dev)
+                        for _ in range(2)))
+    pool = q.KvPool(torch.full((2, wide), -1, **i32), torch.zeros(2, **i32), torch.zeros(pages, **i32),
+                    torch.zeros(-(-pages // 32), **i32), size,
+                    torch.empty(q.qgemv_kv_pool_bytes(2, wide, pages), dtype=torch.uint8, device=dev))
+    q.qgemv_kv_resize(pool, cache, torch.tensor([n0, -1], **i32))
+    q.qgemv_kv_fork(pool, torch.tensor([0, 0], **i32))
+    freqs, mscale = q.qgemv_rope_freqs(rot)
+    rope = q.Rope(torch.tensor(freqs, dtype=torch.float64, device=dev), mscale=mscale)
+    seqs = q.KvSeqs(torch.tensor([0, 0, 1], **i32), pool.lens, pool.tables)
+    parts = [model.qkv[i * H:(i + 1) * H].view(1, heads, dim) for i in range(3)]
+    turned, att = (torch.empty(1, heads, dim, dtype=torch.float32, device=dev) for _ in range(2))
+    work = torch.empty(q.qgemv_kv_attend_bytes(turned, seqs, cache), dtype=torch.uint8, device=dev)
+    grown, one = torch.tensor([-1, n0], **i32), torch.tensor([0, 1], **i32)
+
+    def token(only_attention=False):
+        st = torch.cuda.current_stream().cuda_stream
+        if not only_attention:
+            grown.add_(one)
+            q.qgemv_kv_resize(pool, cache, grown)
+        for i, (mp, r, xp, yp, _, _, m, out_op) in enumerate(model.fcalls):
+            if not only_attention:
+                rc = model.lib.qgemv_rows_op(mp, 0, r, att.data_ptr() if m == 1 else xp, None, q.IN_RMS, model.eps,
+                                             out_op, yp, 0, st)
+                if rc != 0:
+                    raise RuntimeError(f"qgemv_rows_op failed: {rc}")
+            if m == 0:
+                q.qgemv_kv_append(parts[1], parts[2], seqs, cache, i // 4, rope=rope, q=parts[0], q_out=turned)
+                q.qgemv_kv_attend(turned, seqs, cache, i // 4, att, scale=dim ** -0.5, work=work)
+
+    def replayed(f):
+        if args.eager:
+            return f
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            f()
+        return graph.replay
+
+    model.reset_fused()
+    token()
+    torch.cuda.synchronize()
+    run = replayed(token)
+    for _ in range(args.warmup):
+        run()
+    wall, _ = _timed(lambda i: run(), args.steps, torch)
+    n = int(pool.lens[1])
+    # the last layer's attention of the last token, in 64 bits
+    k, v = (t[layers - 1][pool.tables[1, :-(-n // size)].long()].transpose(0, 1).reshape(heads, -1, dim)[:, :n].double()
+            for t in (cache.k, cache.v))
+    w = torch.softmax((k @ turned[0].double()[..., None])[..., 0] * dim ** -0.5, -1)
+    want = (w[:, None] @ v)[:, 0]
+    off = float((att[0].double() - want).abs().max() / want.abs().max())
+    alone = replayed(lambda: token(only_attention=True))
+    alone()
+    wall_a, _ = _timed(lambda i: alone(), args.steps, torch)
+    per = wall / args.steps
+    return {"value": model.bytes_per_token / per / 1e9, "ms_per_step": per * 1e3, "tokens_per_s": 1 / per,
+            "bytes_per_token": model.bytes_per_token, "cache_bytes_per_token": 2 * 2 * layers * n * H,
+            "attention_ms_per_token": wall_a / args.steps * 1e3,
+            "config": {"workload": c["name"] + "_context", "layers": layers, "format": FMT_LABEL[5], "heads": heads,
+                       "head_dim": dim, "n_rot": rot, "context": n0, "cache": "f16, pages of 16",
+                       "launch": "eager" if args.eager else "one HIP graph per token"},
+            "parity": {"attention_max_rel": off, "tol": TOL, "length": n, "pass": bool(off <= TOL and n == total - 1)}}
+
+
 def kquant_dense_workload(args, dev):
     """The dense 20B-class pass in the Q4_K_M mix: Q4_K QKV, out and up, Q6_K down."""
     return dense_workload(args, dev, cfg=6)
@@ -1241,7 +1331,7 @@ def kquant_dense_workload(args, dev):
 WORKLOADS = {"dense20b": dense_workload, "q4_0_4096": q4_0_workload, "moe_mxfp4": moe_workload,
              "ffn_streamed": ffn_streamed_workload, "q8_0_256": q8_0_small_workload,
              "q4_k_m_dense20b": kquant_dense_workload, "dense20b_batch": dense_batch_workload,
-             "moe_streamed": moe_streamed_workload}
+             "moe_streamed": moe_streamed_workload, "dense20b_context": dense_context_workload}
 
 
 def extra_configs(args, dev):
@@ -1315,6 +1405,7 @@ def main(argv=None):
     p.add_argument("--leg", default="all", choices=["all", "ring", "plan", "mapped"],
                    help="ffn_streamed: which streamed modes to run")
     p.add_argument("--batch", type=int, default=4, help="tokens per step of dense20b_batch")
+    p.add_argument("--context", type=int, default=4096, help="cached positions of dense20b_context")
     p.add_argument("--kquant", action="store_true", help="dense20b_batch in the Q4_K_M mix")
     p.add_argument("--mfma", action="store_true",
                    help="dense20b_batch through qgemv_rows_mfma (fp32 matrix cores, 16 tokens per pass)")

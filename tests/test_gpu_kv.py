@@ -662,3 +662,19 @@ def test_offsets_past_32_bits(dev):
     q.qgemv_kv_append(x[:, :1].to(dev), x[:, 1:].to(dev), b.seqs, b.cache, 0)
     page = int(tables[0, 99 // size])
     assert torch.equal(k[0, page, 0, 99 % size].cpu(), x[1, 0]) and torch.equal(v[0, page, 0, 99 % size].cpu(), x[1, 1])
+
+
+def test_bench_pass_with_attention(dev):
+    """The benchmark's pass over a context, eager and replayed: parity of its attention, and room for every token."""
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for more in ([], ["--eager"]):
+        r = subprocess.run([sys.executable, os.path.join(root, "bench.py"), "--workload", "dense20b_context", "--layers", "1",
+                            "--context", "37", "--steps", "3", "--warmup", "1", *more], capture_output=True, text=True,
+                           timeout=100, cwd=root)
+        assert r.returncode == 0, r.stderr[-2000:]
+        line = json.loads(r.stdout.strip().splitlines()[-1])
+        assert line["parity"]["pass"], line["parity"]

@@ -45,7 +45,8 @@ extern "C" {
  * t * tok_stride + h * head_stride of data, its head_dim elements contiguous
  * (a slice of a QKV product's rows has the product's row length as tok_stride).
  * data aligned to one element; strides >= 0, an output's heads may not overlap
- * (QG_E_ARG). */
+ * (QG_E_ARG).  Inputs and outputs of one call must not overlap, but where it
+ * says so. */
 typedef struct qg_heads {
   void *data;
   int32_t type;     /* enum qg_float */

@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
   };
 
   // Where the lane's pieces of 16 keys lie, from the first key on: pages of 16
-  // slots and more hold all of them in a row, and then one address does.
+  // slots and more hold all of them in a row, and then one address does.  (Behind
+  // the last key its own 16 are copied again.)
   const bool in_row = a.seqs.page_shift >= 4 && a.slot_stride < (1 << 24);
   uint32_t k_off[kCopies], v_off[kCopies];
 #pragma unroll
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
     for (int h = 0; h < 2; ++h) {
       const int key0 = base + 16 * h;
       if (in_row) {
-        const int64_t at = key_at(a, min(key0, last_key), page_at(key0)).at;
+        const int64_t at = key_at(a, min(key0, last_key & ~15), page_at(key0)).at;
 #pragma unroll
         for (int j = 0; j < kCopies; ++j) {
           copy_to_lds(ck + at, k_off[j], to + 1024 * (h * kCopies + j));
@@ -697,6 +698,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   };
   // Where the lane's pieces of the wave's keys lie, from the first key on: pages
   // of kKeys slots and more hold all of them in a row, and then one address does.
+  // (Behind the last key its own kKeys are copied again.)
   const bool in_row = a.seqs.page_shift >= log2_of(kKeys) && a.slot_stride < (1 << 24);
   uint32_t k_off[kCopies], v_off[kCopies];
 #pragma unroll
@@ -710,7 +712,8 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
     if (base >= end) return;
     const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + buf * 2 * M::kBytes + first_key * CH * 16);
     if (in_row) {
-      const int64_t at = key_at(a, min(base + first_key, last_key), __builtin_amdgcn_readlane(page, first_key)).at;
+      const int64_t at =
+          key_at(a, min(base + first_key, last_key & -kKeys), __builtin_amdgcn_readlane(page, first_key)).at;
 #pragma unroll
       for (int j = 0; j < kCopies; ++j) {
         if (kCopies * 64 > kKeys * CH && 64 * j + lane >= kKeys * CH) break;

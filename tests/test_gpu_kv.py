@@ -678,3 +678,102 @@ def test_bench_pass_with_attention(dev):
         assert r.returncode == 0, r.stderr[-2000:]
         line = json.loads(r.stdout.strip().splitlines()[-1])
         assert line["parity"]["pass"], line["parity"]
+
+
+def test_two_graphs_with_workspaces_of_their_own(dev):
+    """Two captured calls replayed in turn and at once, with eager work between: every replay has the eager bits."""
+    runs = []
+    for seed, lens, new, kind in ((1, [3000, 70], [1, 1], "bf16"), (2, [900, 2500], [40, 3], "f16")):
+        b = Batch(dev, lens, new, 2, 64, kind, seed=seed)
+        x = queries(b, 8, 64, kind).to(dev)
+        out, lse = torch.zeros_like(x), torch.zeros(b.rows, 8, device=dev)
+        work = torch.empty(q.qgemv_kv_attend_bytes(x, b.seqs, b.cache), dtype=torch.uint8, device=dev)
+
+        def call(b=b, x=x, out=out, lse=lse, work=work):
+            q.qgemv_kv_attend(x, b.seqs, b.cache, 1, out, scale=0.2, lse=lse, work=work)
+
+        call()
+        torch.cuda.synchronize()
+        want = out.clone(), lse.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, out, lse, want, call))
+    side = torch.cuda.Stream()
+    for turn in range(4):
+        for graph, out, lse, want, call in runs:
+            out.fill_(7.0)
+            lse.fill_(7.0)
+        if turn == 3:
+            runs[1][4]()  # eager between
+        torch.cuda.synchronize()
+        runs[0][0].replay()
+        with torch.cuda.stream(side):
+            runs[1][0].replay()
+        torch.cuda.synchronize()
+        for graph, out, lse, want, call in runs:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_append_captured(dev):
+    """Lengths that change on the device between replays: each replay stores at its own positions."""
+    b = Batch(dev, [40, 9], [2, 1], 2, 64, "f16", seed=3)
+    g = gen(5)
+    x = torch.randn(3, 2, 64, generator=g).to(dev)
+    r = rope_of(64, dev)
+    graph = torch.cuda.CUDAGraph()
+    q.qgemv_kv_append(x, x, b.seqs, b.cache, 0, rope=r)
+    with torch.cuda.graph(graph):
+        q.qgemv_kv_append(x, x, b.seqs, b.cache, 0, rope=r)
+
+    def fresh():
+        b.cache.k.copy_(b.k)
+        b.cache.v.copy_(b.v)
+
+    for lens in ([40, 9], [33, 1], [48, 16], [2, 5]):
+        fresh()
+        x.copy_(torch.randn(3, 2, 64, generator=g))
+        b.seqs.lens.copy_(ints(lens, dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = b.cache.k.clone(), b.cache.v.clone()
+        fresh()
+        q.qgemv_kv_append(x, x, b.seqs, b.cache, 0, rope=r)
+        for a, c in zip(got, (b.cache.k, b.cache.v)):
+            assert torch.equal(a.nan_to_num(), c.nan_to_num())
+        p = lens[1] - 1
+        assert torch.equal(b.cache.v[0, int(b.tables[1, p // 16]), :, p % 16], x[2].half())
+
+
+def test_nothing_to_do(dev):
+    """No tokens, no sequences, no pages: outputs stay as they were."""
+    b = Batch(dev, [10], [2], 2, 64, "f16")
+    x = torch.randn(3, 4, 64, device=dev)
+    out = torch.full_like(x, 7.0)
+    none = q.KvSeqs(ints([0], dev), ints([], dev), torch.zeros(0, 3, dtype=torch.int32, device=dev))
+    q.qgemv_kv_attend(x, none, b.cache, 0, out, scale=1.0)
+    q.qgemv_kv_append(x[:, :2], x[:, :2], none, b.cache, 0)
+    q.qgemv_kv_attend(x[:0], b.seqs, b.cache, 0, out[:0], scale=1.0, work=torch.empty(1 << 20, dtype=torch.uint8, device=dev))
+    q.qgemv_rope(x[:0], ints([], dev), rope_of(64, dev), out[:0])
+    q.qgemv_kv_copy(b.cache, ints([], dev), ints([], dev))
+    assert (out == 7.0).all() and torch.equal(b.cache.k.nan_to_num().cpu(), b.k.nan_to_num())
+    # a table without columns: rows that see nothing
+    bare = q.KvSeqs(b.seqs.starts, b.seqs.lens, torch.zeros(1, 0, dtype=torch.int32, device=dev))
+    q.qgemv_kv_append(x[:, :2], x[:, :2], bare, b.cache, 0)
+    q.qgemv_kv_attend(x, bare, b.cache, 0, out, scale=1.0)
+    assert (out[:2] == 0).all() and (out[2:] == 7.0).all()
+    assert torch.equal(b.cache.k.nan_to_num().cpu(), b.k.nan_to_num())
+
+
+def test_attend_keys_about_a_page_end(dev):
+    """Parts of the keys that end in a page's last slots, on the cache's last page, few rows and many."""
+    for size in (16, 32, 64):
+        for n in (size - 1, size, 2 * size - 1, 4 * size - 3, 8 * size - 1):
+            for new in (1, min(n, 40)):
+                b = Batch(dev, [n], [new], 1, 64, "bf16", size, layers=1, seed=n, spare=0)
+                # the pages in order, so that the last one holds the last key
+                b.tables = torch.where(b.tables >= 0, torch.arange(b.tables.shape[1], dtype=torch.int32)[None], -1)
+                for t in (b.k, b.v):
+                    t.copy_(torch.randn(t.shape, generator=gen(n)).to(t.dtype))
+                b.reload()
+                check_attend(b, queries(b, 2, 64, "bf16"), "bf16", layer=0)

@@ -14,9 +14,9 @@ namespace {
 // Rotary positions.  A pair (a, b) at position p with frequency f becomes
 //     (a cos t - b sin t, b cos t + a sin t) mscale,   t = p f,
 // and the gradient's turn is that by -t.  Bound by memory: every value is read
-// and written once.  A workgroup computes the sines of its few tokens once,
-// into LDS, and then walks over all their heads: computed by each lane for
-// itself they would cost more than the loads.  t is reduced in 64 bits to a
+// and written once (8191 tokens, 64 heads of 128, bf16: 51 us, 5.2 TB/s; a large
+// copy does 5.0).  A workgroup computes the sines of its few tokens once,
+// into LDS, and then walks over all their heads.  t is reduced in 64 bits to a
 // quarter turn (p f passes 10^6 radians in a long context, where fp32 has
 // lost the angle), sine and cosine of the rest are fp32.
 // ---------------------------------------------------------------------------
@@ -153,7 +153,8 @@ template <int X, int V> __global__ void __launch_bounds__(256) rope_kernel(RopeA
 // ---------------------------------------------------------------------------
 // New tokens into the cache.  As above, over the heads of q (turned into
 // q_out), k (turned into its slot) and v (copied to its slot); a workgroup
-// first finds its tokens' sequences and slots.
+// first finds its tokens' sequences and slots.  (7 ragged prompts up to 2048
+// tokens, 64 heads over 8 of 128, bf16: 65 us, 5.6 TB/s.)
 // ---------------------------------------------------------------------------
 
 struct AppendArgs {
@@ -245,7 +246,9 @@ int pairs_of(int half) { return half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : 1; }
 
 // How many tokens, or heads of one token, a workgroup takes.
 void share(int64_t n_tok, int n_head, int units, int half, int &toks, int &heads, dim3 &grid) {
-  constexpr int64_t kGroups = 1024;  // four workgroups a compute unit
+  // sixteen workgroups a compute unit (8191 tokens of 64 heads of 128: 51 us, with four 62;
+  // with a token each 55, and 32000 tokens of one head of 64 24 instead of 7.5)
+  constexpr int64_t kGroups = 4096;
   int64_t t = std::max<int64_t>(1, n_tok / kGroups);
   t = std::min<int64_t>(t, kToks);
   if (half > 0) t = std::max<int64_t>(1, std::min<int64_t>(t, kAngles / half));

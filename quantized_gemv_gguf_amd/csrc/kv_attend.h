@@ -50,7 +50,7 @@ constexpr float kInf = __builtin_huge_valf();
 // tile of rows and part of the keys itself: pieces of kPiece keys are counted
 // over all tiles, and a sequence's tiles are cut into parts of so many pieces
 // that about `target` parts come out in all.  A wave does this for itself, its
-// lanes over the sequences: no barrier (64 sequences: 0.6 us).
+// lanes over the sequences: no barrier.
 // ---------------------------------------------------------------------------
 
 constexpr int kFewRows = 16, kFewPiece = 128;
@@ -82,7 +82,7 @@ template <int ROWS, int PIECE> struct Plan {
   // The item of this number among parts (BY_TILE: among tiles).
   template <bool BY_TILE> __device__ Item find(int number) const {
     const int lane = threadIdx.x & 63, n_seq = a.seqs.n_seq;
-    if (n_seq == 1) {  // (the same without a scan: 1.2 us less of a launch's start)
+    if (n_seq == 1) {  // (the same without a scan: 1.1 us less of a launch's start)
       int tiles, pieces;
       size_of(0, tiles, pieces);
       const int parts = a.target > 0 ? (pieces - 1) / pieces_each((int64_t)tiles * pieces) + 1 : 1;
@@ -297,13 +297,14 @@ template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("s
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
-// Few rows: tiles of 16.  Bound by memory: each wave walks every kFewWaves-th 32
+// Few rows: tiles of 16.  Bound by memory: each wave walks every kWaves-th 32
 // keys through a ring of its own in LDS, filled by asynchronous copies some
-// tiles ahead (no barrier, no registers for what is under way; lanes that are
-// next to each other copy what lies next to each other, which loads in the
-// layout of the matrix instructions would not: 64 requests an instruction
-// instead of 16, 160 us for the 64 sequences below).  16 x 16 x 32 instructions;
-// K^T comes by 16-byte reads, V^T by the transposing 8-byte ones.
+// tiles ahead: no barrier, no registers for what is under way, and lanes next to
+// each other copy what lies next to each other.  (Loaded in the layout of the
+// matrix instructions, 64 requests an instruction, the next tile in registers:
+// 64 sequences up to 8192, 64 heads over 8 of 64, 148 us; so, 114, 5.2 TB/s.
+// 131009 positions of 64 heads of 96, fp32 rows: 535, 6.0.)  16 x 16 x 32
+// instructions; K^T comes by 16-byte reads, V^T by the transposing 8-byte ones.
 // A row of 2 D bytes begins at the same bank as another one, so its 16-byte
 // pieces lie at places exchanged by the key's low bits, differently for K and V:
 // as the reads that go together fall on different banks.
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
   const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
   const auto page_of = [&](int key) { return table[min(key, last_key) >> a.seqs.page_shift]; };
   // (the same for a uniform key, through the scalar cache: waiting for a vector
-  // load would wait for the copies too)
+  // load would wait for the copies too, 145 us instead of 117 in the case above)
   const auto page_at = [&](int key) {
     typedef const __attribute__((address_space(4))) int32_t *Constant;
     return ((Constant)table)[min(key, last_key) >> a.seqs.page_shift];
@@ -618,12 +619,20 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
 // columns; K^T comes by 16-byte reads, V^T by the transposing 8-byte ones, whose
 // four keys a lane are those of the scores' layout.
 // Places of a row's pieces are exchanged as above.
+// 8192 tokens, 32 heads over 8 of 128: 543 us, 1.01 PFLOP/s; its matrix
+// instructions alone, without copies, reads of LDS and softmax, take 372.  The
+// next scores computed beside a softmax (keys a tile further ahead), reads of
+// LDS ordered ahead of the products, raised priorities: no gain.  A copy's
+// addresses from one of its page, by the scalar unit, instead of one a lane:
+// 704 to 608; the rows that see the most first: 608 to 565; 16 places exchanged
+// for K, not 8: to 550.
 // The running maximum follows only when a row's grows by more than 8 (in powers
 // of 2): until then weights up to 256 are as exact, and the sums need no factor.
 // ---------------------------------------------------------------------------
 
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves, kManyPiece = 64;
 constexpr float kSlack = 8.0f;
+
 template <int D> struct ManyTile {
   static constexpr int KT = D <= 128 ? 64 : 32;  // keys
   static constexpr int CH = D / 8;               // pieces of a row

@@ -102,7 +102,7 @@ typedef struct qg_kv_seqs {
   const int32_t *tables; /* n_seq x max_pages */
   int32_t n_seq;         /* 0 .. QG_MAX_SEQS */
   int32_t reserved;      /* must be 0 */
-  int64_t max_pages;     /* 0 .. 2^31 - 2^16, max_pages * page_size below 2^31 */
+  int64_t max_pages;     /* 0 .., max_pages * page_size at most 2^31 - 2^16 */
 } qg_kv_seqs;
 
 /* Who holds which page; device memory that the calls below keep up to date.
@@ -118,7 +118,8 @@ typedef struct qg_kv_pool {
   int32_t *used;   /* (n_pages + 31) / 32 */
   int32_t n_seq;   /* 1 .. QG_MAX_SEQS */
   int32_t page_size;
-  int64_t max_pages; /* 1 .., max_pages * page_size below 2^31 */
+  int64_t max_pages; /* 1 .., max_pages * page_size at most 2^31 - 2^16,
+                        n_seq * max_pages below 2^31 */
   int64_t n_pages;   /* 1 .. QG_MAX_POOL_PAGES */
   void *work;        /* device, 16-byte aligned; holds nothing between calls */
   int64_t work_bytes;
@@ -181,7 +182,7 @@ int qgemv_kv_append(const qg_heads *k, const qg_heads *v, const qg_kv_seqs *seqs
  * A weight too small for its type next to the row's largest adds nothing.
  * out is rounded once.  The order of sums may differ for another number of rows
  * or sequences and other lengths of the others.
- * scale > 0 and finite; window >= 0; out has q's sizes; q heads a multiple of
+ * scale > 0, up to 2^127; window >= 0; out has q's sizes; q heads a multiple of
  * the cache's heads, n_tok * q heads at most 2^31 - 2^16.  work: device, 16-byte aligned, at least
  * qgemv_kv_attend_bytes, holds nothing between calls; calls that may run at
  * once need one each (QG_E_SIZE where it is too small). */

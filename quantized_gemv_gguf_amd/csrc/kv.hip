@@ -195,14 +195,14 @@ template <int X, int V> __global__ void __launch_bounds__(256) append_kernel(App
   for (int i = threadIdx.x >> 6; i < toks; i += 4) {
     const int t = t0 + i, s = seq_of(a.seqs, t);
     int64_t to = -1;
-    int p = 0;
+    int64_t p = 0;
     bool in = false;
     if (s >= 0) {
       int start, n, len;
       seq_rows(a.seqs, s, a.n_tok, start, n, len);
       in = t - start < n;
-      p = a.seqs.lens[s] - n + (t - start);
-      if (in && p >= 0 && p < (a.seqs.max_pages << a.seqs.page_shift)) {
+      p = (int64_t)len - n + (t - start);
+      if (in && p >= 0 && p < room_of(a.seqs)) {
         const int64_t page = a.seqs.tables[s * a.seqs.max_pages + (p >> a.seqs.page_shift)];
         if (page >= 0 && page < a.n_pages)
           to = page * a.page_stride + (p & ((1 << a.seqs.page_shift) - 1)) * a.slot_stride;
@@ -210,7 +210,7 @@ template <int X, int V> __global__ void __launch_bounds__(256) append_kernel(App
     }
     if ((threadIdx.x & 63) == 0) {
       slot[i] = to;
-      at[i] = a.pos ? a.pos[t] : p;
+      at[i] = a.pos ? a.pos[t] : (int)p;
       any[i] = in;
     }
   }
@@ -361,7 +361,7 @@ int check_cache(const qg_kv_cache *c) {
 int check_seqs(const qg_kv_seqs *q, const qg_kv_cache *c) {
   if (!q) return QG_E_NULL;
   if (q->n_seq < 0 || q->n_seq > QG_MAX_SEQS || q->max_pages < 0 || q->max_pages > kMaxCount ||
-      q->max_pages * c->page_size > 0x7fffffff)
+      q->max_pages * c->page_size > kMaxCount)
     return QG_E_SHAPE;
   if (q->reserved != 0) return QG_E_ARG;
   if (q->n_seq > 0 && (!q->starts || !q->lens || (q->max_pages > 0 && !q->tables))) return QG_E_NULL;

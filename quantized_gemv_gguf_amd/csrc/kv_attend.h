@@ -55,6 +55,15 @@ constexpr float kInf = __builtin_huge_valf();
 
 constexpr int kFewRows = 16, kFewPiece = 128;
 
+// The first position that one at pos sees, and the end of those that it sees,
+// of a sequence of this length, within its table.
+__device__ __forceinline__ int first_seen(const AttendArgs &a, int pos) {
+  return a.window ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
+}
+__device__ __forceinline__ int end_seen(const AttendArgs &a, int pos, int len) {
+  return min(a.causal ? pos + 1 : len, room_of(a.seqs));
+}
+
 struct Item {
   int s, tile, part, parts;  // parts: of this tile; 0: nothing to do
   int first;                 // the tile's first part among all parts
@@ -70,8 +79,8 @@ template <int ROWS, int PIECE> struct Plan {
     int start, n, len;
     seq_rows(a.seqs, s, a.n_tok, start, n, len);
     tiles = (int)(((int64_t)n * a.group + ROWS - 1) / ROWS);
-    const int lo = a.window ? max(len - n - a.window + 1, 0) : 0;
-    pieces = max(1, (len - min(lo, len) + PIECE - 1) / PIECE);
+    const int hi = end_seen(a, len - 1, len), lo = min(first_seen(a, len - n), hi);
+    pieces = max(1, (int)(((int64_t)hi - lo + PIECE - 1) / PIECE));
   }
   // Pieces of a part.  One of many rows costs its sums' way through memory, as
   // much as some pieces' products: it gets eight at least (100 new tokens of each
@@ -156,10 +165,10 @@ template <int ROWS> __device__ __forceinline__ Range range_of(const AttendArgs &
   const int last = (min(it.n * a.group, (it.tile + 1) * ROWS) - 1) / a.group;
   const int old = it.len - it.n;  // (may be below 0: then the first rows see nothing)
   Range r;
-  r.lo = a.window ? max(old + first - a.window + 1, 0) : 0;
-  r.hi = a.causal ? max(old + last + 1, 0) : it.len;
-  r.all_lo = a.window ? max(old + last - a.window + 1, 0) : 0;
-  r.all_hi = a.causal ? old + first + 1 : it.len;
+  r.hi = max(end_seen(a, old + last, it.len), 0);
+  r.lo = min(first_seen(a, old + first), r.hi);
+  r.all_lo = first_seen(a, old + last);
+  r.all_hi = end_seen(a, old + first, it.len);
   return r;
 }
 
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
   if (it.parts == 0) return;
   const Range range = range_of<kFewRows>(a, it);
   // this part's keys: whole pieces from a multiple of 32 on
-  const int lo = range.lo & ~31, pieces = max(0, (range.hi - lo + kFewPiece - 1) / kFewPiece);
+  const int lo = range.lo & ~31, pieces = max(0, (int)(((int64_t)range.hi - lo + kFewPiece - 1) / kFewPiece));
   const int share = (pieces + it.parts - 1) / it.parts;
   const int begin = lo + min(pieces, it.part * share) * kFewPiece;
   const int end = min(range.hi, lo + min(pieces, (it.part + 1) * share) * kFewPiece);
@@ -420,8 +429,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
   const int row = it.tile * kFewRows + c, tok = row / a.group, q_head = head * a.group + row % a.group;
   const bool real = row < it.n * a.group;
   const int pos = it.len - it.n + tok;
-  const int see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
-  const int see_hi = real ? (a.causal ? pos + 1 : it.len) : 0;
+  const int see_lo = first_seen(a, pos), see_hi = real ? end_seen(a, pos, it.len) : 0;
   V8 q[ST][NT];
   float scale = a.scale;
   {
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   const Item it = Plan<kManyRows, kManyPiece>(a).template find<false>(number);
   if (it.parts == 0) return;
   const Range range = range_of<kManyRows>(a, it);
-  const int lo = range.lo & ~31, pieces = max(0, (range.hi - lo + kManyPiece - 1) / kManyPiece);
+  const int lo = range.lo & ~31, pieces = max(0, (int)(((int64_t)range.hi - lo + kManyPiece - 1) / kManyPiece));
   const int share = (pieces + it.parts - 1) / it.parts;
   const int begin = lo + min(pieces, it.part * share) * kManyPiece;
   const int end = min(range.hi, lo + min(pieces, (it.part + 1) * share) * kManyPiece);
@@ -685,13 +693,11 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   const int row = row0 + c, tok = row / a.group, q_head = head * a.group + row % a.group;
   const bool real = row < rows;
   const int old = it.len - it.n, pos = old + tok;
-  const int see_lo = a.window ? max(pos - a.window + 1, 0) : 0;
-  const int see_hi = real ? (a.causal ? pos + 1 : it.len) : 0;
+  const int see_lo = first_seen(a, pos), see_hi = real ? end_seen(a, pos, it.len) : 0;
   const int first_tok = row0 / a.group, last_tok = (min(row0 + 32, rows) - 1) / a.group;
-  const int wave_lo = a.window ? max(old + first_tok - a.window + 1, 0) : 0;
-  const int wave_hi = row0 < rows ? (a.causal ? old + last_tok + 1 : it.len) : 0;
-  const int whole_lo = a.window ? max(old + last_tok - a.window + 1, 0) : 0;
-  const int whole_hi = a.causal ? old + first_tok + 1 : it.len;
+  const int wave_lo = first_seen(a, old + first_tok);
+  const int wave_hi = row0 < rows ? end_seen(a, old + last_tok, it.len) : 0;
+  const int whole_lo = first_seen(a, old + last_tok), whole_hi = end_seen(a, old + first_tok, it.len);
   const uint8_t *ck = (const uint8_t *)(a.k + head * a.head_stride), *cv = (const uint8_t *)(a.v + head * a.head_stride);
   const int32_t *table = a.seqs.tables + it.s * a.seqs.max_pages;
   const int last_key = max(end - 1, 0);

@@ -40,7 +40,7 @@ AttendShape shape_of(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cach
 }
 
 int64_t part_rows_of(const AttendShape &s, const qg_kv_cache *cache) {
-  return s.target > 0 ? s.parts * cache->n_head * s.rows : 0;
+  return s.target > 0 && s.tiles > 0 ? s.parts * cache->n_head * s.rows : 0;
 }
 
 int check_attend(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache, bool sizes_only) {
@@ -77,7 +77,7 @@ int qgemv_kv_attend(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache
   if ((rc = check_attend(q, seqs, cache, false)) || (rc = check_heads(out, true, QG_MAX_HEAD_DIM))) return rc;
   if (out->n_tok != q->n_tok || out->n_head != q->n_head || out->head_dim != q->head_dim) return QG_E_SHAPE;
   if (layer < 0 || layer >= cache->n_layer) return QG_E_RANGE;
-  if (!std::isfinite(scale) || scale <= 0.0f || window < 0) return QG_E_ARG;
+  if (!std::isfinite(scale * kLog2e) || scale <= 0.0f || window < 0) return QG_E_ARG;
   const AttendShape s = shape_of(q, seqs, cache);
   const int64_t part_rows = part_rows_of(s, cache), bytes = part_rows * (cache->head_dim + 2) * 4;
   if (work_bytes < bytes) return QG_E_SIZE;

@@ -72,14 +72,16 @@ struct Seqs {
 };
 
 // The row range of sequence s, kept within the activations' rows whatever the
-// arrays hold, and its length, kept within its table.
+// arrays hold, and its length (which its table need not hold).
 __device__ __forceinline__ void seq_rows(const Seqs &q, int s, int n_tok, int &start, int &n, int &len) {
   start = min(max(q.starts[s], 0), n_tok);
   n = min(max(q.starts[s + 1], start), n_tok) - start;
-  len = (int)min((int64_t)max(q.lens[s], 0), q.max_pages << q.page_shift);
+  len = max(q.lens[s], 0);
 }
+// Positions that a table holds.
+__device__ __forceinline__ int room_of(const Seqs &q) { return (int)(q.max_pages << q.page_shift); }
 
-constexpr int64_t kMaxCount = 0x7fff0000;  // tokens, pages: an index a little past the end stays an int
+constexpr int64_t kMaxCount = 0x7fff0000;  // tokens, pages, positions: an index a little past the end stays an int
 
 // A grid of at most 2^31 - 1 threads in x.
 constexpr int64_t kMaxGrid = 1 << 23;

@@ -465,7 +465,7 @@ int check_pool(const qg_kv_pool *p) {
   int rc = check_sizes(p->n_seq, p->max_pages, p->n_pages);
   if (rc) return rc;
   if (p->page_size < 1 || p->page_size > 65536 || (p->page_size & (p->page_size - 1)) ||
-      p->max_pages * p->page_size > 0x7fffffff)
+      p->max_pages * p->page_size > kMaxCount)
     return QG_E_SHAPE;
   if (!p->tables || !p->lens || !p->refs || !p->used || !p->work) return QG_E_NULL;
   if ((uintptr_t)p->work & 15) return QG_E_ARG;

@@ -60,13 +60,14 @@ def attended(q, starts, lens, tables, k, v, layer, scale, causal=True, window=0,
     mine = torch.zeros(rows, dtype=torch.bool)
     for s in range(len(lens)):
         lo, hi = int(starts[s]), int(starts[s + 1])
-        n, length = hi - lo, min(int(lens[s]), tables.shape[1] * size)
+        n, length = hi - lo, int(lens[s])
+        held = min(length, tables.shape[1] * size)
         if n <= 0:
             continue
         mine[lo:hi] = True
-        ks, there = gathered(k, layer, tables[s], length, size)
-        vs, _ = gathered(v, layer, tables[s], length, size)
-        j = torch.arange(length)
+        ks, there = gathered(k, layer, tables[s], held, size)
+        vs, _ = gathered(v, layer, tables[s], held, size)
+        j = torch.arange(held)
         for i in range(n):
             p = length - n + i
             seen = there.clone()

@@ -256,6 +256,30 @@ def test_attend_layouts(dev, order, new):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new", [1, 9, 60])
+def test_attend_lengths_past_the_table(dev, new, causal):
+    """Positions that the table does not hold are masked, and do not move the others; the widest window hides nothing,
+    nor does it where rows lie before the sequence's start."""
+    b = Batch(dev, [150, 40, 48], [new, new, new], 2, 64, "bf16", 16, seed=9, room=0)
+    b.tables = b.tables[:, :5].contiguous()  # 80 positions
+    b.lens[1] = 2 ** 31 - 1 if causal else 79
+    b.reload()
+    x = queries(b, 4, 64, "bf16")
+    for window in (0, 2 ** 31 - 1, 100):
+        if b.lens[1] > 1000:  # (the plain form's last sequence would see its whole window past the table)
+            ref = [min(n, 10 ** 6) for n in b.lens]
+        else:
+            ref = b.lens
+        r = kvref.attended(x, b.starts, ref, b.tables, b.k, b.v, 1, 0.3, causal=causal, window=window)
+        out, lse = attend(b, x, "bf16", scale=0.3, causal=causal, window=window)
+        tol, tol_lse = kvref.bounds(r, 64, torch.bfloat16, torch.bfloat16, False)
+        within(out, r["out"], tol, "out")
+        within(lse, r["lse"], tol_lse, "lse")
+    c = Batch(dev, [10, 3], [40, 3], 1, 64, "f16", 16, seed=9)
+    check_attend(c, queries(c, 2, 64, "f16"), "f16", window=2 ** 31 - 1)
+
+
 @pytest.mark.parametrize("new", [1, 40])
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_attend_pages_that_are_not_there(dev, kind, new):

@@ -157,7 +157,7 @@ def test_any_order_of_the_axes():
 
 
 @pytest.mark.parametrize("s,rc", [(None, E_NULL), (seqs(n=-1), E_SHAPE), (seqs(n=4097), E_SHAPE),
-                                  (seqs(pages=-1), E_SHAPE), (seqs(pages=1 << 27), E_SHAPE), (seqs(reserved=1), E_ARG),
+                                  (seqs(pages=-1), E_SHAPE), (seqs(pages=1 << 27), E_SHAPE), (seqs(pages=(1 << 27) - 1), E_SHAPE), (seqs(reserved=1), E_ARG),
                                   (seqs(starts=None), E_NULL), (seqs(lens=None), E_NULL), (seqs(tables=None), E_NULL)])
 def test_sequences_are_refused(s, rc):
     L = q.lib()
@@ -193,7 +193,7 @@ def test_attend_refusals():
     assert call(layer=-1) == E_RANGE and call(layer=2) == E_RANGE
     assert call(x=heads(h=3), y=heads(h=3)) == E_SHAPE and call(x=heads(d=96), y=heads(d=96)) == E_SHAPE
     assert call(y=heads(n=5)) == E_SHAPE and call(y=heads(h=4)) == E_SHAPE and call(y=heads(d=32)) == E_SHAPE
-    for scale in (0.0, -1.0, INF, NAN):
+    for scale in (0.0, -1.0, INF, NAN, 3e38):
         assert call(scale=scale) == E_ARG
     assert call(window=-1) == E_ARG
     need = L.qgemv_kv_attend_bytes(heads(), seqs(pages=64), cache())

@@ -74,7 +74,8 @@ typedef struct qg_rope {
  * at layer * layer_stride + page * page_stride + head * head_stride + slot *
  * slot_stride + i, of k and of v alike.  Both 16-byte aligned, strides
  * multiples of 8 elements, positive, and such that no two elements meet
- * (QG_E_ARG): any order of the axes. */
+ * (QG_E_ARG): any order of the axes.  A page's keys in a layer are at most 2^33
+ * elements. */
 typedef struct qg_kv_cache {
   void *k;
   void *v;

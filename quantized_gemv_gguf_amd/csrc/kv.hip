@@ -337,6 +337,7 @@ int check_cache(const qg_kv_cache *c) {
       c->n_layer > 65536 || c->n_head < 1 || c->n_head > QG_MAX_HEADS || c->head_dim < 32 || c->head_dim % 32 != 0 ||
       c->head_dim > QG_MAX_HEAD_DIM || c->n_pages < 1 || c->n_pages > kMaxCount)
     return QG_E_SHAPE;
+  if ((int64_t)c->n_head * c->page_size * c->head_dim > 1ll << 33) return QG_E_SHAPE;  // copies count its pieces in 32 bits
   if (c->reserved != 0) return QG_E_ARG;
   // from the innermost axis out, each must step past all that is within it
   struct Axis {

@@ -147,6 +147,13 @@ def test_caches_are_refused(i):
     assert L.qgemv_kv_compact(pool(), c, None) == rc
 
 
+def test_pages_past_32_bits_of_pieces_are_refused():
+    L = q.lib()
+    for h, size, d, rc in ((1024, 32768, 256, 0), (1024, 65536, 256, E_SHAPE), (1023, 65536, 160, E_SHAPE),
+                           (512, 65536, 256, 0)):
+        assert L.qgemv_kv_copy(cache(h=h, size=size, d=d), FAKE, FAKE, 0, None) == rc
+
+
 def test_any_order_of_the_axes():
     L = q.lib()
     for strides in [(16384, 2048, 1024, 64), (16384, 2048, 64, 128), (2048, 4096, 1024, 64), (64, 4096, 2048, 128),

@@ -1,8 +1,8 @@
 // kv_attend.h -- attention of new tokens over a paged cache.
 //
-// A row (t, h) of q with the keys it sees, m = max_j s_j, gives
+// A row (t, h) of q with the keys it sees, any m near max_j s_j, gives
 //     o = sum_j e^(s_j - m) v_j / l,   l = sum_j e^(s_j - m) + e^(sink - m).
-// Keys are walked once, in pieces: of a piece's maximum m', sum l' and products
+// Keys are walked once, in pieces: of a piece's m', sum l' and products
 // o' (all fp32) the running ones become m'' = max(m, m'), l'' = l e^(m - m'') +
 // l' e^(m' - m''), and o'' likewise; so do those of parts of the keys that
 // different workgroups have walked.
@@ -181,6 +181,10 @@ template <> struct Kind<QG_F16> {
   typedef _Float16 H;
   typedef _Float16 V8 __attribute__((ext_vector_type(8)));
   static constexpr int kWide = 2;            // terms that hold an fp32 (22 bits and the sign of the second)
+  // log2 of a row's largest weight: of 16 binades above 1 and 24 below, weights
+  // of at most 1 would use the lower ones alone, and small ones would lose bits
+  // that their sum l counts.  So they are lost below 2^-40 of the largest.
+  static constexpr float kTop = 15.0f;
   static constexpr uint32_t kExp = 0x7c00u;  // the exponent of infinities and NaN
   static constexpr uint32_t kOne = 0x3c00u;
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
@@ -194,6 +198,7 @@ template <> struct Kind<QG_BF16> {
   typedef __bf16 H;
   typedef __bf16 V8 __attribute__((ext_vector_type(8)));
   static constexpr int kWide = 3;
+  static constexpr float kTop = 0.0f;
   static constexpr uint32_t kExp = 0x7f80u;
   static constexpr uint32_t kOne = 0x3f80u;
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
     float top = p[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) top = fmaxf(top, p[j]);
-    top = fmaxf(m, max_of_row16(top) * scale);
+    top = fmaxf(m, max_of_row16(top) * scale - K::kTop);
     if (__any(top > m)) {
       const float f = top > m ? exp2_of(m - top) : 1.0f;  // (of m = -inf, 0)
       l *= f;
@@ -635,7 +640,8 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
 // 704 to 608; the rows that see the most first: 608 to 565; 16 places exchanged
 // for K, not 8: to 550.
 // The running maximum follows only when a row's grows by more than 8 (in powers
-// of 2): until then weights up to 256 are as exact, and the sums need no factor.
+// of 2): until then weights up to 256 times as large are as exact, and the sums
+// need no factor.  (So those of fp16 are lost below 2^-32 of the largest.)
 // ---------------------------------------------------------------------------
 
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves, kManyPiece = 64;
@@ -673,6 +679,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   using V8 = typename K::V8;
   using M = ManyTile<D>;
   constexpr int KT = M::KT, CH = M::CH, U = KT / 32, ST = D / 16, DT = D / 32;
+  constexpr float kAbove = T == QG_F16 ? K::kTop - kSlack : 0.0f;  // log2 of the running maximum's own weight
   // a wave copies a quarter of a tile's keys
   constexpr int kKeys = KT / kManyWaves, kCopies = (kKeys * CH + 63) / 64;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][M::kBytes];  // of a tile: K, V
@@ -855,7 +862,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-    top = max_of_row32(top) * scale;
+    top = max_of_row32(top) * scale - kAbove;
     if (__any(top > m + kSlack)) {
       const float f = top > m ? exp2_of(m - top) : 1.0f;  // (of m = -inf, 0)
       l *= f;

@@ -185,6 +185,9 @@ template <> struct Kind<QG_F16> {
   // of at most 1 would use the lower ones alone, and small ones would lose bits
   // that their sum l counts.  So they are lost below 2^-40 of the largest.
   static constexpr float kTop = 15.0f;
+  // and of a q row's that is taken in terms: its values down to 2^-15 of the
+  // largest have 22 bits, smaller ones are held to 2^-39 of it
+  static constexpr int kRowTop = 14;
   static constexpr uint32_t kExp = 0x7c00u;  // the exponent of infinities and NaN
   static constexpr uint32_t kOne = 0x3c00u;
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
@@ -199,6 +202,7 @@ template <> struct Kind<QG_BF16> {
   typedef __bf16 V8 __attribute__((ext_vector_type(8)));
   static constexpr int kWide = 3;
   static constexpr float kTop = 0.0f;
+  static constexpr int kRowTop = 0;
   static constexpr uint32_t kExp = 0x7f80u;
   static constexpr uint32_t kOne = 0x3f80u;
   static __device__ __forceinline__ f32x4 mfma16(V8 a, V8 b, f32x4 c) {
@@ -222,8 +226,8 @@ template <int T, int NT> __device__ __forceinline__ void terms_of(const float (&
   }
 }
 
-// 2^e with the exponent of the largest of a row's values (0 for a row of zeros,
-// infinities and NaN): an fp32 row divided by it has terms in fp16.
+// The exponent of the largest of a row's values (0 for a row of zeros, infinities
+// and NaN): an fp32 row divided by its power of 2 has terms in fp16.
 __device__ __forceinline__ int row_exponent(float most) {
   const int e = (int)((__float_as_uint(most) >> 23) & 255);
   return e == 0 || e == 255 ? 0 : e - 127;
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
       for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[t][i]));
     }
     if (T == QG_F16 && NT > 1) {
-      const int e = row_exponent(max_of_row16(most));
+      const int e = row_exponent(max_of_row16(most)) - K::kRowTop;
       scale = ldexpf(scale, e);
 #pragma unroll
       for (int t = 0; t < ST; ++t)
@@ -791,7 +795,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
       for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[t][i]));
     }
     if (T == QG_F16 && NT > 1) {
-      const int e = row_exponent(max_of_row32(most));
+      const int e = row_exponent(max_of_row32(most)) - K::kRowTop;
       scale = ldexpf(scale, e);
 #pragma unroll
       for (int t = 0; t < ST; ++t)

@@ -229,8 +229,21 @@ template <int T, int NT> __device__ __forceinline__ void terms_of(const float (&
 // The exponent of the largest of a row's values (0 for a row of zeros, infinities
 // and NaN): an fp32 row divided by its power of 2 has terms in fp16.
 __device__ __forceinline__ int row_exponent(float most) {
-  const int e = (int)((__float_as_uint(most) >> 23) & 255);
-  return e == 0 || e == 255 ? 0 : e - 127;
+  const uint32_t bits = __float_as_uint(most) & 0x7fffffff;
+  const int e = (int)(bits >> 23);
+  return bits == 0 || e == 255 ? 0 : e > 0 ? e - 127 : -118 - __builtin_clz(bits);
+}
+
+// The scale of such a row is scale * 2^e; where that would pass fp32, the scores
+// need not: they are multiplied by 2^more first.
+struct RowScale {
+  float scale;
+  int more;
+};
+__device__ __forceinline__ RowScale row_scale(float scale, int e) {
+  const int at = (int)(__float_as_uint(scale) >> 23) - 127;
+  const int more = max(at + e - 126, 0);
+  return {ldexpf(scale, e - more), more};
 }
 
 // Lanes that are 16 and 32 apart hold the same q row: the largest, the sum.
@@ -441,6 +454,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
   const int see_lo = first_seen(a, pos), see_hi = real ? end_seen(a, pos, it.len) : 0;
   V8 q[ST][NT];
   float scale = a.scale;
+  int more = 0;
   {
     float x[ST][8];
     float most = 0.0f;
@@ -455,7 +469,9 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
     }
     if (T == QG_F16 && NT > 1) {
       const int e = row_exponent(max_of_row16(most)) - K::kRowTop;
-      scale = ldexpf(scale, e);
+      const RowScale by = row_scale(scale, e);
+      scale = by.scale;
+      more = by.more;
 #pragma unroll
       for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -465,6 +481,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
     for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
   }
 
+  const bool scaled_twice = T == QG_F16 && NT > 1 && __any(more > 0);
   f32x4 o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = f32x4{0, 0, 0, 0};
@@ -493,6 +510,10 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = s[j / 4][j & 3];
+    if (scaled_twice) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = ldexpf(p[j], more);
+    }
     const uint32_t there = there_of(base);
     if (!all_see(base, there)) {
       const uint32_t seen = seen_of(base, there);
@@ -782,6 +803,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 
   V8 q[ST][NT];
   float scale = a.scale;
+  int more = 0;
   {
     float x[ST][8];
     float most = 0.0f;
@@ -796,7 +818,9 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
     }
     if (T == QG_F16 && NT > 1) {
       const int e = row_exponent(max_of_row32(most)) - K::kRowTop;
-      scale = ldexpf(scale, e);
+      const RowScale by = row_scale(scale, e);
+      scale = by.scale;
+      more = by.more;
 #pragma unroll
       for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -805,6 +829,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 #pragma unroll
     for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
   }
+  const bool scaled_twice = T == QG_F16 && NT > 1 && __any(more > 0);
   int buf = 0;
   for (int base = begin; base < end; base += KT, buf ^= 1) {
     wait_copies<0>();
@@ -849,6 +874,12 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 #pragma unroll
         for (int k = 0; k < NT; ++k) s[u] = K::mfma32(key, q[t][k], s[u]);
       }
+    if (scaled_twice) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] = ldexpf(s[u][i], more);
+    }
     const bool whole = base >= whole_lo && base + KT <= whole_hi && (now & kAll) == kAll;
     if (!whole) {
 #pragma unroll

@@ -181,7 +181,7 @@ int qgemv_kv_append(const qg_heads *k, const qg_heads *v, const qg_kv_seqs *seqs
  * matrix cores take them), 2^-11 or 2^-8 of each; otherwise q and the weights are
  * taken in two terms of QG_F16, 2^-22 of each, or three of QG_BF16, 2^-24.  In
  * QG_F16 a row's weights are held to 2^-32 of its largest or less, its q values to
- * 2^-39, so one far below that adds nothing.
+ * 2^-39, in QG_BF16 both to 2^-133, so one far below that adds nothing.
  * out is rounded once.  The order of sums may differ for another number of rows
  * or sequences and other lengths of the others.
  * scale > 0, up to 2^127; window >= 0; out has q's sizes; q heads a multiple of

@@ -226,6 +226,23 @@ template <int T, int NT> __device__ __forceinline__ void terms_of(const float (&
   }
 }
 
+// The same of an fp32 row's values.  bf16's three terms hold all 24 bits (down to
+// 2^-133, where bf16 ends: looking for rows that lie below costs prompts with a
+// window 2%); the first is cut, not rounded, which would make the largest infinite.
+template <int T, int NT> __device__ __forceinline__ void row_terms_of(const float (&x)[8], typename Kind<T>::V8 (&t)[NT]) {
+  if (T == QG_BF16 && NT == 3) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float cut = __uint_as_float(__float_as_uint(x[i]) & 0xffff0000u), left = x[i] - cut;
+      t[0][i] = (typename Kind<T>::H)cut;
+      t[1][i] = (typename Kind<T>::H)left;
+      t[NT - 1][i] = (typename Kind<T>::H)(left - (float)t[1][i]);
+    }
+  } else {
+    terms_of<T, NT>(x, t);
+  }
+}
+
 // The exponent of the largest of a row's values (0 for a row of zeros, infinities
 // and NaN): an fp32 row divided by its power of 2 has terms in fp16.
 __device__ __forceinline__ int row_exponent(float most) {
@@ -478,7 +495,7 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
         for (int i = 0; i < 8; ++i) x[t][i] = ldexpf(x[t][i], -e);
     }
 #pragma unroll
-    for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
+    for (int t = 0; t < ST; ++t) row_terms_of<T, NT>(x[t], q[t]);
   }
 
   const bool scaled_twice = T == QG_F16 && NT > 1 && __any(more > 0);
@@ -827,7 +844,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
         for (int i = 0; i < 8; ++i) x[t][i] = ldexpf(x[t][i], -e);
     }
 #pragma unroll
-    for (int t = 0; t < ST; ++t) terms_of<T, NT>(x[t], q[t]);
+    for (int t = 0; t < ST; ++t) row_terms_of<T, NT>(x[t], q[t]);
   }
   const bool scaled_twice = T == QG_F16 && NT > 1 && __any(more > 0);
   int buf = 0;

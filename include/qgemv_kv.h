@@ -174,8 +174,11 @@ int qgemv_kv_append(const qg_heads *k, const qg_heads *v, const qg_kv_seqs *seqs
  * does not matter.  sinks (device, one fp32 per q head: a logit without a value)
  * and lse (device, n_tok x q heads, fp32: the log of the denominator, m's factor
  * put back) may be NULL.  A row that sees nothing, or whose scores are all -inf,
- * gets zeros, and lse the sink's logit or -inf.  Rows that belong to no sequence
- * are left as they were.
+ * gets zeros, whatever its values hold, and lse the sink's logit or -inf.  A row
+ * that sees a value without a size (infinite, NaN) has none there either: NaN, or
+ * the infinity where its weight is not 0 (one too small for its type may be).  An
+ * infinite q or key may make a score NaN, and so the row, where q is taken in terms.
+ * Rows that belong to no sequence are left as they were.
  * Scores, sums and the softmax are fp32.  Where q and out have the cache's type,
  * the weights exp(s_j - m) are rounded once to it before they meet v (as the
  * matrix cores take them), 2^-11 or 2^-8 of each; otherwise q and the weights are

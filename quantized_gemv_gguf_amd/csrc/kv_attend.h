@@ -302,17 +302,21 @@ __device__ __forceinline__ float of_kind(float count, int kind) {
   return count > 0.0f ? kind == kNan ? __builtin_nanf("") : kind == kUp ? kInf : -kInf : 0.0f;
 }
 
-// A finished row's factor, and the logarithm of its denominator (base e).
-__device__ __forceinline__ void finish_row(const AttendArgs &a, int head, float m, float l, float &f, float &lse) {
+// A finished row's factor (or that no key of its weighs anything: then its sums
+// may be NaN, of weights 0 and values without a size, and it is zeros), and the
+// logarithm of its denominator (base e).
+__device__ __forceinline__ void finish_row(const AttendArgs &a, int head, float m, float l, float &f, bool &none,
+                                           float &lse) {
+  none = l == 0.0f;
   if (a.sinks) {
     const float z = a.sinks[head] * kLog2e, top = fmaxf(m, z);
     const float w = top == -kInf ? 0.0f : exp2_of(z - top);
     const float keep = m == -kInf ? 0.0f : exp2_of(m - top);
     l = l * keep + w;
-    f = l == 0.0f ? 0.0f : keep / l;
+    f = keep / l;
     m = top;
   } else {
-    f = l == 0.0f ? 0.0f : 1.0f / l;
+    f = 1.0f / l;
   }
   lse = l == 0.0f ? -kInf : (m + log2f_of(l)) * kLn2;
 }
@@ -652,9 +656,10 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
       const int64_t t = it.start + out_row / a.group;
       const int h = head * a.group + out_row % a.group;
       float f, lse;
-      finish_row(a, h, top, total, f, lse);
+      bool none;
+      finish_row(a, h, top, total, f, none, lse);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] *= f;
+      for (int e = 0; e < E; ++e) v[e] = none ? 0.0f : v[e] * f;
       store_row(a.out, t, h, at, v);
       if (a.lse && (threadIdx.x & 15) == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
     } else {
@@ -992,12 +997,15 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   if (it.parts == 1) {
     const int64_t t = it.start + tok;
     float f, lse;
-    finish_row(a, q_head, m, l, f, lse);
+    bool none;
+    finish_row(a, q_head, m, l, f, none, lse);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float v[4] = {o[d][4 * i] * f, o[d][4 * i + 1] * f, o[d][4 * i + 2] * f, o[d][4 * i + 3] * f};
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = none ? 0.0f : o[d][4 * i + j] * f;
         store_row(a.out, t, q_head, 32 * d + 8 * i + 4 * h, v);
       }
     if (a.lse && h == 0) a.lse[t * a.group * a.kv_heads + q_head] = lse;
@@ -1076,8 +1084,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int rows
     const int64_t t = it.start + row / a.group;
     const int h = head * a.group + row % a.group;
     float f, lse;
-    finish_row(a, h, m, l, f, lse);
-    const float out[4] = {v[0] * f, v[1] * f, v[2] * f, v[3] * f};
+    bool none;
+    finish_row(a, h, m, l, f, none, lse);
+    float out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = none ? 0.0f : v[i] * f;
     store_row(a.out, t, h, at, out);
     if (a.lse && at == 0) a.lse[t * a.group * a.kv_heads + h] = lse;
   }

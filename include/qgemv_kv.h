@@ -182,9 +182,10 @@ int qgemv_kv_append(const qg_heads *k, const qg_heads *v, const qg_kv_seqs *seqs
  * Scores, sums and the softmax are fp32.  Where q and out have the cache's type,
  * the weights exp(s_j - m) are rounded once to it before they meet v (as the
  * matrix cores take them), 2^-11 or 2^-8 of each; otherwise q and the weights are
- * taken in two terms of QG_F16, 2^-22 of each, or three of QG_BF16, 2^-24.  In
- * QG_F16 a row's weights are held to 2^-32 of its largest or less, its q values to
- * 2^-39, in QG_BF16 both to 2^-133, so one far below that adds nothing.
+ * taken in two terms of QG_F16, 2^-22 of each, or three of QG_BF16, 2^-24.  What
+ * is far below the largest adds nothing: weights are held to 2^-32 of the row's
+ * largest at least in QG_F16, 2^-118 in QG_BF16, q's terms to 2^-39 of the row's
+ * largest value in QG_F16, in QG_BF16 to 2^-133.
  * out is rounded once.  The order of sums may differ for another number of rows
  * or sequences and other lengths of the others.
  * scale > 0, up to 2^127; window >= 0; out has q's sizes; q heads a multiple of

@@ -201,7 +201,7 @@ template <> struct Kind<QG_BF16> {
   typedef __bf16 H;
   typedef __bf16 V8 __attribute__((ext_vector_type(8)));
   static constexpr int kWide = 3;
-  static constexpr float kTop = 0.0f;
+  static constexpr float kTop = 0.0f;  // (bf16 has fp32's range, and values as large)
   static constexpr int kRowTop = 0;
   static constexpr uint32_t kExp = 0x7f80u;
   static constexpr uint32_t kOne = 0x3f80u;
@@ -688,7 +688,9 @@ __global__ void __launch_bounds__(64 * FewTile<D>::kWaves) attend_few_kernel(Att
 // for K, not 8: to 550.
 // The running maximum follows only when a row's grows by more than 8 (in powers
 // of 2): until then weights up to 256 times as large are as exact, and the sums
-// need no factor.  (So those of fp16 are lost below 2^-32 of the largest.)
+// need no factor.  (So those of fp16 are lost below 2^-32 of the largest, and a
+// maximum's own weight in bf16 is 2^-8, as larger ones than 1 would make the sums
+// of values near fp32's end infinite.)
 // ---------------------------------------------------------------------------
 
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves, kManyPiece = 64;
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
   using V8 = typename K::V8;
   using M = ManyTile<D>;
   constexpr int KT = M::KT, CH = M::CH, U = KT / 32, ST = D / 16, DT = D / 32;
-  constexpr float kAbove = T == QG_F16 ? K::kTop - kSlack : 0.0f;  // log2 of the running maximum's own weight
+  constexpr float kAbove = K::kTop - kSlack;  // log2 of the running maximum's own weight
   // a wave copies a quarter of a tile's keys
   constexpr int kKeys = KT / kManyWaves, kCopies = (kKeys * CH + 63) / 64;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][M::kBytes];  // of a tile: K, V

@@ -208,9 +208,10 @@ int64_t qgemv_kv_pool_bytes(int64_t n_seq, int64_t max_pages, int64_t n_pages);
  * longer needed are let go.  Then, sequence after sequence, growing ones take
  * the free pages of the lowest numbers.  A last page that is partly filled and
  * held by others too is copied, in every layer, to a page of the sequence's own
- * before it grows into it; where all who hold it grow, the first of them keeps it.
- * A sequence whose pages, with those of all before it, are not there any more
- * or that would pass max_pages stays at its old length (pool->lens tells).
+ * before it grows into it; where all who hold it are to grow, the first of them
+ * keeps it.  A sequence whose pages, with those of all before it, are not there any
+ * more or that would pass max_pages stays at its old length (pool->lens tells), and
+ * so does one that would keep a page with a longer sequence that stays.
  * The cache's page_size and n_pages must be the pool's (QG_E_SHAPE). */
 int qgemv_kv_resize(const qg_kv_pool *pool, const qg_kv_cache *cache, const int32_t *lens, qg_stream_t stream);
 

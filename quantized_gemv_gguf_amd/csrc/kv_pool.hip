@@ -141,8 +141,10 @@ __global__ void __launch_bounds__(256) cut_kernel(Pool p, const int32_t *lens) {
   }
 }
 
+constexpr int kStays = -2;  // of a sequence's kept page
+
 __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t *lens) {
-  __shared__ int pre[QG_MAX_SEQS], last[QG_MAX_SEQS];
+  __shared__ int pre[QG_MAX_SEQS], last[QG_MAX_SEQS], kept[QG_MAX_SEQS];
   __shared__ int copies;
   const int n = p.n_seq, tid = threadIdx.x;
   int32_t *src = p.work + kHead, *dst = src + n, *list = dst + n;
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
     const int s = tid + i * kThreads;
     copied[i] = false;
     if (s >= n) continue;
+    kept[s] = -1;
     const int len = length_of(p, s), want = lens[s], page = last[s];
     const int64_t wide = pages_of(want, p.shift);
     int need = want > len && wide <= p.max_pages ? (int)wide - pages_of(len, p.shift) : 0;
@@ -178,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
           }
         copied[i] = !(growing == refs && first == s);
         need += copied[i];
+        if (!copied[i]) kept[s] = page;
       }
     }
     pre[s] = need;
@@ -210,11 +214,26 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
     }
     __syncthreads();
   }
+  const auto share_of = [&](int s) { return (s + 1 < n ? pre[s + 1] : total) - pre[s]; };
+  const auto finds_all = [&](int s) { return share_of(s) == 0 || pre[s] + share_of(s) <= free_pages; };
+  // One that keeps a page writes into it from its own length on, where a longer
+  // holder that finds no page for its copy has its positions: it stays.
+  for (int s = tid; s < n && total > free_pages; s += kThreads) {
+    if (kept[s] < 0) continue;
+    const int len = length_of(p, s);
+    for (int o = s + 1; o < n; ++o)
+      if (last[o] == kept[s] && length_of(p, o) > len && !finds_all(o)) {
+        kept[s] = kStays;
+        break;
+      }
+  }
+  __syncthreads();
+  const auto grows = [&](int s) { return kept[s] != kStays && finds_all(s); };
   const int given = min(total, free_pages);
   for (int k = tid; k < given; k += kThreads) {
-    const int s = owner_of(pre, n, k), share = (s + 1 < n ? pre[s + 1] : total) - pre[s];
+    const int s = owner_of(pre, n, k);
     const int page = list[k], r = k - pre[s], copied_page = last[s];
-    if (pre[s] + share > free_pages) {  // (given to one that does not find all of its own)
+    if (!grows(s)) {  // (given to one that does not find all of its own, or stays)
       atomicAnd(&p.used[page >> 5], (int)~(1u << (page & 31)));
       continue;
     }
@@ -231,9 +250,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(Pool p, const int32_t 
   __syncthreads();
   for (int s = tid; s < n; s += kThreads) {
     const int len = length_of(p, s), want = lens[s] < 0 ? len : lens[s];
-    const int share = (s + 1 < n ? pre[s + 1] : total) - pre[s];
-    const bool fits = pages_of(want, p.shift) <= p.max_pages && (share == 0 || pre[s] + share <= free_pages);
-    p.lens[s] = fits ? want : len;
+    p.lens[s] = pages_of(want, p.shift) <= p.max_pages && grows(s) ? want : len;
   }
   if (tid == 0) p.work[0] = copies;
 }

@@ -1026,8 +1026,8 @@ __global__ void __launch_bounds__(64 * kManyWaves, many_waves(D, NT)) attend_man
 // ---------------------------------------------------------------------------
 // The parts of a tile joined, where there are several.  A workgroup takes
 // `rows` of the tile's rows (all 16 of few, or one where there are few tiles and
-// so may be hundreds of parts; 16 of many): groups of its lanes take a row's
-// every so many parts, 4 values a lane.
+// so may be hundreds of parts; all 128 of many, or 16 where there are few tiles):
+// groups of its lanes take a row's every so many parts, 4 values a lane.
 // ---------------------------------------------------------------------------
 
 template <int D, int ROWS, int PIECE>
@@ -1040,6 +1040,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int rows
   const int sub = (int)(group / a.kv_heads), head = (int)(group - (int64_t)sub * a.kv_heads);
   const Item it = Plan<ROWS, PIECE>(a).template find<true>(sub / per);
   if (it.parts < 2) return;
+  // (starts that do not rise give more rows than the workspace is for)
+  if (it.first < 0 || ((int64_t)it.first + it.parts) * a.kv_heads * ROWS > a.part_rows) return;
   const int row0 = it.tile * ROWS + sub % per * rows, real = min(rows, it.n * a.group - row0);
   if (real <= 0) return;
   int each = kGroups;  // groups of a row

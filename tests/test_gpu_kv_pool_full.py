@@ -2,6 +2,8 @@
 written over."""
 from __future__ import annotations
 
+import random
+
 import pytest
 import torch
 
@@ -82,3 +84,50 @@ def test_full_pools(dev, lens, want, pages, got):
         for page in row[:held]:
             refs[page] += 1
     assert p.pool.refs.tolist() == refs and p.pool.used.tolist() == [sum((r > 0) << i for i, r in enumerate(refs))]
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_steps_of_scarce_pages(dev, seed):
+    """Random growth, cuts, forks and compaction of a pool that is often full: every sequence's tokens are its own
+    history's, pages and counts as the tables have them."""
+    r = random.Random(seed)
+    n, size, wide = r.choice([2, 3, 5, 30]), r.choice([1, 4, 16]), r.choice([2, 5])
+    pages = r.choice([2, n, n * wide // 2 + 1])
+    full = lambda shape, v: torch.full(shape, v, dtype=torch.int32, device=dev)  # noqa: E731
+    pool = q.KvPool(full((n, wide), -1), full((n,), 0), full((pages,), 0), full((-(-pages // 32),), 0), size,
+                    torch.empty(q.qgemv_kv_pool_bytes(n, wide, pages), dtype=torch.uint8, device=dev))
+    cache = q.KvCache(*(torch.zeros(1, pages, 1, size, 32, dtype=torch.float16, device=dev) for _ in range(2)))
+    own, token = [[] for _ in range(n)], 0
+    for step in range(20):
+        kind = r.choice(["resize", "resize", "resize", "fork", "compact"])
+        if kind == "fork":
+            parents = [r.choice([s, s, -1, r.randrange(n), r.randrange(n)]) for s in range(n)]
+            q.qgemv_kv_fork(pool, ints(parents, dev))
+            own = [list(own[f]) if f >= 0 else [] for f in parents]
+        elif kind == "compact":
+            q.qgemv_kv_compact(pool, cache)
+        else:
+            want = [r.choice([len(h) + r.randint(1, size + 1), r.randint(0, len(h)), -1]) for h in own]
+            q.qgemv_kv_resize(pool, cache, ints(want, dev))
+            starts, new = [0], []
+            for h, w, m in zip(own, want, pool.lens.tolist()):
+                assert m == len(h) if w < 0 else m == w if w <= len(h) else m in (w, len(h))
+                del h[m:]
+                for _ in range(m - len(h)):
+                    token = (token + 1) % 2048
+                    new.append(token)
+                    h.append(token)
+                starts.append(len(new))
+            if new:
+                x = torch.tensor(new, dtype=torch.float32, device=dev).view(-1, 1, 1).expand(-1, 1, 32).contiguous()
+                q.qgemv_kv_append(x, x, q.KvSeqs(ints(starts, dev), pool.lens, pool.tables), cache, 0)
+        refs = [0] * pages
+        for s, (h, row) in enumerate(zip(own, pool.tables.cpu())):
+            at, held = torch.arange(len(h)), -(-len(h) // size)
+            assert cache.k.cpu()[0, row.long()[at // size], 0, at % size, 3].tolist() == h, (step, kind, s)
+            assert (row[held:] == -1).all()
+            for page in row[:held].tolist():
+                refs[page] += 1
+        assert pool.lens.tolist() == [len(h) for h in own] and pool.refs.tolist() == refs
+        word = [sum((x > 0) << i for i, x in enumerate(refs[w:w + 32])) for w in range(0, pages, 32)]
+        assert [w & 0xffffffff for w in pool.used.tolist()] == word

@@ -187,7 +187,9 @@ int qgemv_kv_append(const qg_heads *k, const qg_heads *v, const qg_kv_seqs *seqs
  * largest at least in QG_F16, 2^-118 in QG_BF16, q's terms to 2^-39 of the row's
  * largest value in QG_F16, in QG_BF16 to 2^-133.
  * out is rounded once.  The order of sums may differ for another number of rows
- * or sequences and other lengths of the others.
+ * or sequences and other lengths of the others.  One of two kernels serves all of
+ * a call, by its rows a sequence on average: single tokens and long chunks can be
+ * faster in calls of their own.
  * scale > 0, up to 2^127; window >= 0; out has q's sizes; q heads a multiple of
  * the cache's heads, n_tok * q heads at most 2^31 - 2^16.  work: device, 16-byte aligned, at least
  * qgemv_kv_attend_bytes, holds nothing between calls; calls that may run at
@@ -197,7 +199,11 @@ int qgemv_kv_attend(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache
                     void *work, int64_t work_bytes, qg_stream_t stream);
 
 /* Bytes of the workspace of a qgemv_kv_attend call with these sizes (pointers
- * are not looked at), or a negative status. */
+ * are not looked at), or a negative status.  A call with fewer tokens, sequences
+ * or heads may need more than a larger one, whose keys are cut into fewer parts
+ * (with tables for 32768 positions, 32 heads over 8 of 128, one sequence of 2048
+ * tokens needs none and of 8 tokens 35 MB): a workspace for several kinds of calls
+ * is as large as the largest of their sizes. */
 int64_t qgemv_kv_attend_bytes(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache);
 
 /* Bytes of a pool's workspace, or a negative status. */

@@ -4,9 +4,10 @@ perf/more_operators.py through the library, and a table of what rocprofv3 saw.
     cd /tmp && export TMPDIR=/tmp
     rocprofv3 --kernel-trace --stats --output-format csv -d t -o r -- python3 -u REPO/profiles/paged_cache_operators.py run 12
     rocprofv3 --pmc SET --output-format csv -d c0 -o r -- python3 -u REPO/profiles/paged_cache_operators.py run 3
-    python3 REPO/profiles/paged_cache_operators.py table t/r_kernel_trace.csv c*/r_counter_collection.csv
+    python3 REPO/profiles/paged_cache_operators.py table 12 3 t/r_kernel_trace.csv c*/r_counter_collection.csv
 
-with the sets SETS below, each in a run of its own.
+with the sets SETS below, each in a run of its own.  Times and bytes are those of a
+pass, summed over a kernel's launches in it (some of which find nothing to do).
 """
 import csv
 import hashlib
@@ -61,7 +62,7 @@ def median(values):
     return sorted(values)[len(values) // 2]
 
 
-def table(trace, counters):
+def table(passes, counted, trace, counters):
     names = [c["name"] for c in cases()[1]]
     times, got = launches(trace), {}
     assert len(times) == len(names), (len(times), len(names))
@@ -71,18 +72,19 @@ def table(trace, counters):
         for name, run_ in zip(names, runs):
             for kernel, r in run_:
                 got.setdefault((name, kernel), {}).setdefault(r["Counter_Name"], []).append(float(r["Counter_Value"]))
-    print("| case | kernel | median us | min us | memory side read MB | written MB | L2 to L1 GB | MFMA | LDS | VALU |")
-    print("|---|---|---|---|---|---|---|---|---|---|")
+    print("| case | kernel | launches | us a pass | median us | longest us | memory side read MB | written MB | L2 to L1 GB | "
+          "MFMA | LDS | VALU |")
+    print("|---|---|---|---|---|---|---|---|---|---|---|---|")
     for name, run_ in zip(names, times):
         for kernel in dict.fromkeys(k for k, _ in run_):
             us = [(int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3 for k, r in run_ if k == kernel]
-            c = {k: median(v) for k, v in got[name, kernel].items()}
+            c = {k: sum(v) / counted for k, v in got[name, kernel].items()}
             cycles = c["GRBM_GUI_ACTIVE"] / 8  # of one XCD
             share = [c["SQ_VALU_MFMA_BUSY_CYCLES"] / (4 * 256 * cycles), c["SQ_LDS_IDX_ACTIVE"] / (256 * cycles),
                      c["SQ_ACTIVE_INST_VALU"] / (256 * cycles)]
-            print(f"| {name} | `{kernel}` | {median(us):.1f} | {min(us):.1f} | {c['FETCH_SIZE'] * 2048 / 1e6:.1f} | "
-                  f"{c['WRITE_SIZE'] * 1024 / 1e6:.1f} | {c['TCP_TCC_READ_REQ_sum'] * 128 / 1e9:.2f} | "
-                  + " | ".join(f"{100 * s:.0f}%" for s in share) + " |")
+            print(f"| {name} | `{kernel}` | {len(us) // passes} | {sum(us) / passes:.1f} | {median(us):.1f} | {max(us):.1f} | "
+                  f"{c['FETCH_SIZE'] * 2048 / 1e6:.1f} | {c['WRITE_SIZE'] * 1024 / 1e6:.1f} | "
+                  f"{c['TCP_TCC_READ_REQ_sum'] * 128 / 1e9:.2f} | " + " | ".join(f"{100 * s:.0f}%" for s in share) + " |")
     from quantized_gemv_gguf_amd import build
     h = hashlib.sha256()
     for path in build.kv_source_paths():
@@ -94,4 +96,4 @@ if __name__ == "__main__":
     if sys.argv[1] == "run":
         run(int(sys.argv[2]))
     else:
-        table(sys.argv[2], sys.argv[3:])
+        table(int(sys.argv[2]), int(sys.argv[3]), sys.argv[4], sys.argv[5:])

@@ -986,7 +986,8 @@ def _ints(t, n: int, dev: int, name: str) -> int:
 
 
 def _c32(n) -> int:
-    """A number for a C int: past 32 bits, where it would be cut, the largest, which is refused."""
+    """A number for a C int: past 32 bits, where it would be cut, the largest, which is refused (as a window it is the
+    widest)."""
     return max(min(int(n), 0x7fffffff), -0x80000000)
 
 
@@ -1078,7 +1079,7 @@ def qgemv_kv_append(k, v, seqs: KvSeqs, cache: KvCache, layer: int, rope: Rope =
 
 
 def qgemv_kv_attend_bytes(q, seqs: KvSeqs, cache: KvCache) -> int:
-    """Bytes of ``work`` for a qgemv_kv_attend of these sizes."""
+    """Bytes of ``work`` for a qgemv_kv_attend of these sizes (a smaller call may need more)."""
     dev = _current()
     n = lib().qgemv_kv_attend_bytes(_heads(q, dev, "q"), _seqs(seqs, dev), _cache(cache, dev))
     if n < 0:

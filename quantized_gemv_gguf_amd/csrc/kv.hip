@@ -154,7 +154,7 @@ template <int X, int V> __global__ void __launch_bounds__(256) rope_kernel(RopeA
 // New tokens into the cache.  As above, over the heads of q (turned into
 // q_out), k (turned into its slot) and v (copied to its slot); a workgroup
 // first finds its tokens' sequences and slots.  (7 ragged prompts up to 2048
-// tokens, 64 heads over 8 of 128, bf16: 65 us, 5.6 TB/s.)
+// tokens, 7948 in all, 64 heads over 8 of 128, bf16: 64 us, 5.1 TB/s.)
 // ---------------------------------------------------------------------------
 
 struct AppendArgs {

@@ -17,9 +17,13 @@ int64_t few_at_once(int dim) {
 AttendShape shape_of(const qg_heads *q, const qg_kv_seqs *seqs, const qg_kv_cache *cache) {
   AttendShape s = {};
   const int64_t group = q->n_head / cache->n_head, n_seq = seqs->n_seq;
-  // (of 16 rows a sequence on average, few and many take about the same: 8
-  // sequences of 4000, 4 tokens each, 32 heads over 8 of 128, 40 and 36 us; of 64
-  // 56 and 29, of 4 65 and 84)
+  // (About 16 rows a sequence, on average, the two take about the same: few and
+  // many, of 16 rows, 42 and 37 us for 8 sequences of 4000, 32 heads over 8 of 128,
+  // bf16; 142 and 150 for 64 heads of 96, fp16; 18 and 29 for one sequence of 8000;
+  // of 20 rows 50 and 37, of 17 166 and 150, of 20 19 and 29; of 64 65 and 42.
+  // A chunk beside single tokens takes one kernel with them: 63 tokens over up to
+  // 2049 positions and 512 over 4096, 64 heads of 96, 595 us, in two calls 411; of
+  // 64 heads over 8 of 64 and up to 8192 153 and 174.)
   s.rows = q->n_tok * group > kFewRows * n_seq ? kManyRows : kFewRows;
   const bool few = s.rows == kFewRows;
   // every sequence may end in a partial tile, of one row at least

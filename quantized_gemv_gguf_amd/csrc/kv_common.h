@@ -83,7 +83,7 @@ __device__ __forceinline__ int room_of(const Seqs &q) { return (int)(q.max_pages
 
 constexpr int64_t kMaxCount = 0x7fff0000;  // tokens, pages, positions: an index a little past the end stays an int
 
-// A grid of at most 2^31 - 1 threads in x.
+// Workgroups of one launch in x: at most 2^31 threads.
 constexpr int64_t kMaxGrid = 1 << 23;
 
 // kv.hip: statuses of the arguments.

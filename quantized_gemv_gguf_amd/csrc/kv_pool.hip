@@ -369,9 +369,10 @@ __global__ void __launch_bounds__(256) moved_counts_kernel(Pool p) {
 }
 
 // ---------------------------------------------------------------------------
-// Copies of pages, all layers, keys and values.  Bound by memory: 4500 pages of 8
-// layers, 1.2 GB, 433 us, 5.4 TB/s read and written.  A job is up to 16 KB of one page's part in one layer; a part that is smaller is taken by
-// as many lanes as it has 16-byte pieces.
+// Copies of pages, all layers, keys and values.  Bound by memory: 1.1 GB of pages
+// of 8 layers 447 us, 5.0 TB/s read and written.  A job is up to 16 KB of one
+// page's part in one layer; a part that is smaller is taken by as many lanes as it
+// has 16-byte pieces.
 // ---------------------------------------------------------------------------
 
 constexpr int kPiece = 1024;  // 16-byte pieces of a job
